@@ -122,7 +122,11 @@ typedef struct {
      * MFMA with per-block scales, for every batch size (path must be 0 or 1). The
      * fused FFN quantizes x before gate/up and h (rounded to bf16) before down.
      * Kernel order for timing: row ids, quantize, grouped GEMM[, quantize h, down
-     * grouped GEMM], reduce / fix-up. 0 (default): bf16 activations. */
+     * grouped GEMM], reduce / fix-up. 0 (default): bf16 activations.
+     * 2: MXFP4 activations (MXFP4 experts only): activation rows are quantized to MXFP4
+     * (moe_quantize_mxfp4's format) and multiplied with the experts' codes by the block
+     * scaled FP4 MFMA, fp32 accumulation. The fused FFN quantizes x before gate/up and the
+     * float32 h before down. Kernel order for timing: as for 1. */
     int32_t act_quant;
     int32_t reserved[5];
     void *const *timing_events;
@@ -271,6 +275,96 @@ moe_status moe_quantize_act(const void *x, moe_dtype x_type, int64_t rows, int64
 moe_status moe_router_topk(const float *logits, int64_t n_tokens, int32_t n_experts, int32_t n_used,
                            int32_t *ids, float *route_w, void *stream);
 
+/*
+ * moe_quantize_mxfp4 -- rows to MXFP4 (the weight format above, from the OCP Microscaling
+ * v1.0 specification): the activation format of act_quant = 2, and the way to make MXFP4
+ * experts from bf16 or float32 ones (rows = n_mat * rows of the matrices). Each row is cut
+ * into blocks of 32 columns. With m = max|x| of a block, its scale byte is
+ * max(floor(log2 m) - 2 + 127, 0) (0 for a block of zeros), and each element gets the E2M1
+ * code nearest to x / 2^(byte - 127), ties to the even code, magnitudes over 6 taken as 6;
+ * a value that rounds to zero keeps its sign. A block with an infinity or a NaN gets scale
+ * byte 255 (every value NaN) and codes 0.
+ *   x       device BF16 or F32 [rows][K], K % 32 == 0 (MOE_ELIMIT otherwise), 16-byte aligned
+ *   codes   device uint8 [rows][K/2] (written, 16-byte aligned), column 2i in bits 0-3
+ *   scales  device uint8 [rows][K/32] (written)
+ *   values  NULL, or device [rows][K] of x's type (written, 16-byte aligned; may be x
+ *           itself): the values the codes stand for, exactly representable in both types --
+ *           what quantization-aware training puts in place of x
+ * rows = 0 is a no-op. rows * K / 32 < 2^31 (MOE_ELIMIT). No workspace. Deterministic.
+ */
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_type, int64_t rows, int64_t K,
+                              uint8_t* codes, uint8_t* scales, void* values, void* stream);
+
+/*
+ * moe_router_scored -- routing by scores over all experts, the form of routers trained with
+ * a balance bias and expert groups; moe_router_topk is the softmax over the picks alone.
+ * For each token, with l its logits:
+ *   score   s_e = exp(l_e) / sum_f exp(l_f) (MOE_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e))
+ *           (MOE_SCORE_SIGMOID)
+ *   choice  c_e = s_e + bias[e] (bias NULL: the order of the logits); the bias steers the
+ *           choice and enters neither scores nor weights
+ *   groups  the experts form n_group groups of n_experts / n_group neighbours. A group's
+ *           score is its largest choice (group_top = 1) or the sum of its two largest ones
+ *           (group_top = 2; a single one counts alone); the topk_group best groups are
+ *           kept, equal scores lower group first
+ *   picks   the n_used largest choices in the kept groups, descending, equal choices lower
+ *           expert first
+ *   weight  scale * s_i, or with renorm scale * s_i / sum of the picks' s
+ * Choices are compared as 64-bit values, so the picks do not depend on float32 rounding.
+ * Masks: an expert whose logit is -inf or NaN, or whose bias is -inf or NaN, is never
+ * picked; a logit of -inf or NaN also has score 0 and stays out of the softmax's sum.
+ * Picks that find no expert (a token with every logit -inf, say padding) get id -1 and
+ * weight 0, which the calls above skip. Logits of +inf take the limit: sigmoid 1, softmax
+ * shared equally among them.
+ *   logits   device F32 or BF16 [n_tokens][n_experts]
+ *   bias     NULL or device float32 [n_experts]
+ *   ids      device int32 [n_tokens][n_used] (written)
+ *   route_w  device float32 [n_tokens][n_used] (written)
+ *   scores   NULL or device float32 [n_tokens][n_experts] (written): s, for balance losses
+ * Requires 1 <= n_used <= topk_group * n_experts / n_group, n_experts <= 1024,
+ * n_experts % n_group == 0, 1 <= topk_group <= n_group (MOE_EINVAL / MOE_ELIMIT
+ * otherwise), a finite scale, n_tokens < 2^22. No workspace. Deterministic.
+ * n_tokens = 0 is a no-op.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+    int32_t score;      /* moe_score                                              */
+    int32_t n_group;    /* 1: no groups                                           */
+    int32_t topk_group; /* groups kept                                            */
+    int32_t group_top;  /* choices summed to a group's score: 1 or 2              */
+    int32_t renorm;     /* 1: weights divided by the sum of the picks' scores     */
+    float scale;        /* factor on the weights                                  */
+    int32_t reserved[2];
+} moe_router_config;
+moe_status moe_router_scored(const void* logits, moe_dtype logits_type, const float* bias,
+                             int64_t n_tokens, int32_t n_experts, int32_t n_used,
+                             const moe_router_config* cfg, int32_t* ids, float* route_w,
+                             float* scores, void* stream);
+
+/*
+ * moe_router_scored_backward -- the gradient of the logits through moe_router_scored's
+ * weights and scores (the choice itself and the bias have none):
+ *   d_logits[t][f] = sum_s d_route_w[t][s] * d route_w[t][s] / d l_f
+ *                  + sum_e d_scores[t][e] * d s_e / d l_f
+ *   logits     as in the forward call
+ *   ids        device int32 [n_tokens][n_used], the forward call's; entries outside
+ *              [0, n_experts) or naming a masked logit contribute nothing, an expert named
+ *              more than once gets the sum of its entries' gradients
+ *   d_route_w  device float32 [n_tokens][n_used]
+ *   d_scores   NULL, or device float32: row t at d_scores + t * d_scores_stride. A stride of
+ *              0 gives every token the same row (a balance loss's gradient), else the
+ *              stride is at least n_experts (MOE_EINVAL)
+ *   d_logits   device [n_tokens][n_experts] of the logits' type (written, computed in
+ *              float32 and rounded once; masked logits get 0). It may be logits itself.
+ * cfg: score, renorm and scale as in the forward call; its group fields are not read.
+ * No workspace. Deterministic. n_tokens = 0 is a no-op.
+ */
+moe_status moe_router_scored_backward(const void* logits, moe_dtype logits_type, const int32_t* ids,
+                                      const float* d_route_w, const float* d_scores,
+                                      int64_t d_scores_stride, int64_t n_tokens, int32_t n_experts,
+                                      int32_t n_used, const moe_router_config* cfg, void* d_logits,
+                                      void* stream);
+
 /* Workspace sizes in bytes for the calls above with the same arguments (0 if the
  * arguments are invalid; a valid call may also need 0 bytes, then ws may be NULL). */
 size_t moe_row_ids_workspace_size(int64_t n_tokens, int32_t n_used, int32_t n_experts);
@@ -295,8 +389,8 @@ int32_t moe_select_path(int64_t n_tokens, int32_t n_used, int32_t n_experts, int
 
 /* The path moe_mul_mat_id / moe_ffn_fused take for experts of weight_type (MOE_Q8_0,
  * MOE_MXFP4, MOE_IQ4_NL or MOE_IQ4_XS) under opt: 1 grouped GEMM, 2 GEMV, 3 the grouped
- * GEMM over quantized activations (opt->act_quant = 1, Q8_0 only), or a negative
- * moe_status (MOE_EINVAL for other weight types, or for options the call would reject).
+ * GEMM over quantized activations (opt->act_quant = 1, Q8_0 only), 4 the grouped GEMM over
+ * MXFP4 activations (opt->act_quant = 2, MXFP4 only), or a negative moe_status (MOE_EINVAL for other weight types, or for options the call would reject).
  * Q8_0 gives the same answer as moe_select_path. Pure host function. */
 int32_t moe_select_path_typed(int64_t n_tokens, int32_t n_used, int32_t n_experts, int64_t act_width,
                               moe_dtype weight_type, const moe_options *opt);

@@ -24,13 +24,15 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 MOE_OK, MOE_EINVAL, MOE_ELIMIT, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
 MOE_F32, MOE_BF16, MOE_Q8_0, MOE_MXFP4, MOE_IQ4_NL, MOE_IQ4_XS = 0, 1, 2, 3, 4, 5
 PATH_AUTO, PATH_GEMM, PATH_GEMV = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}   # moe_score
 
 # Every symbol include/moe.h declares.
 EXPORTS = ("moe_row_ids", "moe_mul_mat_id", "moe_ffn_fused", "moe_router_topk",
            "moe_row_ids_workspace_size", "moe_mul_mat_id_workspace_size",
            "moe_ffn_fused_workspace_size", "moe_select_path", "moe_select_path_typed",
            "moe_status_string", "moe_last_error",
-           "moe_last_stage_count", "moe_ffn_fused_noalloc", "moe_quantize_act", "moe_gather_rows")
+           "moe_last_stage_count", "moe_ffn_fused_noalloc", "moe_quantize_act", "moe_gather_rows",
+           "moe_quantize_mxfp4", "moe_router_scored", "moe_router_scored_backward")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -52,6 +54,12 @@ class c_moe_options(ctypes.Structure):
                 ("n_timing_events", ctypes.c_int32), ("reserved2", ctypes.c_int32)]
 
 
+class c_moe_router_config(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 2)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libmoe.so is not built (%s); run `python indirect_expert_matmul_amd/build.py`"
@@ -67,8 +75,13 @@ def _load():
     lib.moe_ffn_fused_noalloc.argtypes = [W, W, W, W, W, W, P, ctypes.c_int, P, P, I64, I32, P, O, P]
     lib.moe_quantize_act.argtypes = [P, ctypes.c_int, I64, I64, P, P, P]
     lib.moe_gather_rows.argtypes = [P, ctypes.c_int, I64, I64, P, I64, P, P]
+    C = ctypes.POINTER(c_moe_router_config)
+    lib.moe_quantize_mxfp4.argtypes = [P, ctypes.c_int, I64, I64, P, P, P, P]
+    lib.moe_router_scored.argtypes = [P, ctypes.c_int, P, I64, I32, I32, C, P, P, P, P]
+    lib.moe_router_scored_backward.argtypes = [P, ctypes.c_int, P, P, P, I64, I64, I32, I32, C, P, P]
     for f in (lib.moe_row_ids, lib.moe_mul_mat_id, lib.moe_ffn_fused, lib.moe_router_topk,
-              lib.moe_ffn_fused_noalloc, lib.moe_quantize_act, lib.moe_gather_rows):
+              lib.moe_ffn_fused_noalloc, lib.moe_quantize_act, lib.moe_gather_rows,
+              lib.moe_quantize_mxfp4, lib.moe_router_scored, lib.moe_router_scored_backward):
         f.restype = ctypes.c_int
     lib.moe_row_ids_workspace_size.argtypes = [I64, I32, I32]
     lib.moe_mul_mat_id_workspace_size.argtypes = [W, ctypes.c_int, I32, I64, I32, O]
@@ -224,6 +237,15 @@ def _keep_alive(stream, *tensors):
                 t.record_stream(stream)
 
 
+def _check_device(stream, *tensors):
+    """The kernels run on the stream's device (the current one's without a stream): tensors of
+    another device are refused, as a launch there would read the wrong memory."""
+    dev = torch.cuda.current_device() if stream is None else stream.device.index
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("tensors on %s, but the stream runs on cuda:%d" % (t.device, dev))
+
+
 def _check_ids(ids: torch.Tensor, route_w: Optional[torch.Tensor] = None):
     """ids must be int32 [T][k] (torch.topk gives int64, which would be read as wrong
     experts), route_w float32 of the same shape."""
@@ -316,6 +338,117 @@ def moe_quantize_act(x: torch.Tensor, stream=None):
     return q, d
 
 
+def moe_quantize_mxfp4(x: torch.Tensor, return_values: bool = False, stream=None):
+    """(codes uint8 [..., K/2], scales uint8 [..., K/32]) of the rows of x [..., K] (bf16 or its
+    16-bit patterns, or float32) in MXFP4; a 3-D x gives the two tensors of ``Weights``. With
+    ``return_values`` also the values the codes stand for, in x's dtype."""
+    if x.dim() < 2 or x.shape[-1] % 32 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., K] with K % 32 == 0")
+    _dev_check(x)
+    _check_device(stream, x)
+    K = x.shape[-1]
+    rows = x.numel() // K
+    lead = tuple(x.shape[:-1])
+    codes = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+    values = torch.empty_like(x) if return_values else None
+    _keep_alive(stream, codes, scales, values)
+    _check(lib.moe_quantize_mxfp4(x.data_ptr(), _xtype(x), rows, K, codes.data_ptr(), scales.data_ptr(),
+                                  None if values is None else values.data_ptr(), _stream(stream)),
+           "moe_quantize_mxfp4")
+    return (codes, scales, values) if return_values else (codes, scales)
+
+
+def _router_config(score, n_group, topk_group, group_top, renorm, scale) -> c_moe_router_config:
+    if score not in SCORES:
+        raise ValueError("score must be one of %s (got %r)" % (", ".join(sorted(SCORES)), score))
+    return c_moe_router_config(SCORES[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
+
+
+def _check_logits(logits: torch.Tensor, stream) -> int:
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be float32 or bfloat16 [n_tokens][n_experts] (got %s of shape %s)"
+                         % (logits.dtype, tuple(logits.shape)))
+    _dev_check(logits)
+    _check_device(stream, logits)
+    return _xtype(logits)
+
+
+def _check_tensor(t: torch.Tensor, name: str, dtype, shape, device):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s of shape %s on %s (got %s of shape %s on %s)"
+                         % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
+
+
+def moe_router_scored(logits: torch.Tensor, n_used: int, bias: Optional[torch.Tensor] = None,
+                      score: str = "softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 2,
+                      renorm: bool = True, scale: float = 1.0, return_scores: bool = False,
+                      ids: Optional[torch.Tensor] = None, route_w: Optional[torch.Tensor] = None,
+                      scores: Optional[torch.Tensor] = None, stream=None):
+    """(ids int32 [T][k], route_w float32 [T][k]) from router logits (float32 or bfloat16 [T][E]):
+    softmax or sigmoid scores over all experts, a float32 ``bias`` [E] that steers the choice alone,
+    the ``topk_group`` best of ``n_group`` expert groups, the k best choices in them, weighted by
+    ``scale`` times their scores, renormalised over the picks if ``renorm``. With ``return_scores``
+    also the scores, float32 [T][E]. Experts with a logit of -inf or NaN are never picked; a pick
+    that finds no expert has id -1 and weight 0."""
+    st = _check_logits(logits, stream)
+    T, E = logits.shape
+    dev = logits.device
+    cfg = _router_config(score, n_group, topk_group, group_top, renorm, scale)
+    if bias is not None:
+        _check_tensor(bias, "bias", torch.float32, (E,), dev)
+    made = []
+    if ids is None:
+        ids = torch.empty((T, n_used), dtype=torch.int32, device=dev)
+        made.append(ids)
+    if route_w is None:
+        route_w = torch.empty((T, n_used), dtype=torch.float32, device=dev)
+        made.append(route_w)
+    if scores is None and return_scores:
+        scores = torch.empty((T, E), dtype=torch.float32, device=dev)
+        made.append(scores)
+    if made:
+        _keep_alive(stream, *made)
+    _check_tensor(ids, "ids", torch.int32, (T, n_used), dev)
+    _check_tensor(route_w, "route_w", torch.float32, (T, n_used), dev)
+    if scores is not None:
+        _check_tensor(scores, "scores", torch.float32, (T, E), dev)
+    _check(lib.moe_router_scored(logits.data_ptr(), st, None if bias is None else bias.data_ptr(), T, E,
+                                 n_used, ctypes.byref(cfg), ids.data_ptr(), route_w.data_ptr(),
+                                 None if scores is None else scores.data_ptr(), _stream(stream)),
+           "moe_router_scored")
+    return (ids, route_w, scores) if scores is not None else (ids, route_w)
+
+
+def moe_router_scored_backward(logits: torch.Tensor, ids: torch.Tensor, d_route_w: torch.Tensor,
+                               d_scores: Optional[torch.Tensor] = None, score: str = "softmax",
+                               renorm: bool = True, scale: float = 1.0,
+                               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of the logits (their dtype and shape) from those of moe_router_scored's
+    route_w (float32 [T][k]) and, optionally, scores: ``d_scores`` float32 [T][E] or, the same
+    for every token, [E]. ``ids``, ``score``, ``renorm`` and ``scale`` are the forward call's."""
+    st = _check_logits(logits, stream)
+    T, E = logits.shape
+    dev = logits.device
+    cfg = _router_config(score, 1, 1, 1, renorm, scale)
+    _check_ids(ids)
+    _check_tensor(ids, "ids", torch.int32, (T, ids.shape[1]), dev)
+    _check_tensor(d_route_w, "d_route_w", torch.float32, ids.shape, dev)
+    stride = 0
+    if d_scores is not None:
+        _check_tensor(d_scores, "d_scores", torch.float32, (T, E) if d_scores.dim() == 2 else (E,), dev)
+        stride = E if d_scores.dim() == 2 else 0
+    if out is None:
+        out = torch.empty_like(logits)
+        _keep_alive(stream, out)
+    _check_tensor(out, "out", logits.dtype, (T, E), dev)
+    _check(lib.moe_router_scored_backward(logits.data_ptr(), st, ids.data_ptr(), d_route_w.data_ptr(),
+                                          None if d_scores is None else d_scores.data_ptr(), stride, T, E,
+                                          ids.shape[1], ctypes.byref(cfg), out.data_ptr(), _stream(stream)),
+           "moe_router_scored_backward")
+    return out
+
+
 def moe_router_topk(logits: torch.Tensor, n_used: int, ids: Optional[torch.Tensor] = None,
                     route_w: Optional[torch.Tensor] = None, stream=None):
     """(ids int32 [T][k], route_w float32 [T][k]) from router logits float32 [T][E]:
@@ -356,7 +489,8 @@ def moe_mul_mat_id(w: Weights, src1: torch.Tensor, ids: torch.Tensor,
                    workspace: Optional[torch.Tensor] = None, stream=None, events=None,
                    act_quant: int = 0):
     """GGML_OP_MUL_MAT_ID: float32 [T][k][N] per slot, or [T][N] weighted by route_w.
-    ``act_quant=1``: the quantized-activation (int8 MFMA) grouped GEMM, Q8_0 experts."""
+    ``act_quant=1``: the quantized-activation (int8 MFMA) grouped GEMM, Q8_0 experts;
+    ``act_quant=2``: MXFP4 activations (FP4 MFMA), MXFP4 experts."""
     _check_ids(ids, route_w)
     T, k = ids.shape
     cw = w.c()
@@ -399,7 +533,8 @@ def moe_ffn_fused(gate: Weights, up: Weights, down: Weights, x: torch.Tensor, id
                   workspace: Optional[torch.Tensor] = None, stream=None, events=None,
                   act_quant: int = 0):
     """Fused MoE FFN: float32 [T][n_embd]. ``act_quant=1``: the quantized-activation
-    (int8 MFMA) grouped GEMMs, Q8_0 experts."""
+    (int8 MFMA) grouped GEMMs, Q8_0 experts; ``act_quant=2``: MXFP4 activations (FP4 MFMA),
+    MXFP4 experts."""
     _check_ids(ids, route_w)
     T, k = ids.shape
     cg, cu, cd = gate.c(), up.c(), down.c()

@@ -161,11 +161,19 @@ int select_path_fmt(int64_t T, int32_t k, int32_t E, int64_t act_width, bool fp4
 }
 
 // With options.act_quant = 1: 3 (the quantized-activation grouped GEMM, Q8_0 experts
-// only, whatever the batch size), else the choice above; or a negative status.
+// only, whatever the batch size), with 2: 4 (the MXFP4-activation grouped GEMM, MXFP4
+// experts only), else the choice above; or a negative status.
 int select_path_aq(int64_t T, int32_t k, int32_t E, int64_t act_width, int32_t wtype,
                    const moe_options* o) {
     const int32_t aq = o ? o->act_quant : 0;
-    if (aq != 0 && aq != 1) return fail(MOE_EINVAL, "options.act_quant must be 0 or 1 (got %d)", aq);
+    if (aq < 0 || aq > 2) return fail(MOE_EINVAL, "options.act_quant must be 0, 1 or 2 (got %d)", aq);
+    if (aq == 2) {
+        if (wtype != MOE_MXFP4) return fail(MOE_EINVAL, "MXFP4 activations (act_quant = 2) need MXFP4 experts");
+        if (o->path != 0 && o->path != 1)
+            return fail(MOE_EINVAL, "MXFP4 activations run on the grouped GEMM only: options.path must "
+                        "be 0 or 1 (got %d)", o->path);
+        return 4;
+    }
     if (!aq)
         return select_path_fmt(T, k, E, act_width,
                                wtype == MOE_MXFP4 || wtype == MOE_IQ4_NL || wtype == MOE_IQ4_XS, o,
@@ -219,6 +227,7 @@ struct FfnPlan {
     // quantized-activation path: codes and block scales of x, h and the shared h
     int8_t *xq, *hq, *hshq;
     float *xd, *hd, *hshd;
+    uint8_t *xs, *hs, *hshs;   // MXFP4 activations: E8M0 scale bytes (codes in xq, hq, hshq)
 };
 
 FfnPlan carve_ffn(Carve& c, const FfnDims& d, int path) {
@@ -235,6 +244,16 @@ FfnPlan carve_ffn(Carve& c, const FfnDims& d, int path) {
         p.hd = (float*)c.take((size_t)n * (d.n_ff / 32) * 4);
         p.hshq = (int8_t*)c.take((size_t)d.S * d.T * d.n_ff_sh);
         p.hshd = (float*)c.take((size_t)d.S * d.T * (d.n_ff_sh / 32) * 4);
+    } else if (path == 4) {
+        p.r = carve_row_ids(c, n, d.E, true, kFp4TileM);
+        p.xq = (int8_t*)c.take((size_t)d.T * d.n_embd / 2);
+        p.xs = (uint8_t*)c.take((size_t)d.T * (d.n_embd / 32));
+        p.h = c.take((size_t)n * d.n_ff * 4);
+        p.hsh = c.take((size_t)d.S * d.T * d.n_ff_sh * 4);
+        p.hq = (int8_t*)c.take((size_t)n * d.n_ff / 2);
+        p.hs = (uint8_t*)c.take((size_t)n * (d.n_ff / 32));
+        p.hshq = (int8_t*)c.take((size_t)d.S * d.T * d.n_ff_sh / 2);
+        p.hshs = (uint8_t*)c.take((size_t)d.S * d.T * (d.n_ff_sh / 32));
     } else if (path == 1) {
         p.msub = gemm_pick_msub((double)n / d.E);
         p.r = carve_row_ids(c, n, d.E, true, gemm_tile_m(p.msub));
@@ -256,6 +275,7 @@ struct MmidPlan {
     void* y;
     int8_t* aq;   // quantized-activation path: src1 codes [T*B][K] and block scales
     float* ad;
+    uint8_t* as;  // MXFP4 activations: E8M0 scale bytes (codes [T*B][K/2] in aq)
 };
 
 MmidPlan carve_mmid(Carve& c, int64_t T, int32_t k, int32_t E, int64_t N, bool weighted, bool q8, int path,
@@ -267,6 +287,10 @@ MmidPlan carve_mmid(Carve& c, int64_t T, int32_t k, int32_t E, int64_t N, bool w
         p.r = carve_row_ids(c, n, E, true, kQ8aTileM);
         p.aq = (int8_t*)c.take((size_t)(T * B) * K);
         p.ad = (float*)c.take((size_t)(T * B) * (K / 32) * 4);
+    } else if (path == 4) {
+        p.r = carve_row_ids(c, n, E, true, kFp4TileM);
+        p.aq = (int8_t*)c.take((size_t)(T * B) * K / 2);
+        p.as = (uint8_t*)c.take((size_t)(T * B) * (K / 32));
     } else if (!q8 || path == 1) {
         p.msub = gemm_pick_msub((double)n / E);
         p.r = carve_row_ids(c, n, E, true, q8 ? gemm_tile_m(p.msub) : 0);
@@ -385,6 +409,181 @@ QuantPart qpart(const void* src, int64_t rows, int64_t K, int8_t* q, float* d) {
     p.q = q;
     p.d = d;
     return p;
+}
+
+// ---------------------------------------------------------------- MXFP4 activations
+constexpr int64_t kFp4MaxBlocks = 1LL << 31;   // 32-column blocks one quantization takes
+
+QuantFp4Part fp4_part(const void* src, int64_t rows, int64_t K, int8_t* q, uint8_t* s) {
+    QuantFp4Part p{};
+    p.src = src;
+    p.rows = rows;
+    p.K = K;
+    p.q = (uint8_t*)q;
+    p.s = s;
+    return p;
+}
+
+// One side of an MXFP4-activation GEMM launch: the routed experts' segments ...
+GemmProblem fp4_routed(const moe_weights* w1, const moe_weights* w2, const RowIdsPlan& r, int64_t n,
+                       const int8_t* aq, const uint8_t* as, void* out) {
+    GemmProblem p{};
+    p.qs1 = (const int8_t*)w1->data;
+    p.d1 = (const uint16_t*)w1->scales;
+    if (w2) {
+        p.qs2 = (const int8_t*)w2->data;
+        p.d2 = (const uint16_t*)w2->scales;
+    }
+    p.N = (int32_t)w1->rows;
+    p.K = (int32_t)w1->cols;
+    p.bounds = r.bounds;
+    p.tile_off = r.tile_a;
+    p.tile_tab = r.tile_tab;
+    p.n_seg = (int32_t)w1->n_mat;
+    p.m_tiles_max = (int32_t)m_tiles_bound(n, w1->n_mat, kFp4TileM);
+    p.Aq = aq;
+    p.As = as;
+    p.out = out;
+    p.ldo = w1->rows;
+    return p;
+}
+// ... and the shared experts', each over all T tokens.
+GemmProblem fp4_shared(const moe_weights* w1, const moe_weights* w2, int64_t T, const int8_t* aq,
+                       const uint8_t* as, void* out) {
+    GemmProblem p = fp4_routed(w1, w2, RowIdsPlan{}, 0, aq, as, out);
+    p.seg_len = (int32_t)T;
+    p.m_tiles_max = (int32_t)(w1->n_mat * ((T + kFp4TileM - 1) / kFp4TileM));
+    return p;
+}
+
+moe_status check_fp4_act(const void* x, const char* name) {
+    if ((uintptr_t)x % 16) return fail(MOE_EINVAL, "MXFP4 activations: %s must be 16-byte aligned", name);
+    return MOE_OK;
+}
+moe_status check_fp4_weights(const moe_weights* w, const char* name) {
+    if (w && w->n_mat && (uintptr_t)w->data % 16)
+        return fail(MOE_EINVAL, "MXFP4 activations: the codes of %s must be 16-byte aligned", name);
+    return MOE_OK;
+}
+moe_status check_fp4_limits(const GemmArgs& g, int64_t act_blocks, const char* what) {
+    if (act_blocks >= kFp4MaxBlocks)
+        return fail(MOE_ELIMIT, "%s: too many activation blocks (rows * K / 32 must be under 2^31)", what);
+    if (gemm_fp4_max_threads(g) >= k4GiB)
+        return fail(MOE_ELIMIT, "%s: the grouped GEMM grid exceeds 2^32 work-items", what);
+    return MOE_OK;
+}
+void fp4_tiles(RowIdsArgs& ra, const RowIdsPlan& r) {
+    ra.tile_off[0] = r.tile_a;
+    ra.tile_m[0] = kFp4TileM;
+    ra.tile_tab[0] = r.tile_tab;
+    ra.tile_cap[0] = r.tile_cap;
+}
+
+// The fused FFN up to the per-slot rows (p.y, p.ysh): row ids, x -> codes, gate/up, the
+// float32 h -> codes, down.
+moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, const moe_weights* up,
+                   const moe_weights* down, const moe_weights* sg, const moe_weights* su,
+                   const moe_weights* sd, const void* x, const int32_t* ids, Timer& tm, hipStream_t st) {
+    moe_status s;
+    const int64_t n = d.T * d.k;
+    const bool shared = d.S > 0;
+    if ((s = check_fp4_act(x, "x")) || (s = check_fp4_weights(gate, "gate")) ||
+        (s = check_fp4_weights(up, "up")) || (s = check_fp4_weights(down, "down")))
+        return s;
+    if (shared && ((s = check_fp4_weights(sg, "sh_gate")) || (s = check_fp4_weights(su, "sh_up")) ||
+                   (s = check_fp4_weights(sd, "sh_down"))))
+        return s;
+    RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
+    fp4_tiles(ra, p.r);
+    QuantFp4Args qx{}, qh{};
+    qx.src_bf16 = 1;
+    qx.n_part = 1;
+    qx.part[0] = fp4_part(x, d.T, d.n_embd, p.xq, p.xs);
+    qh.n_part = shared ? 2 : 1;
+    qh.part[0] = fp4_part(p.h, n, d.n_ff, p.hq, p.hs);
+    GemmArgs g{}, g2{};
+    g.mode = 1;
+    g.n_prob = g2.n_prob = shared ? 2 : 1;
+    g.p[0] = fp4_routed(gate, up, p.r, n, p.xq, p.xs, p.h);
+    g.p[0].a_rows = p.r.ids_src1;
+    g2.p[0] = fp4_routed(down, nullptr, p.r, n, p.hq, p.hs, p.y);
+    g2.p[0].out_rows = p.r.ids_dst;
+    if (shared) {
+        qh.part[1] = fp4_part(p.hsh, (int64_t)d.S * d.T, d.n_ff_sh, p.hshq, p.hshs);
+        g.p[1] = fp4_shared(sg, su, d.T, p.xq, p.xs, p.hsh);
+        g.p[1].a_row_mod = (int32_t)d.T;
+        g2.p[1] = fp4_shared(sd, nullptr, d.T, p.hshq, p.hshs, p.ysh);
+    }
+    if ((s = check_fp4_limits(g, d.T * (d.n_embd / 32), "gate/up"))) return s;
+    if ((s = check_fp4_limits(g2, n * (d.n_ff / 32) + (int64_t)d.S * d.T * (d.n_ff_sh / 32), "down"))) return s;
+    tm.begin();
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_quant_mxfp4(qx, st), "quantize x"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_gemm_fp4(g, st), "gate/up grouped GEMM (MXFP4)"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_quant_mxfp4(qh, st), "quantize h"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_gemm_fp4(g2, st), "down grouped GEMM (MXFP4)"))) return s;
+    tm.end();
+    return MOE_OK;
+}
+
+// moe_mul_mat_id up to the per-slot rows: row ids, src1 -> codes, grouped GEMM.
+moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, int32_t B,
+                    const int32_t* ids, int64_t T, int32_t k, float* slot_out, Timer& tm, hipStream_t st) {
+    moe_status s;
+    const int64_t n = T * k;
+    if ((s = check_fp4_act(src1, "src1")) || (s = check_fp4_weights(w, "w"))) return s;
+    RowIdsArgs ra = row_ids_args(ids, n, k, (int32_t)w->n_mat, B, p.r);
+    fp4_tiles(ra, p.r);
+    QuantFp4Args qa{};
+    qa.src_bf16 = 1;
+    qa.n_part = 1;
+    qa.part[0] = fp4_part(src1, T * B, w->cols, p.aq, p.as);
+    GemmArgs g{};
+    g.n_prob = 1;
+    g.p[0] = fp4_routed(w, nullptr, p.r, n, p.aq, p.as, slot_out);
+    g.p[0].a_rows = p.r.ids_src1;
+    g.p[0].out_rows = p.r.ids_dst;
+    if ((s = check_fp4_limits(g, T * B * (w->cols / 32), "mul_mat_id"))) return s;
+    tm.begin();
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_quant_mxfp4(qa, st), "quantize src1"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_gemm_fp4(g, st), "grouped GEMM (MXFP4)"))) return s;
+    tm.end();
+    return MOE_OK;
+}
+
+moe_status check_router(const moe_router_config* c, int64_t T, int32_t E, int32_t k, bool choose) {
+    moe_status s;
+    if ((s = check_tokens(T, k))) return s;
+    if ((s = check_experts(E))) return s;
+    if (!c) return fail(MOE_EINVAL, "router config is NULL");
+    if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID)
+        return fail(MOE_EINVAL, "router config: score must be 0 (softmax) or 1 (sigmoid) (got %d)", c->score);
+    if (c->renorm != 0 && c->renorm != 1)
+        return fail(MOE_EINVAL, "router config: renorm must be 0 or 1 (got %d)", c->renorm);
+    if (!(c->scale - c->scale == 0.f)) return fail(MOE_EINVAL, "router config: scale must be finite");
+    if (!choose) return MOE_OK;
+    if (c->n_group < 1 || E % c->n_group)
+        return fail(MOE_EINVAL, "router config: n_group (%d) must divide n_experts (%d)", c->n_group, E);
+    if (c->topk_group < 1 || c->topk_group > c->n_group)
+        return fail(MOE_EINVAL, "router config: topk_group must be 1 to n_group (got %d)", c->topk_group);
+    if (c->group_top != 1 && c->group_top != 2)
+        return fail(MOE_EINVAL, "router config: group_top must be 1 or 2 (got %d)", c->group_top);
+    if ((int64_t)k * c->n_group > (int64_t)c->topk_group * E)
+        return fail(MOE_EINVAL, "n_used (%d) exceeds the experts of %d kept groups", k, c->topk_group);
+    return MOE_OK;
 }
 
 }  // namespace
@@ -632,6 +831,8 @@ moe_status moe_ffn_fused(const moe_weights* gate, const moe_weights* up, const m
         tm.begin();
         if ((s = hip_check(launch_gemm_q8a(g2, st), "down grouped GEMM (int8)"))) return s;
         tm.end();
+    } else if (path == 4) {
+        if ((s = ffn_fp4(d, p, gate, up, down, sh_gate, sh_up, sh_down, x, ids, tm, st))) return s;
     } else if (path == 1) {
         const int bm = gemm_tile_m(p.msub);
         RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
@@ -916,6 +1117,8 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
         tm.begin();
         if ((s = hip_check(launch_gemm_q8a(g, st), "grouped GEMM (int8)"))) return s;
         tm.end();
+    } else if (path == 4) {
+        if ((s = mmid_fp4(p, w, src1, B, ids, n_tokens, k, slot_out, tm, st))) return s;
     } else if (!q8 || path == 1) {
         const int bm = gemm_tile_m(p.msub);
         RowIdsArgs ra = row_ids_args(ids, n, k, E, B, p.r);
@@ -1034,6 +1237,84 @@ moe_status moe_quantize_act(const void* x, moe_dtype x_type, int64_t rows, int64
     a.src_bf16 = x_type == MOE_BF16;
     a.part[0] = qpart(x, rows, K, q, d);
     return hip_check(launch_quant_act(a, (hipStream_t)stream), "quantize activations");
+}
+
+moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_type, int64_t rows, int64_t K,
+                              uint8_t* codes, uint8_t* scales, void* values, void* stream) {
+    g_err.clear();
+    if (x_type != MOE_BF16 && x_type != MOE_F32) return fail(MOE_EINVAL, "x must be BF16 or F32");
+    if (rows < 0 || K <= 0) return fail(MOE_EINVAL, "rows must be >= 0 and K > 0");
+    if (K % 32) return fail(MOE_ELIMIT, "K must be a multiple of 32 (got %lld)", (long long)K);
+    if (rows == 0) return MOE_OK;
+    if (!x || !codes || !scales) return fail(MOE_EINVAL, "NULL pointer argument");
+    if (((uintptr_t)x | (uintptr_t)codes | (uintptr_t)values) % 16)
+        return fail(MOE_EINVAL, "x, codes and values must be 16-byte aligned");
+    if (rows >= kFp4MaxBlocks || K / 32 >= kFp4MaxBlocks || rows * (K / 32) >= kFp4MaxBlocks)
+        return fail(MOE_ELIMIT, "rows * K / 32 must be under 2^31");
+    QuantFp4Args a{};
+    a.n_part = 1;
+    a.src_bf16 = x_type == MOE_BF16;
+    a.part[0] = fp4_part(x, rows, K, (int8_t*)codes, scales);
+    a.part[0].values = values;
+    return hip_check(launch_quant_mxfp4(a, (hipStream_t)stream), "quantize to MXFP4");
+}
+
+moe_status moe_router_scored(const void* logits, moe_dtype logits_type, const float* bias,
+                             int64_t n_tokens, int32_t n_experts, int32_t n_used,
+                             const moe_router_config* cfg, int32_t* ids, float* route_w,
+                             float* scores, void* stream) {
+    moe_status s;
+    g_err.clear();
+    if (logits_type != MOE_F32 && logits_type != MOE_BF16) return fail(MOE_EINVAL, "logits must be F32 or BF16");
+    if ((s = check_router(cfg, n_tokens, n_experts, n_used, true))) return s;
+    if (n_tokens > 0 && (!logits || !ids || !route_w)) return fail(MOE_EINVAL, "NULL pointer argument");
+    RouterScoredArgs a{};
+    a.logits = logits;
+    a.bf16 = logits_type == MOE_BF16;
+    a.bias = bias;
+    a.T = n_tokens;
+    a.E = n_experts;
+    a.k = n_used;
+    a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+    a.n_group = cfg->n_group;
+    a.topk_group = cfg->topk_group;
+    a.group_top = cfg->group_top;
+    a.renorm = cfg->renorm;
+    a.scale = cfg->scale;
+    a.ids = ids;
+    a.w = route_w;
+    a.scores = scores;
+    return hip_check(launch_router_scored(a, (hipStream_t)stream), "scored router");
+}
+
+moe_status moe_router_scored_backward(const void* logits, moe_dtype logits_type, const int32_t* ids,
+                                      const float* d_route_w, const float* d_scores,
+                                      int64_t d_scores_stride, int64_t n_tokens, int32_t n_experts,
+                                      int32_t n_used, const moe_router_config* cfg, void* d_logits,
+                                      void* stream) {
+    moe_status s;
+    g_err.clear();
+    if (logits_type != MOE_F32 && logits_type != MOE_BF16) return fail(MOE_EINVAL, "logits must be F32 or BF16");
+    if ((s = check_router(cfg, n_tokens, n_experts, n_used, false))) return s;
+    if (d_scores && d_scores_stride != 0 && d_scores_stride < n_experts)
+        return fail(MOE_EINVAL, "d_scores_stride must be 0 or at least n_experts (got %lld)",
+                    (long long)d_scores_stride);
+    if (n_tokens > 0 && (!logits || !ids || !d_route_w || !d_logits)) return fail(MOE_EINVAL, "NULL pointer argument");
+    RouterGradArgs a{};
+    a.logits = logits;
+    a.bf16 = logits_type == MOE_BF16;
+    a.ids = ids;
+    a.dw = d_route_w;
+    a.ds = d_scores;
+    a.ds_stride = d_scores_stride;
+    a.T = n_tokens;
+    a.E = n_experts;
+    a.k = n_used;
+    a.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
+    a.renorm = cfg->renorm;
+    a.scale = cfg->scale;
+    a.dl = d_logits;
+    return hip_check(launch_router_grad(a, (hipStream_t)stream), "scored router gradient");
 }
 
 moe_status moe_router_topk(const float* logits, int64_t n_tokens, int32_t n_experts, int32_t n_used,

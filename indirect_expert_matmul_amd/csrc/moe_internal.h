@@ -121,6 +121,9 @@ struct GemmProblem {
     // scales [rows][K/32] (one per 32-column block); rows indexed as for A
     const int8_t* Aq;
     const float* Ad;
+    // MXFP4-activation GEMM only: codes in Aq ([rows][K/2], even column in the low nibble)
+    // and E8M0 scale bytes [rows][K/32]
+    const uint8_t* As;
     const int32_t* a_rows;    // A row of position j, or nullptr: row (a_row_mod ? j % a_row_mod : j)
     int32_t a_row_mod;
     void* out;
@@ -187,6 +190,29 @@ hipError_t launch_quant_act(const QuantArgs& a, hipStream_t st);
 hipError_t launch_gemm_q8a(const GemmArgs& a, hipStream_t st);
 int64_t gemm_q8a_max_threads(const GemmArgs& a);
 constexpr int kQ8aTileM = 128;
+
+// ---------------------------------------------------------------- MXFP4 activations
+// Rows of 32-column blocks -> E2M1 codes and E8M0 scale bytes (moe_quantize_mxfp4).
+struct QuantFp4Part {
+    const void* src;   // [rows][K], bf16 bits (src_bf16) or float32
+    int64_t rows, K;   // K % 32 == 0
+    uint8_t* q;        // [rows][K/2]
+    uint8_t* s;        // [rows][K/32]
+    void* values;      // nullptr, or [rows][K] of src's type
+};
+struct QuantFp4Args {
+    QuantFp4Part part[2]; // one launch quantizes up to two tensors
+    int32_t n_part;
+    int32_t src_bf16;
+    int64_t blocks0;   // set by the launcher: thread blocks of part 0
+};
+hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
+// Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
+// activations (Aq / As); tile_tab required for routed problems, tile height kFp4TileM.
+// mode 1 writes silu(gate) * up in float32.
+hipError_t launch_gemm_fp4(const GemmArgs& a, hipStream_t st);
+int64_t gemm_fp4_max_threads(const GemmArgs& a);
+constexpr int kFp4TileM = 64;
 
 // ---------------------------------------------------------------- fp32 grouped matmul (Tiny)
 struct GemmF32Args {
@@ -261,6 +287,38 @@ struct RouterArgs {
     float* w;             // [T][k]
 };
 hipError_t launch_router(const RouterArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- scored routing
+struct RouterScoredArgs {
+    const void* logits;   // [T][E], bf16 bits (bf16) or float32
+    int32_t bf16;
+    const float* bias;    // [E] or nullptr
+    int64_t T;
+    int32_t E;            // <= kMaxExperts
+    int32_t k;            // 1 <= k <= topk_group * E / n_group
+    int32_t sigmoid;      // 0 softmax
+    int32_t n_group, topk_group, group_top;
+    int32_t renorm;
+    float scale;
+    int32_t* ids;         // [T][k]
+    float* w;             // [T][k]
+    float* scores;        // [T][E] or nullptr
+};
+hipError_t launch_router_scored(const RouterScoredArgs& a, hipStream_t st);
+struct RouterGradArgs {
+    const void* logits;
+    int32_t bf16;
+    const int32_t* ids;   // [T][k]
+    const float* dw;      // [T][k]
+    const float* ds;      // nullptr, or row t at ds + t * ds_stride
+    int64_t ds_stride;
+    int64_t T;
+    int32_t E, k;
+    int32_t sigmoid, renorm;
+    float scale;
+    void* dl;             // [T][E], the logits' type
+};
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t st);
 
 // ---------------------------------------------------------------- reduce / scatter (K5)
 struct ReduceArgs {
