@@ -126,7 +126,8 @@ typedef struct {
      * 2: MXFP4 activations (MXFP4 experts only): activation rows are quantized to MXFP4
      * (moe_quantize_mxfp4's format) and multiplied with the experts' codes by the block
      * scaled FP4 MFMA, fp32 accumulation. The fused FFN quantizes x before gate/up and the
-     * float32 h before down. Kernel order for timing: as for 1. */
+     * float32 h before down. Kernel order for timing: row ids, quantize, grouped GEMM[, down
+     * grouped GEMM], reduce / fix-up. */
     int32_t act_quant;
     int32_t reserved[5];
     void *const *timing_events;

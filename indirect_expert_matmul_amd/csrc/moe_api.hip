@@ -246,14 +246,12 @@ FfnPlan carve_ffn(Carve& c, const FfnDims& d, int path) {
         p.hshd = (float*)c.take((size_t)d.S * d.T * (d.n_ff_sh / 32) * 4);
     } else if (path == 4) {
         p.r = carve_row_ids(c, n, d.E, true, kFp4TileM);
-        p.xq = (int8_t*)c.take((size_t)d.T * d.n_embd / 2);
-        p.xs = (uint8_t*)c.take((size_t)d.T * (d.n_embd / 32));
-        p.h = c.take((size_t)n * d.n_ff * 4);
-        p.hsh = c.take((size_t)d.S * d.T * d.n_ff_sh * 4);
-        p.hq = (int8_t*)c.take((size_t)n * d.n_ff / 2);
-        p.hs = (uint8_t*)c.take((size_t)n * (d.n_ff / 32));
-        p.hshq = (int8_t*)c.take((size_t)d.S * d.T * d.n_ff_sh / 2);
-        p.hshs = (uint8_t*)c.take((size_t)d.S * d.T * (d.n_ff_sh / 32));
+        p.xq = (int8_t*)c.take((size_t)d.T * fp4_code_row(d.n_embd));
+        p.xs = (uint8_t*)c.take((size_t)d.T * fp4_scale_row(d.n_embd));
+        p.hq = (int8_t*)c.take((size_t)n * fp4_code_row(d.n_ff));
+        p.hs = (uint8_t*)c.take((size_t)n * fp4_scale_row(d.n_ff));
+        p.hshq = (int8_t*)c.take((size_t)d.S * d.T * fp4_code_row(d.n_ff_sh));
+        p.hshs = (uint8_t*)c.take((size_t)d.S * d.T * fp4_scale_row(d.n_ff_sh));
     } else if (path == 1) {
         p.msub = gemm_pick_msub((double)n / d.E);
         p.r = carve_row_ids(c, n, d.E, true, gemm_tile_m(p.msub));
@@ -289,8 +287,8 @@ MmidPlan carve_mmid(Carve& c, int64_t T, int32_t k, int32_t E, int64_t N, bool w
         p.ad = (float*)c.take((size_t)(T * B) * (K / 32) * 4);
     } else if (path == 4) {
         p.r = carve_row_ids(c, n, E, true, kFp4TileM);
-        p.aq = (int8_t*)c.take((size_t)(T * B) * K / 2);
-        p.as = (uint8_t*)c.take((size_t)(T * B) * (K / 32));
+        p.aq = (int8_t*)c.take((size_t)(T * B) * fp4_code_row(K));
+        p.as = (uint8_t*)c.take((size_t)(T * B) * fp4_scale_row(K));
     } else if (!q8 || path == 1) {
         p.msub = gemm_pick_msub((double)n / E);
         p.r = carve_row_ids(c, n, E, true, q8 ? gemm_tile_m(p.msub) : 0);
@@ -421,6 +419,7 @@ QuantFp4Part fp4_part(const void* src, int64_t rows, int64_t K, int8_t* q, uint8
     p.K = K;
     p.q = (uint8_t*)q;
     p.s = s;
+    p.padded = 1;
     return p;
 }
 
@@ -465,7 +464,12 @@ moe_status check_fp4_weights(const moe_weights* w, const char* name) {
         return fail(MOE_EINVAL, "MXFP4 activations: the codes of %s must be 16-byte aligned", name);
     return MOE_OK;
 }
-moe_status check_fp4_limits(const GemmArgs& g, int64_t act_blocks, const char* what) {
+// gathered_rows: rows of the activation tensor that is addressed through the row map.
+moe_status check_fp4_limits(const GemmArgs& g, int64_t act_blocks, int64_t gathered_rows, const char* what) {
+    for (int i = 0; i < g.n_prob; i++)
+        if (g.p[i].K >= (1 << 24)) return fail(MOE_ELIMIT, "%s: MXFP4 activations need cols < 2^24", what);
+    if (gathered_rows * fp4_code_row(g.p[0].K) > k4GiB - 256)
+        return fail(MOE_ELIMIT, "%s: the gathered MXFP4 activation codes must be under 4 GiB", what);
     if (act_blocks >= kFp4MaxBlocks)
         return fail(MOE_ELIMIT, "%s: too many activation blocks (rows * K / 32 must be under 2^31)", what);
     if (gemm_fp4_max_threads(g) >= k4GiB)
@@ -479,8 +483,8 @@ void fp4_tiles(RowIdsArgs& ra, const RowIdsPlan& r) {
     ra.tile_cap[0] = r.tile_cap;
 }
 
-// The fused FFN up to the per-slot rows (p.y, p.ysh): row ids, x -> codes, gate/up, the
-// float32 h -> codes, down.
+// The fused FFN up to the per-slot rows (p.y, p.ysh): row ids, x -> codes, gate/up (whose
+// epilogue quantizes the float32 h), down.
 moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, const moe_weights* up,
                    const moe_weights* down, const moe_weights* sg, const moe_weights* su,
                    const moe_weights* sd, const void* x, const int32_t* ids, Timer& tm, hipStream_t st) {
@@ -495,27 +499,27 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
         return s;
     RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
     fp4_tiles(ra, p.r);
-    QuantFp4Args qx{}, qh{};
+    QuantFp4Args qx{};
     qx.src_bf16 = 1;
     qx.n_part = 1;
     qx.part[0] = fp4_part(x, d.T, d.n_embd, p.xq, p.xs);
-    qh.n_part = shared ? 2 : 1;
-    qh.part[0] = fp4_part(p.h, n, d.n_ff, p.hq, p.hs);
     GemmArgs g{}, g2{};
     g.mode = 1;
+    g.nt = g2.nt = 2;
     g.n_prob = g2.n_prob = shared ? 2 : 1;
-    g.p[0] = fp4_routed(gate, up, p.r, n, p.xq, p.xs, p.h);
+    g.p[0] = fp4_routed(gate, up, p.r, n, p.xq, p.xs, p.hq);
+    g.p[0].out_s = p.hs;
     g.p[0].a_rows = p.r.ids_src1;
     g2.p[0] = fp4_routed(down, nullptr, p.r, n, p.hq, p.hs, p.y);
     g2.p[0].out_rows = p.r.ids_dst;
     if (shared) {
-        qh.part[1] = fp4_part(p.hsh, (int64_t)d.S * d.T, d.n_ff_sh, p.hshq, p.hshs);
-        g.p[1] = fp4_shared(sg, su, d.T, p.xq, p.xs, p.hsh);
+        g.p[1] = fp4_shared(sg, su, d.T, p.xq, p.xs, p.hshq);
+        g.p[1].out_s = p.hshs;
         g.p[1].a_row_mod = (int32_t)d.T;
         g2.p[1] = fp4_shared(sd, nullptr, d.T, p.hshq, p.hshs, p.ysh);
     }
-    if ((s = check_fp4_limits(g, d.T * (d.n_embd / 32), "gate/up"))) return s;
-    if ((s = check_fp4_limits(g2, n * (d.n_ff / 32) + (int64_t)d.S * d.T * (d.n_ff_sh / 32), "down"))) return s;
+    if ((s = check_fp4_limits(g, d.T * (d.n_embd / 32), d.T, "gate/up"))) return s;
+    if ((s = check_fp4_limits(g2, n * (d.n_ff / 32) + (int64_t)d.S * d.T * (d.n_ff_sh / 32), 0, "down"))) return s;
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
     tm.end();
@@ -524,9 +528,6 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g, st), "gate/up grouped GEMM (MXFP4)"))) return s;
-    tm.end();
-    tm.begin();
-    if ((s = hip_check(launch_quant_mxfp4(qh, st), "quantize h"))) return s;
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g2, st), "down grouped GEMM (MXFP4)"))) return s;
@@ -548,10 +549,11 @@ moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, i
     qa.part[0] = fp4_part(src1, T * B, w->cols, p.aq, p.as);
     GemmArgs g{};
     g.n_prob = 1;
+    g.nt = 2;
     g.p[0] = fp4_routed(w, nullptr, p.r, n, p.aq, p.as, slot_out);
     g.p[0].a_rows = p.r.ids_src1;
     g.p[0].out_rows = p.r.ids_dst;
-    if ((s = check_fp4_limits(g, T * B * (w->cols / 32), "mul_mat_id"))) return s;
+    if ((s = check_fp4_limits(g, T * B * (w->cols / 32), T * B, "mul_mat_id"))) return s;
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
     tm.end();
@@ -1256,6 +1258,7 @@ moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_type, int64_t rows, int
     a.src_bf16 = x_type == MOE_BF16;
     a.part[0] = fp4_part(x, rows, K, (int8_t*)codes, scales);
     a.part[0].values = values;
+    a.part[0].padded = 0;
     return hip_check(launch_quant_mxfp4(a, (hipStream_t)stream), "quantize to MXFP4");
 }
 

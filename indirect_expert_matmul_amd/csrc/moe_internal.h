@@ -121,12 +121,13 @@ struct GemmProblem {
     // scales [rows][K/32] (one per 32-column block); rows indexed as for A
     const int8_t* Aq;
     const float* Ad;
-    // MXFP4-activation GEMM only: codes in Aq ([rows][K/2], even column in the low nibble)
-    // and E8M0 scale bytes [rows][K/32]
+    // MXFP4-activation GEMM only: codes in Aq ([rows][fp4_code_row(K)], even column in the
+    // low nibble, 0 past K) and E8M0 scale bytes [rows][fp4_scale_row(K)]
     const uint8_t* As;
     const int32_t* a_rows;    // A row of position j, or nullptr: row (a_row_mod ? j % a_row_mod : j)
     int32_t a_row_mod;
     void* out;
+    uint8_t* out_s;           // MXFP4-activation GEMM, mode 1: scale bytes of h (codes in out)
     int64_t ldo;
     const int32_t* out_rows;  // nullptr: row j; else out_rows[j]
     // 1: segments average at most one M tile, so each weight slab is read once per
@@ -139,6 +140,7 @@ struct GemmArgs {
     GemmProblem p[2];
     int32_t n_prob;
     int32_t mode;             // 0: fp32 out = acc; 1: bf16 out = silu(acc_gate) * acc_up
+    int32_t nt;               // MXFP4-activation GEMM: weight rows per wave / 32 (1 or 2; 2 in mode 1)
     int32_t grid_real;        // blocks carrying tiles (before padding to a multiple of 8)
     // 0: Q8_0 experts; 1: MXFP4 -- qs1/qs2 hold two E2M1 codes per byte ([n_mat][N][K/2],
     // even column in the low nibble), d1/d2 the E8M0 scale bytes ([n_mat][N][K/32]);
@@ -199,7 +201,14 @@ struct QuantFp4Part {
     uint8_t* q;        // [rows][K/2]
     uint8_t* s;        // [rows][K/32]
     void* values;      // nullptr, or [rows][K] of src's type
+    // 1: rows padded as the grouped GEMM reads them: fp4_code_row(K) code bytes (0 past K)
+    // and fp4_scale_row(K) scale bytes (scale 1 up to the last code stage)
+    int32_t padded;
 };
+// Bytes of an activation row in the grouped GEMM's operands: codes padded to whole stages of
+// 128 columns, scale bytes to 16 (what one load takes).
+inline __host__ __device__ int64_t fp4_code_row(int64_t K) { return (K + 127) / 128 * 64; }
+inline __host__ __device__ int64_t fp4_scale_row(int64_t K) { return (K / 32 + 15) / 16 * 16; }
 struct QuantFp4Args {
     QuantFp4Part part[2]; // one launch quantizes up to two tensors
     int32_t n_part;
@@ -209,10 +218,10 @@ struct QuantFp4Args {
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
 // activations (Aq / As); tile_tab required for routed problems, tile height kFp4TileM.
-// mode 1 writes silu(gate) * up in float32.
+// mode 1 writes silu(gate) * up quantized, as padded activation rows (out, out_s).
 hipError_t launch_gemm_fp4(const GemmArgs& a, hipStream_t st);
 int64_t gemm_fp4_max_threads(const GemmArgs& a);
-constexpr int kFp4TileM = 64;
+constexpr int kFp4TileM = 128;
 
 // ---------------------------------------------------------------- fp32 grouped matmul (Tiny)
 struct GemmF32Args {

@@ -10,78 +10,99 @@
 // (checked value by value against the comparison form over all exponents, ties and
 // subnormals). A field of 255 (infinity or NaN) makes the whole block NaN.
 //
-// First form: one thread per block.
+// Memory bound: a wave reads 1 KB at a time, each lane 16 bytes, so a block's maximum is a
+// few lane shuffles (4 lanes of bf16, 8 of float32) and every access of the wave, the
+// codes' 2 or 4 bytes a lane included, is one contiguous run. Each thread has kU such
+// pieces in flight.
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
-
-// Value of E2M1 code c (0..15) in units of the scale.
-__device__ __forceinline__ float e2m1(int c) {
-    const int m = c & 7;
-    const float v = m < 4 ? 0.5f * m : (m < 6 ? (float)(m - 2) : (float)(2 * m - 8));
-    return (c & 8) ? -v : v;
-}
+constexpr int kU = 4;   // 16-byte pieces per thread
 
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void k_quant_mxfp4(QuantFp4Args args) {
+    constexpr int LANES = BF16 ? 4 : 8;                        // lanes per block of 32
+    constexpr int PER = kThreads / LANES;                      // blocks per piece row
     const bool second = (int64_t)blockIdx.x >= args.blocks0;
     const QuantFp4Part& a = args.part[second ? 1 : 0];
-    const int64_t blk = ((int64_t)blockIdx.x - (second ? args.blocks0 : 0)) * kThreads + threadIdx.x;
-    const int64_t KB = a.K >> 5;
-    if (blk >= a.rows * KB) return;
-    float v[32];
-    if constexpr (BF16) {
-        const i32x4* src = (const i32x4*)((const uint16_t*)a.src + blk * 32);
+    const int64_t base = ((int64_t)blockIdx.x - (second ? args.blocks0 : 0)) * (PER * kU) + threadIdx.x / LANES;
+    const uint32_t KB = (uint32_t)(a.K >> 5);
+    const int64_t total = a.rows * KB;                         // < 2^31
+    const int sub = threadIdx.x % LANES;
+    i32x4 x[kU];
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+        const int64_t blk = min(base + u * PER, total - 1);    // spare lanes repeat the last block
+        x[u] = __builtin_nontemporal_load((const i32x4*)a.src + blk * LANES + sub);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+        const int64_t blk = base + u * PER;
+        uint32_t top = 0;   // largest magnitude as bits: NaN and infinity sort above all numbers
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const i32x4 w = src[i];
+            const uint32_t w = (uint32_t)x[u][i];
+            if constexpr (BF16) top = max(top, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u));
+            else top = max(top, w & 0x7fffffffu);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                v[8 * i + 2 * j] = __builtin_bit_cast(float, (uint32_t)w[j] << 16);
-                v[8 * i + 2 * j + 1] = __builtin_bit_cast(float, (uint32_t)w[j] & 0xffff0000u);
+        for (int m = 1; m < LANES; m <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+        const int field = (int)(top >> 23);
+        const bool bad = field == 255;
+        const uint32_t byte = bad ? 255u : (uint32_t)max(field - 2, 0);
+        // the scale as a float32: subnormal 2^-127 for byte 0
+        const float scale = __uint_as_float(byte ? byte << 23 : 0x00400000u);
+        uint32_t q = 0;
+        if constexpr (BF16) {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, (uint32_t)x[u][0]), scale, 0);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, (uint32_t)x[u][1]), scale, 1);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, (uint32_t)x[u][2]), scale, 2);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2, (uint32_t)x[u][3]), scale, 3);
+        } else {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __int_as_float(x[u][0]), __int_as_float(x[u][1]), scale, 0);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __int_as_float(x[u][2]), __int_as_float(x[u][3]), scale, 1);
+        }
+        if (bad) q = 0;
+        if (blk >= total) continue;
+        int64_t cb = blk;        // where the block's codes and scale byte go, in blocks
+        int64_t sb = blk;
+        if (a.padded) {
+            const uint32_t r = (uint32_t)blk / KB, b = (uint32_t)blk - r * KB;
+            const uint32_t KBc = (KB + 3) & ~3u;   // blocks in whole stages
+            cb = r * (fp4_code_row(a.K) / 16) + b;
+            sb = r * fp4_scale_row(a.K) + b;
+            if (b == KB - 1)
+                for (uint32_t p = 1; p < KBc - b; p++) {
+                    if constexpr (BF16) ((uint32_t*)a.q)[(cb + p) * LANES + sub] = 0;
+                    else ((uint16_t*)a.q)[(cb + p) * LANES + sub] = 0;
+                    if (sub == 0) a.s[sb + p] = 127;
+                }
+        }
+        if constexpr (BF16) ((uint32_t*)a.q)[cb * LANES + sub] = q;
+        else ((uint16_t*)a.q)[cb * LANES + sub] = (uint16_t)q;
+        if (sub == 0) a.s[sb] = (uint8_t)byte;
+        if (a.values) {
+            i32x4 y;
+            const uint32_t nan = BF16 ? 0x7fc07fc0u : 0x7fc00000u;
+            if constexpr (BF16) {
+                y[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0));
+                y[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1));
+                y[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2));
+                y[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3));
+            } else {
+                const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 0);
+                const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, scale, 1);
+                y = i32x4{__float_as_int(lo[0]), __float_as_int(lo[1]), __float_as_int(hi[0]), __float_as_int(hi[1])};
             }
-        }
-    } else {
-        const f32x4* src = (const f32x4*)((const float*)a.src + blk * 32);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const f32x4 w = src[i];
-#pragma unroll
-            for (int j = 0; j < 4; j++) v[4 * i + j] = w[j];
-        }
-    }
-    uint32_t top = 0;   // largest magnitude as bits: NaN and infinity sort above all numbers
-#pragma unroll
-    for (int i = 0; i < 32; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    const int field = (int)(top >> 23);
-    const bool bad = field == 255;
-    const int byte = bad ? 255 : max(field - 2, 0);
-    // the scale as a float32: subnormal 2^-127 for byte 0
-    const float scale = __uint_as_float(byte ? (uint32_t)byte << 23 : 0x00400000u);
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        uint32_t p = 0;
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, v[8 * i], v[8 * i + 1], scale, 0);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, v[8 * i + 2], v[8 * i + 3], scale, 1);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, v[8 * i + 4], v[8 * i + 5], scale, 2);
-        p = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(p, v[8 * i + 6], v[8 * i + 7], scale, 3);
-        q[i] = bad ? 0u : p;
-    }
-    *(i32x4*)(a.q + blk * 16) = i32x4{(int)q[0], (int)q[1], (int)q[2], (int)q[3]};
-    a.s[blk] = (uint8_t)byte;
-    if (a.values) {
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-            const float y = bad ? __uint_as_float(0x7fc00000u) : e2m1((q[i >> 3] >> (4 * (i & 7))) & 15) * scale;
-            if constexpr (BF16) ((uint16_t*)a.values)[blk * 32 + i] = (uint16_t)(__float_as_uint(y) >> 16);
-            else ((float*)a.values)[blk * 32 + i] = y;
+            if (bad) y = i32x4{(int)nan, (int)nan, (int)nan, (int)nan};
+            __builtin_nontemporal_store(y, (i32x4*)a.values + blk * LANES + sub);
         }
     }
 }
@@ -90,8 +111,9 @@ __global__ __launch_bounds__(kThreads) void k_quant_mxfp4(QuantFp4Args args) {
 
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a0, hipStream_t st) {
     QuantFp4Args a = a0;
+    const int64_t per = kThreads / (a.src_bf16 ? 4 : 8) * kU;   // blocks of 32 per thread block
     int64_t grid[2] = {0, 0};
-    for (int i = 0; i < a.n_part; i++) grid[i] = (a.part[i].rows * (a.part[i].K >> 5) + kThreads - 1) / kThreads;
+    for (int i = 0; i < a.n_part; i++) grid[i] = (a.part[i].rows * (a.part[i].K >> 5) + per - 1) / per;
     a.blocks0 = grid[0];
     const int64_t total = grid[0] + grid[1];
     if (total <= 0) return hipSuccess;
