@@ -161,18 +161,25 @@ int select_path_fmt(int64_t T, int32_t k, int32_t E, int64_t act_width, bool fp4
 }
 
 // With options.act_quant = 1: 3 (the quantized-activation grouped GEMM, Q8_0 experts
-// only, whatever the batch size), with 2: 4 (the MXFP4-activation grouped GEMM, MXFP4
-// experts only), else the choice above; or a negative status.
+// only, whatever the batch size), with 2 (MXFP4 experts only): 4 (the MXFP4-activation
+// grouped GEMM) or 5 (its GEMV), else the choice above; or a negative status. S: shared
+// experts; min_width: the narrowest activation row.
 int select_path_aq(int64_t T, int32_t k, int32_t E, int64_t act_width, int32_t wtype,
-                   const moe_options* o) {
+                   const moe_options* o, int64_t S = 0, int64_t min_width = 1LL << 30) {
     const int32_t aq = o ? o->act_quant : 0;
     if (aq < 0 || aq > 2) return fail(MOE_EINVAL, "options.act_quant must be 0, 1 or 2 (got %d)", aq);
     if (aq == 2) {
         if (wtype != MOE_MXFP4) return fail(MOE_EINVAL, "MXFP4 activations (act_quant = 2) need MXFP4 experts");
-        if (o->path != 0 && o->path != 1)
-            return fail(MOE_EINVAL, "MXFP4 activations run on the grouped GEMM only: options.path must "
-                        "be 0 or 1 (got %d)", o->path);
-        return 4;
+        const bool dec_ok = T * (int64_t)k <= kDecFp4Slots && S * T <= kDecFp4Slots && min_width >= 128;
+        if (o->path == 1) return 4;
+        if (o->path == 2) {
+            if (!dec_ok)
+                return fail(MOE_EINVAL, "GEMV path with MXFP4 activations needs n_tokens*n_used and "
+                            "n_tokens*shared experts <= %d and widths >= 128", kDecFp4Slots);
+            return 5;
+        }
+        if (o->path != 0) return fail(MOE_EINVAL, "options.path must be 0, 1 or 2 (got %d)", o->path);
+        return dec_ok ? 5 : 4;
     }
     if (!aq)
         return select_path_fmt(T, k, E, act_width,
@@ -228,6 +235,7 @@ struct FfnPlan {
     int8_t *xq, *hq, *hshq;
     float *xd, *hd, *hshd;
     uint8_t *xs, *hs, *hshs;   // MXFP4 activations: E8M0 scale bytes (codes in xq, hq, hshq)
+    bool fuse;                 // path 5: the down GEMV writes out itself
 };
 
 FfnPlan carve_ffn(Carve& c, const FfnDims& d, int path) {
@@ -252,6 +260,11 @@ FfnPlan carve_ffn(Carve& c, const FfnDims& d, int path) {
         p.hs = (uint8_t*)c.take((size_t)n * fp4_scale_row(d.n_ff));
         p.hshq = (int8_t*)c.take((size_t)d.S * d.T * fp4_code_row(d.n_ff_sh));
         p.hshs = (uint8_t*)c.take((size_t)d.S * d.T * fp4_scale_row(d.n_ff_sh));
+    } else if (path == 5) {   // h in float32; a small batch's down sums the slots itself
+        p.h = c.take((size_t)n * d.n_ff * 4);
+        p.hsh = c.take((size_t)d.S * d.T * d.n_ff_sh * 4);
+        p.fuse = decode_fp4_fuses(n, d.E, d.S, d.n_ff > d.n_ff_sh ? d.n_ff : d.n_ff_sh);
+        if (p.fuse) return p;
     } else if (path == 1) {
         p.msub = gemm_pick_msub((double)n / d.E);
         p.r = carve_row_ids(c, n, d.E, true, gemm_tile_m(p.msub));
@@ -274,6 +287,7 @@ struct MmidPlan {
     int8_t* aq;   // quantized-activation path: src1 codes [T*B][K] and block scales
     float* ad;
     uint8_t* as;  // MXFP4 activations: E8M0 scale bytes (codes [T*B][K/2] in aq)
+    bool fuse;    // path 5: the GEMV writes the weighted sum itself
 };
 
 MmidPlan carve_mmid(Carve& c, int64_t T, int32_t k, int32_t E, int64_t N, bool weighted, bool q8, int path,
@@ -289,6 +303,9 @@ MmidPlan carve_mmid(Carve& c, int64_t T, int32_t k, int32_t E, int64_t N, bool w
         p.r = carve_row_ids(c, n, E, true, kFp4TileM);
         p.aq = (int8_t*)c.take((size_t)(T * B) * fp4_code_row(K));
         p.as = (uint8_t*)c.take((size_t)(T * B) * fp4_scale_row(K));
+    } else if (path == 5) {
+        p.fuse = weighted && decode_fp4_fuses(n, E, 0, K);
+        if (p.fuse) return p;
     } else if (!q8 || path == 1) {
         p.msub = gemm_pick_msub((double)n / E);
         p.r = carve_row_ids(c, n, E, true, q8 ? gemm_tile_m(p.msub) : 0);
@@ -338,6 +355,11 @@ moe_status validate_ffn(const moe_weights* gate, const moe_weights* up, const mo
         d->n_ff_sh = (int32_t)sg->rows;
     }
     return MOE_OK;
+}
+
+int64_t ffn_min_width(const FfnDims& d) {
+    int64_t w = d.n_embd < d.n_ff ? d.n_embd : d.n_ff;
+    return d.S && d.n_ff_sh < w ? d.n_ff_sh : w;
 }
 
 int64_t ffn_act_width(const FfnDims& d) {
@@ -566,6 +588,92 @@ moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, i
     return MOE_OK;
 }
 
+DecFp4Weights fp4_dec_weights(const moe_weights* w1, const moe_weights* w2) {
+    DecFp4Weights d{};
+    if (!w1 || !w1->n_mat) return d;
+    d.q1 = (const uint8_t*)w1->data;
+    d.s1 = (const uint8_t*)w1->scales;
+    if (w2) {
+        d.q2 = (const uint8_t*)w2->data;
+        d.s2 = (const uint8_t*)w2->scales;
+    }
+    d.n_mat = (int32_t)w1->n_mat;
+    d.N = (int32_t)w1->rows;
+    d.K = (int32_t)w1->cols;
+    return d;
+}
+
+// The fused FFN by GEMV: gate/up (float32 h), then down (p.fuse: with the sum over the slots).
+moe_status ffn_dec_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, const moe_weights* up,
+                       const moe_weights* down, const moe_weights* sg, const moe_weights* su,
+                       const moe_weights* sd, const void* x, const int32_t* ids, const float* route_w,
+                       float* out, Timer& tm, hipStream_t st) {
+    moe_status s;
+    const bool shared = d.S > 0;
+    if ((s = check_fp4_act(x, "x")) || (s = check_fp4_weights(gate, "gate")) ||
+        (s = check_fp4_weights(up, "up")) || (s = check_fp4_weights(down, "down")))
+        return s;
+    if (shared && ((s = check_fp4_weights(sg, "sh_gate")) || (s = check_fp4_weights(su, "sh_up")) ||
+                   (s = check_fp4_weights(sd, "sh_down"))))
+        return s;
+    DecFp4Args a{};
+    a.ids = ids;
+    a.T = (int32_t)d.T;
+    a.k = d.k;
+    a.E = d.E;
+    DecFp4Args b = a;
+    a.rw = fp4_dec_weights(gate, up);
+    if (shared) a.sw = fp4_dec_weights(sg, su);
+    a.act = a.sact = x;
+    a.act_B = 1;
+    a.mode = 1;
+    a.out = (float*)p.h;
+    a.sout = (float*)p.hsh;
+    b.rw = fp4_dec_weights(down, nullptr);
+    if (shared) b.sw = fp4_dec_weights(sd, nullptr);
+    b.act = p.h;
+    b.sact = p.hsh;
+    b.f32 = 1;
+    b.act_B = d.k;
+    b.sact_jstride = d.T;
+    b.fuse = p.fuse;
+    b.route_w = route_w;
+    b.out_tok = out;
+    b.out = (float*)p.y;
+    b.sout = (float*)p.ysh;
+    tm.begin();
+    if ((s = hip_check(launch_decode_fp4(a, st), "gate/up GEMV (MXFP4)"))) return s;
+    tm.end();
+    tm.begin();
+    if ((s = hip_check(launch_decode_fp4(b, st), "down GEMV (MXFP4)"))) return s;
+    tm.end();
+    return MOE_OK;
+}
+
+// moe_mul_mat_id by GEMV: per-slot rows to slot_out, or (p.fuse) the weighted sum to dst.
+moe_status mmid_dec_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, int32_t B,
+                        const int32_t* ids, int64_t T, int32_t k, const float* route_w, float* slot_out,
+                        float* dst, Timer& tm, hipStream_t st) {
+    moe_status s;
+    if ((s = check_fp4_act(src1, "src1")) || (s = check_fp4_weights(w, "w"))) return s;
+    DecFp4Args a{};
+    a.ids = ids;
+    a.T = (int32_t)T;
+    a.k = k;
+    a.E = (int32_t)w->n_mat;
+    a.rw = fp4_dec_weights(w, nullptr);
+    a.act = src1;
+    a.act_B = B;
+    a.out = slot_out;
+    a.fuse = p.fuse;
+    a.route_w = route_w;
+    a.out_tok = dst;
+    tm.begin();
+    if ((s = hip_check(launch_decode_fp4(a, st), "GEMV (MXFP4)"))) return s;
+    tm.end();
+    return MOE_OK;
+}
+
 moe_status check_router(const moe_router_config* c, int64_t T, int32_t E, int32_t k, bool choose) {
     moe_status s;
     if ((s = check_tokens(T, k))) return s;
@@ -693,7 +801,8 @@ size_t moe_ffn_fused_workspace_size(const moe_weights* gate, const moe_weights* 
     if (validate_ffn(gate, &up, &down, (su ? sh_gate : nullptr), su, (su ? &sdown : nullptr),
                      x_type, n_tokens, n_used, &d))
         return 0;
-    const int path = select_path_aq(d.T, d.k, d.E, ffn_act_width(d), gate->type, opt);
+    const int path = select_path_aq(d.T, d.k, d.E, ffn_act_width(d), gate->type, opt, d.S,
+                                    ffn_min_width(d));
     if (path < 0) return 0;
     Carve c(nullptr);
     carve_ffn(c, d, path);
@@ -715,7 +824,8 @@ moe_status moe_ffn_fused(const moe_weights* gate, const moe_weights* up, const m
         return MOE_OK;
     }
     if (!x || !ids || !route_w || !out) return fail(MOE_EINVAL, "NULL pointer argument");
-    const int path = select_path_aq(d.T, d.k, d.E, ffn_act_width(d), gate->type, opt);
+    const int path = select_path_aq(d.T, d.k, d.E, ffn_act_width(d), gate->type, opt, d.S,
+                                    ffn_min_width(d));
     if (path < 0) return (moe_status)path;
     Carve sz(nullptr);
     carve_ffn(sz, d, path);
@@ -835,6 +945,9 @@ moe_status moe_ffn_fused(const moe_weights* gate, const moe_weights* up, const m
         tm.end();
     } else if (path == 4) {
         if ((s = ffn_fp4(d, p, gate, up, down, sh_gate, sh_up, sh_down, x, ids, tm, st))) return s;
+    } else if (path == 5) {
+        if ((s = ffn_dec_fp4(d, p, gate, up, down, sh_gate, sh_up, sh_down, x, ids, route_w, out, tm, st))) return s;
+        reduced = p.fuse;
     } else if (path == 1) {
         const int bm = gemm_tile_m(p.msub);
         RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
@@ -1031,7 +1144,7 @@ size_t moe_mul_mat_id_workspace_size(const moe_weights* w, moe_dtype src1_type,
     if (validate_mmid(w, src1_type, src1_rows_per_token, n_tokens, n_used)) return 0;
     const bool q8 = w->type != MOE_F32;   // quantized experts
     if (!q8 && opt && ((opt->path != 0 && opt->path != 1) || opt->act_quant)) return 0;
-    const int path = q8 ? select_path_aq(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt) : 1;
+    const int path = q8 ? select_path_aq(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt, 0, w->cols) : 1;
     if (path < 0) return 0;
     // the weighted and unweighted calls use the same plan size when weighted
     Carve c(nullptr);
@@ -1062,7 +1175,7 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
         return fail(MOE_EINVAL, "quantized activations (act_quant = 1) need Q8_0 experts");
     if (!q8 && n_tokens * k * (int64_t)N >= k4GiB - 256)
         return fail(MOE_ELIMIT, "float32 mul_mat_id: n_tokens * n_used * N must be under 2^32");
-    const int path = q8 ? select_path_aq(n_tokens, k, E, K, w->type, opt) : 1;
+    const int path = q8 ? select_path_aq(n_tokens, k, E, K, w->type, opt, 0, K) : 1;
     if (path < 0) return (moe_status)path;
     const bool weighted = route_w != nullptr;
     Carve sz(nullptr);
@@ -1121,6 +1234,12 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
         tm.end();
     } else if (path == 4) {
         if ((s = mmid_fp4(p, w, src1, B, ids, n_tokens, k, slot_out, tm, st))) return s;
+    } else if (path == 5) {
+        if ((s = mmid_dec_fp4(p, w, src1, B, ids, n_tokens, k, route_w, slot_out, dst, tm, st))) return s;
+        if (p.fuse || !weighted) {   // written in full, rows of invalid slots too
+            g_stages = tm.stage;
+            return MOE_OK;
+        }
     } else if (!q8 || path == 1) {
         const int bm = gemm_tile_m(p.msub);
         RowIdsArgs ra = row_ids_args(ids, n, k, E, B, p.r);

@@ -223,6 +223,38 @@ hipError_t launch_gemm_fp4(const GemmArgs& a, hipStream_t st);
 int64_t gemm_fp4_max_threads(const GemmArgs& a);
 constexpr int kFp4TileM = 128;
 
+// GEMV (decode) path of MXFP4 activations: T * k and S * T slots of at most kDecFp4Slots each.
+constexpr int kDecFp4Slots = 64;
+constexpr int kDecFp4Lds = 128 * 1024;
+struct DecFp4Weights {
+    const uint8_t *q1, *s1;   // codes [n_mat][N][K/2], scale bytes [n_mat][N][K/32]
+    const uint8_t *q2, *s2;   // gate/up mode: up weights
+    int32_t n_mat, N, K;
+};
+struct DecFp4Args {
+    const int32_t* ids;       // [T][k]
+    int32_t T, k, E;
+    DecFp4Weights rw, sw;     // routed, shared (n_mat = 0: none)
+    // activation row of routed slot i = (t, s): t (act_B = 1) or i; of shared expert j, token t:
+    // sact_jstride * j + t. bf16, or float32 (f32)
+    const void* act;
+    int32_t act_B, f32;
+    const void* sact;
+    int64_t sact_jstride;
+    int32_t mode;             // 0 raw, 1 silu(gate) * up
+    float* out;               // routed: [T*k][N]
+    float* sout;              // shared: [n_mat][T][N]
+    // fuse: the weighted sum over each token's slots and the shared experts to out_tok [T][N]
+    // instead (mode 0)
+    int32_t fuse;
+    const float* route_w;
+    float* out_tok;
+    int32_t kp, d_max, xs, rg;   // set by the launcher
+};
+hipError_t launch_decode_fp4(const DecFp4Args& a, hipStream_t st);
+// Whether a weighted call over n = T * k slots, S shared experts and K columns fuses the sum.
+bool decode_fp4_fuses(int64_t n, int64_t E, int64_t S, int64_t K);
+
 // ---------------------------------------------------------------- fp32 grouped matmul (Tiny)
 struct GemmF32Args {
     const float* W;        // [E][N][K]

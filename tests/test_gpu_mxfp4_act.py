@@ -145,16 +145,46 @@ def test_mul_mat_id_grouped(E, k, T, K, N, B_is_k, routing):
     _mul_mat_id(E, k, T, K, N, k if B_is_k else 1, ids, moe.PATH_GEMM)
 
 
-def test_mul_mat_id_wide_scales_and_nan_scale():
+@pytest.mark.parametrize("E,k,T,K,N,B_is_k,routing", [
+    (3, 2, 1, 128, 64, False, "uniform"),    # one token, the shortest rows
+    (32, 4, 1, 2880, 2880, False, "uniform"),# one token, GPT-OSS-shaped
+    (32, 4, 8, 2880, 200, True, "uniform"),  # several slots an expert, K ends inside a superstep
+    (4, 2, 32, 544, 33, False, "uniform"),   # 64 slots, up to 32 of one expert, odd N
+    (1, 1, 64, 160, 17, False, "uniform"),   # 64 slots of one expert
+    (1, 2, 31, 192, 5, True, "repeat"),      # the same expert in both slots
+    (2, 1, 3, 16416, 16, False, "uniform"),  # several rounds of two supersteps a wave
+    (16, 4, 5, 4096, 48, False, "bad"),
+    (256, 8, 2, 7168, 40, False, "uniform"), # wide rows
+    (1000, 7, 9, 1056, 16, False, "uniform"),
+    (8, 2, 9, 128, 64, False, "none"),       # every id invalid
+])
+def test_mul_mat_id_gemv(E, k, T, K, N, B_is_k, routing):
+    rng = np.random.default_rng(T * 31 + E)
+    if routing == "repeat":
+        ids = rng.integers(0, E, size=(T, k)).astype(np.int32)
+    elif routing == "none":
+        ids = np.full((T, k), -1, np.int32)
+        ids[3] = E
+    else:
+        ids = synth.draw_ids_uniform(3, T, E, k)
+    if routing == "bad":
+        ids[0, 0], ids[T - 1, k - 1] = -1, E + 2
+        ids[2] = -7
+    _mul_mat_id(E, k, T, K, N, k if B_is_k else 1, ids, moe.PATH_GEMV)
+    assert moe.last_stage_count() == 1      # unweighted: one launch
+
+
+@pytest.mark.parametrize("path", [moe.PATH_GEMM, moe.PATH_GEMV])
+def test_mul_mat_id_wide_scales_and_nan_scale(path):
     """Scales over most of the E8M0 range and a NaN scale in one expert row."""
-    ids = synth.draw_ids_uniform(4, 40, 4, 2)
-    _mul_mat_id(4, 2, 40, 256, 96, 1, ids, moe.PATH_GEMM, lo=60, hi=190)
+    ids = synth.draw_ids_uniform(4, 30, 4, 2)
+    _mul_mat_id(4, 2, 30, 256, 96, 1, ids, path, lo=60, hi=190)
     codes, scales, _ = _experts(4, 96, 256, 9)
     scales[2, 17, 3] = 255
     w = ref64.decode(ref64.unpack(codes), scales)
-    dx, x = _act(40, 256, 2)
+    dx, x = _act(30, 256, 2)
     dx[11, 70] = float("inf")
-    got = moe.moe_mul_mat_id(_upload(codes, scales), dx, dev_i32(ids), act_quant=2).cpu().numpy()
+    got = moe.moe_mul_mat_id(_upload(codes, scales), dx, dev_i32(ids), act_quant=2, path=path).cpu().numpy()
     ref, _ = ref64.mul_mat_id(ref64.decode(*ref64.quantize(dx.double().cpu().numpy())), w, ids)
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     assert np.isnan(ref[11]).all() and np.isnan(ref).mean() < 0.2
@@ -200,13 +230,45 @@ def test_ffn(E, k, T, n_embd, n_ff, S, routing):
     if routing == "bad":
         ids[0, 0], ids[5] = -1, E
     _ffn_case(E, k, T, n_embd, n_ff, S, ids, path=moe.PATH_GEMM)
-    assert moe.last_stage_count() >= 4
+    assert moe.last_stage_count() == 5      # row ids, quantize x, gate/up, down, reduce
 
 
-def test_router_layer_and_graph():
-    """Scored routing (one padding token) into the FFN on MXFP4 activations, with experts quantized
-    here: eager, the no-allocation call and five replays of a captured graph give the same bytes."""
-    E, k, T, n_embd, n_ff = 16, 4, 40, 128, 96
+@pytest.mark.parametrize("E,k,T,n_embd,n_ff,S,routing", [
+    (8, 2, 12, 160, 128, 0, "uniform"),
+    (8, 3, 20, 256, 160, 2, "bad"),
+    (4, 6, 10, 128, 256, 1, "repeat"),
+    (4, 2, 1, 352, 192, 1, "uniform"),
+    (16, 4, 1, 2880, 1440, 0, "uniform"),
+    (3, 1, 64, 544, 128, 1, "uniform"),     # 64 slots and 64 shared rows
+    (6, 2, 3, 128, 192, 3, "none"),         # only the shared experts
+])
+def test_ffn_gemv(E, k, T, n_embd, n_ff, S, routing):
+    ids = np.random.default_rng(T * 31 + E).integers(0, E, size=(T, k)).astype(np.int32)
+    if routing == "bad":
+        ids[0, 0], ids[5] = -1, E
+    if routing == "none":
+        ids[:] = -1
+    got, *rest = _ffn_case(E, k, T, n_embd, n_ff, S, ids, path=moe.PATH_GEMV)
+    assert moe.last_stage_count() in (2, 3)     # gate/up, down with the sum, or the reduce behind it
+    again = _ffn_case(E, k, T, n_embd, n_ff, S, ids, path=moe.PATH_GEMV)[0]
+    assert torch.equal(got, again)
+
+
+def test_narrow_rows_take_the_grouped_gemm():
+    """Rows under 128 columns: the automatic choice is the grouped GEMM, the forced GEMV is refused."""
+    ids = synth.draw_ids_uniform(3, 2, 4, 2)
+    _mul_mat_id(4, 2, 2, 96, 40, 1, ids, moe.PATH_AUTO)
+    assert moe.last_stage_count() == 4
+    with pytest.raises(moe.MoeError):
+        _mul_mat_id(4, 2, 2, 96, 40, 1, ids, moe.PATH_GEMV)
+
+
+@pytest.mark.parametrize("T", [40, 9])
+def test_router_layer_and_graph(T):
+    """Scored routing (one padding token) into the FFN on MXFP4 activations (grouped GEMM, and GEMV),
+    with experts quantized here: eager, the no-allocation call and five replays of a captured graph
+    give the same bytes."""
+    E, k, n_embd, n_ff = 16, 4, 128, 160
     g = torch.Generator().manual_seed(3)
     mk = lambda *s: moe.Weights(*moe.moe_quantize_mxfp4((0.1 * torch.randn(s, generator=g)).cuda()))
     gate, up, down = mk(E, n_ff, n_embd), mk(E, n_ff, n_embd), mk(E, n_embd, n_ff)

@@ -103,7 +103,7 @@ def test_mxfp4_act_validation():
     def w(typ=moe.MOE_MXFP4, n_mat=8, rows=64, cols=128, data=FAKE):
         return moe.c_moe_weights(typ, data, FAKE, n_mat, rows, cols)
 
-    def mm(wt=None, path=0, ws=1 << 40, x=FAKE, aq=2, T=16, k=2):
+    def mm(wt=None, path=0, ws=1 << 40, x=FAKE, aq=2, T=64, k=2):
         opt = moe._options(path, act_quant=aq)
         return moe.lib.moe_mul_mat_id(ctypes.byref(wt or w()), x, moe.MOE_BF16, 1, FAKE, T, k, None, FAKE,
                                       ctypes.byref(opt), FAKE, ws, None)
@@ -114,6 +114,11 @@ def test_mxfp4_act_validation():
     assert mm(aq=3) == moe.MOE_EINVAL
     assert mm(aq=-1) == moe.MOE_EINVAL
     assert mm(path=7) == moe.MOE_EINVAL
+    assert mm(path=2) == moe.MOE_EINVAL                   # 128 slots: past the GEMV's 64
+    assert "GEMV" in moe.last_error()
+    assert mm(path=2, T=32, x=FAKE + 2) == moe.MOE_EINVAL
+    assert mm(path=2, T=32, wt=w(data=FAKE + 8)) == moe.MOE_EINVAL
+    assert mm(path=2, T=1, wt=w(cols=100)) == moe.MOE_ELIMIT
     assert mm(x=FAKE + 2) == moe.MOE_EINVAL               # activations not 16-byte aligned
     assert mm(wt=w(data=FAKE + 8)) == moe.MOE_EINVAL      # codes not 16-byte aligned
     assert mm(wt=w(cols=100)) == moe.MOE_ELIMIT
@@ -123,11 +128,15 @@ def test_mxfp4_act_validation():
     def ffn(g=g, d=d, ws=16):
         return moe.lib.moe_ffn_fused(ctypes.byref(g), ctypes.byref(g), ctypes.byref(d), None, None, None, FAKE,
                                      moe.MOE_BF16, FAKE, FAKE, 16, 2, FAKE, ctypes.byref(opt), FAKE, ws, None)
-    assert ffn() == moe.MOE_EWORKSPACE
+    assert ffn() == moe.MOE_EWORKSPACE                    # the GEMV path's h
     assert ffn(g=w(moe.MOE_Q8_0), d=w(moe.MOE_Q8_0, rows=128, cols=64)) == moe.MOE_EINVAL
     assert ffn(d=w(rows=128, cols=64, data=FAKE + 4), ws=1 << 40) == moe.MOE_EINVAL
     assert moe.lib.moe_ffn_fused_workspace_size(ctypes.byref(g), None, moe.MOE_BF16, 16, 2, ctypes.byref(opt)) > 0
-    assert moe.moe_select_path_typed(4096, 4, 32, 2880, moe.MOE_MXFP4, act_quant=2) == 4
+    typed = moe.moe_select_path_typed
+    assert typed(4096, 4, 32, 2880, moe.MOE_MXFP4, act_quant=2) == 4
+    assert typed(1, 4, 32, 2880, moe.MOE_MXFP4, act_quant=2) == 5
+    assert typed(1, 4, 32, 2880, moe.MOE_MXFP4, path=moe.PATH_GEMM, act_quant=2) == 4
+    assert typed(16, 4, 32, 2880, moe.MOE_MXFP4, path=moe.PATH_GEMV, act_quant=2) == 5
     for typ in (moe.MOE_Q8_0, moe.MOE_IQ4_XS):
         with pytest.raises(moe.MoeError):
             moe.moe_select_path_typed(4, 4, 32, 2880, typ, act_quant=2)
