@@ -12,6 +12,7 @@ import fails -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -191,9 +192,19 @@ def _options(path: int = PATH_AUTO, tau: float = 0.0, events: Optional[Sequence[
     return o
 
 
+@functools.lru_cache(maxsize=64)
+def _fixed_options(path: int, tau: float, act_quant: int):
+    """_options without events: a struct that the calls only read, made once per set of values."""
+    return _options(path, tau, None, act_quant)
+
+
+def _call_options(path, tau, events, act_quant):
+    return _options(path, tau, events, act_quant) if events else _fixed_options(path, tau, act_quant)
+
+
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # torch's current stream, without building its Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
@@ -240,7 +251,7 @@ def _keep_alive(stream, *tensors):
 def _check_device(stream, *tensors):
     """The kernels run on the stream's device (the current one's without a stream): tensors of
     another device are refused, as a launch there would read the wrong memory."""
-    dev = torch.cuda.current_device() if stream is None else stream.device.index
+    dev = torch._C._cuda_getDevice() if stream is None else stream.device.index
     for t in tensors:
         if t is not None and t.device.index != dev:
             raise ValueError("tensors on %s, but the stream runs on cuda:%d" % (t.device, dev))
@@ -359,7 +370,9 @@ def moe_quantize_mxfp4(x: torch.Tensor, return_values: bool = False, stream=None
     return (codes, scales, values) if return_values else (codes, scales)
 
 
+@functools.lru_cache(maxsize=64)
 def _router_config(score, n_group, topk_group, group_top, renorm, scale) -> c_moe_router_config:
+    """The struct for these values (the calls only read it)."""
     if score not in SCORES:
         raise ValueError("score must be one of %s (got %r)" % (", ".join(sorted(SCORES)), score))
     return c_moe_router_config(SCORES[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
@@ -375,7 +388,7 @@ def _check_logits(logits: torch.Tensor, stream) -> int:
 
 
 def _check_tensor(t: torch.Tensor, name: str, dtype, shape, device):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s of shape %s on %s (got %s of shape %s on %s)"
                          % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
@@ -401,18 +414,20 @@ def moe_router_scored(logits: torch.Tensor, n_used: int, bias: Optional[torch.Te
     if ids is None:
         ids = torch.empty((T, n_used), dtype=torch.int32, device=dev)
         made.append(ids)
+    else:
+        _check_tensor(ids, "ids", torch.int32, (T, n_used), dev)
     if route_w is None:
         route_w = torch.empty((T, n_used), dtype=torch.float32, device=dev)
         made.append(route_w)
-    if scores is None and return_scores:
-        scores = torch.empty((T, E), dtype=torch.float32, device=dev)
-        made.append(scores)
-    if made:
-        _keep_alive(stream, *made)
-    _check_tensor(ids, "ids", torch.int32, (T, n_used), dev)
-    _check_tensor(route_w, "route_w", torch.float32, (T, n_used), dev)
+    else:
+        _check_tensor(route_w, "route_w", torch.float32, (T, n_used), dev)
     if scores is not None:
         _check_tensor(scores, "scores", torch.float32, (T, E), dev)
+    elif return_scores:
+        scores = torch.empty((T, E), dtype=torch.float32, device=dev)
+        made.append(scores)
+    if made and stream is not None:
+        _keep_alive(stream, *made)
     _check(lib.moe_router_scored(logits.data_ptr(), st, None if bias is None else bias.data_ptr(), T, E,
                                  n_used, ctypes.byref(cfg), ids.data_ptr(), route_w.data_ptr(),
                                  None if scores is None else scores.data_ptr(), _stream(stream)),
@@ -441,7 +456,8 @@ def moe_router_scored_backward(logits: torch.Tensor, ids: torch.Tensor, d_route_
     if out is None:
         out = torch.empty_like(logits)
         _keep_alive(stream, out)
-    _check_tensor(out, "out", logits.dtype, (T, E), dev)
+    else:
+        _check_tensor(out, "out", logits.dtype, (T, E), dev)
     _check(lib.moe_router_scored_backward(logits.data_ptr(), st, ids.data_ptr(), d_route_w.data_ptr(),
                                           None if d_scores is None else d_scores.data_ptr(), stride, T, E,
                                           ids.shape[1], ctypes.byref(cfg), out.data_ptr(), _stream(stream)),
@@ -505,15 +521,16 @@ def moe_mul_mat_id(w: Weights, src1: torch.Tensor, ids: torch.Tensor,
         out = torch.empty(shape, dtype=torch.float32, device=ids.device)
         _keep_alive(stream, out)
     st = _xtype(src1)
-    opt = _options(path, tau, events, act_quant)
+    opt = _call_options(path, tau, events, act_quant)
     need = lib.moe_mul_mat_id_workspace_size(ctypes.byref(cw), st, src1_rows_per_token, T, k,
                                              ctypes.byref(opt))
-    ws = _workspace(need, ids.device, workspace, stream)
+    ws = _workspace(need, ids.device, workspace, stream) if need else None
     _check(lib.moe_mul_mat_id(ctypes.byref(cw), src1.data_ptr(), st, src1_rows_per_token,
                               ids.data_ptr(), T, k,
                               None if route_w is None else route_w.data_ptr(), out.data_ptr(),
-                              ctypes.byref(opt), ws.data_ptr(), ws.numel() * ws.element_size(),
-                              _stream(stream)), "moe_mul_mat_id")
+                              ctypes.byref(opt), None if ws is None else ws.data_ptr(),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_mul_mat_id")
     return out
 
 
@@ -546,7 +563,7 @@ def moe_ffn_fused(gate: Weights, up: Weights, down: Weights, x: torch.Tensor, id
     if out is None:
         out = torch.empty((T, cg.cols), dtype=torch.float32, device=x.device)
         _keep_alive(stream, out)
-    opt = _options(path, tau, events, act_quant)
+    opt = _call_options(path, tau, events, act_quant)
     need = lib.moe_ffn_fused_workspace_size(ctypes.byref(cg),
                                             ctypes.byref(cs[0]) if cs[0] is not None else None,
                                             MOE_BF16, T, k, ctypes.byref(opt))
@@ -578,7 +595,7 @@ def moe_ffn_fused_noalloc(gate: Weights, up: Weights, down: Weights, x: torch.Te
     if out is None:
         out = torch.empty((T, cg.cols), dtype=torch.float32, device=x.device)
         _keep_alive(stream, out)
-    opt = _options(path, tau, events, act_quant)
+    opt = _call_options(path, tau, events, act_quant)
     ref = [ctypes.byref(c) if c is not None else None for c in cs]
     _check(lib.moe_ffn_fused_noalloc(ctypes.byref(cg), ctypes.byref(cu), ctypes.byref(cd), ref[0], ref[1],
                                      ref[2], x.data_ptr(), _xtype(x), ids.data_ptr(), route_w.data_ptr(),
