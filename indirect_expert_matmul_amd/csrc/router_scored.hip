@@ -18,8 +18,8 @@
 //       - without a bias the order is that of the logits, which is exact as it stands, and
 //         renormalised weights need the picks' exponentials only.
 //   * k_router_scored (all other sizes, and the function the first one falls back on): one
-//     wave a token, lane l holds experts l, l + 64, ..., float64 throughout, k rounds of a
-//     wave maximum over 64-bit keys.
+//     wave a token, lane l takes experts l, l + 64, ..., float64 throughout, the choices'
+//     64-bit keys in LDS, k rounds of a wave maximum.
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -49,16 +49,41 @@ __device__ __forceinline__ double row_ror(double v) {
     const uint32_t lo = (uint32_t)row_ror<N>((int)(uint32_t)u), hi = (uint32_t)row_ror<N>((int)(uint32_t)(u >> 32));
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-// Reductions over the wave: row rotations inside 16 lanes, then the LDS crossbar for the two
-// steps across them.
+// The lanes' values exchanged across the rows of 16: one result has those of the even rows (half
+// 0) in both rows of a pair (both halves of the wave), the other those of the odd ones (half 1).
+struct Pair {
+    uint32_t x, y;
+};
+template <int ROWS>
+__device__ __forceinline__ Pair across(uint32_t v) {
+    if constexpr (ROWS == 1) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return {r[0], r[1]};
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return {r[0], r[1]};
+    }
+}
+template <int ROWS, class F>
+__device__ __forceinline__ float across(float v, F f) {
+    const Pair p = across<ROWS>(__float_as_uint(v));
+    return f(__uint_as_float(p.x), __uint_as_float(p.y));
+}
+template <int ROWS, class F>
+__device__ __forceinline__ double across(double v, F f) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const Pair lo = across<ROWS>((uint32_t)u), hi = across<ROWS>((uint32_t)(u >> 32));
+    return f(__builtin_bit_cast(double, ((uint64_t)hi.x << 32) | lo.x), __builtin_bit_cast(double, ((uint64_t)hi.y << 32) | lo.y));
+}
+// Reductions over the wave, the same bits in every lane; no LDS.
 template <class V, class F>
 __device__ __forceinline__ V wave_reduce(V v, F f) {
     v = f(v, row_ror<8>(v));
     v = f(v, row_ror<4>(v));
     v = f(v, row_ror<2>(v));
     v = f(v, row_ror<1>(v));
-    v = f(v, __shfl_xor(v, 16));
-    return f(v, __shfl_xor(v, 32));
+    v = across<1>(v, f);
+    return across<2>(v, f);
 }
 template <class V>
 __device__ __forceinline__ V wave_sum(V v) {
@@ -69,22 +94,30 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 // Largest key of the wave and the lowest index that holds it.
 __device__ __forceinline__ void wave_best(uint64_t& key, int& idx) {
-    auto take = [&](uint64_t k2, int i2) {
-        const bool t = k2 > key || (k2 == key && i2 < idx);
-        key = t ? k2 : key;
-        idx = t ? i2 : idx;
-    };
+    auto better = [](uint64_t k1, int i1, uint64_t k2, int i2) { return k2 > k1 || (k2 == k1 && i2 < i1); };
     auto rotated = [&](auto n) {
         constexpr int N = decltype(n)::value;
         const uint32_t lo = (uint32_t)row_ror<N>((int)(uint32_t)key), hi = (uint32_t)row_ror<N>((int)(uint32_t)(key >> 32));
-        take(((uint64_t)hi << 32) | lo, row_ror<N>(idx));
+        const uint64_t k2 = ((uint64_t)hi << 32) | lo;
+        const int i2 = row_ror<N>(idx);
+        const bool t = better(key, idx, k2, i2);
+        key = t ? k2 : key;
+        idx = t ? i2 : idx;
+    };
+    auto crossed = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        const Pair lo = across<N>((uint32_t)key), hi = across<N>((uint32_t)(key >> 32)), i = across<N>((uint32_t)idx);
+        const uint64_t k1 = ((uint64_t)hi.x << 32) | lo.x, k2 = ((uint64_t)hi.y << 32) | lo.y;
+        const bool t = better(k1, (int)i.x, k2, (int)i.y);
+        key = t ? k2 : k1;
+        idx = t ? (int)i.y : (int)i.x;
     };
     rotated(std::integral_constant<int, 8>{});
     rotated(std::integral_constant<int, 4>{});
     rotated(std::integral_constant<int, 2>{});
     rotated(std::integral_constant<int, 1>{});
-    take(__shfl_xor((unsigned long long)key, 16), __shfl_xor(idx, 16));
-    take(__shfl_xor((unsigned long long)key, 32), __shfl_xor(idx, 32));
+    crossed(std::integral_constant<int, 1>{});
+    crossed(std::integral_constant<int, 2>{});
 }
 // Order key of a choice: larger numbers give larger keys, -0 counts as +0; NaN and -inf
 // give 0 (never picked).
@@ -101,67 +134,62 @@ __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i)
     return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
 
+// LDS words of route_wave beside the keys: groups, then picks.
+__host__ __device__ __forceinline__ int route_extra(const RouterScoredArgs& a) {
+    const int p = (a.k + 1) / 2;
+    return a.n_group > p ? a.n_group : p;
+}
+
 // Ratio of the sigmoids of l and of lmax >= l, without overflow or 0 / 0.
 __device__ __forceinline__ float sigmoid_ratio(float l, float lmax) {
     if (lmax > 0.f) return (1.f + expf(-lmax)) / (1.f + expf(-l));
     return expf(l - lmax) * ((1.f + expf(lmax)) / (1.f + expf(l)));
 }
 
-// Routes token t with one wave, in float64. s_key, s_grp: E and n_group words of LDS of this wave's own.
-template <int NC>
-__device__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key, uint64_t* s_grp) {
+// Routes token t with one wave, in float64. s_key: E words of LDS of this wave's own, s_grp:
+// max(n_group, (k + 1) / 2) more. Loops over a lane's experts stay loops: as the fallback of
+// k_route_rows this runs rarely and from a cold instruction cache, where 14 KB of unrolled code
+// made the last wave of a launch 11 us late.
+__device__ __forceinline__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key, uint64_t* s_grp) {
     const int lane = threadIdx.x & 63;
     const int E = a.E, k = a.k, per = E / a.n_group;
-    float l[NC];   // NaN taken as -inf
+    auto logit = [&](int e) -> float {   // NaN taken as -inf
+        const float x = load_logit(a.logits, a.bf16, t * E + e);
+        return x != x ? -INFINITY : x;
+    };
     float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < NC; c++) {
-        const int e = lane + 64 * c;
-        const float x = e < E ? load_logit(a.logits, a.bf16, t * E + e) : -INFINITY;
-        l[c] = x != x ? -INFINITY : x;
-        top = fmaxf(top, l[c]);
+#pragma unroll 4
+    for (int e = lane; e < E; e += 64) {   // the logits wait in the keys' places
+        const float l = logit(e);
+        s_key[e] = __float_as_uint(l);
+        top = fmaxf(top, l);
     }
     top = wave_max(top);
     const bool none = top == -INFINITY, inf = top == INFINITY;
-    // scores: softmax as exp(l - top) / den; infinite logits share the sum
-    double den = 0;
-    double s[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c++) {
-        if (a.sigmoid) s[c] = 1.0 / (1.0 + exp(-(double)l[c]));
-        else s[c] = none ? 0.0 : inf ? (l[c] == INFINITY ? 1.0 : 0.0) : exp((double)l[c] - (double)top);
-        den += s[c];
+    // softmax as exp(l - top) / den; infinite logits share the sum
+    double den = 1.0;
+    auto score = [&](float l) -> double {
+        if (a.sigmoid) return 1.0 / (1.0 + exp(-(double)l));
+        return (none ? 0.0 : inf ? (l == INFINITY ? 1.0 : 0.0) : exp((double)l - (double)top)) / den;
+    };
+    if (!a.sigmoid && !none) {
+        double sum = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) sum += score(__uint_as_float((uint32_t)s_key[e]));
+        den = wave_sum(sum);
     }
-    if (!a.sigmoid) {
-        den = wave_sum(den);
-#pragma unroll
-        for (int c = 0; c < NC; c++) s[c] = none ? 0.0 : s[c] / den;
+    const bool grouped = a.topk_group < a.n_group;
+    // sums of scores rank the groups, while the experts' order without a bias is that of the logits
+    const bool two_orders = grouped && a.group_top == 2 && !a.bias;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+        const float l = __uint_as_float((uint32_t)s_key[e]);
+        const double s = a.bias || two_orders || a.scores ? score(l) : 0.0;
+        if (a.scores) a.scores[t * E + e] = (float)s;
+        s_key[e] = !(l > -INFINITY) ? 0 : order_key(a.bias ? s + (double)a.bias[e] : two_orders ? s : (double)l);
     }
-    if (a.scores) {
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-            const int e = lane + 64 * c;
-            if (e < E) a.scores[t * E + e] = (float)s[c];
-        }
-    }
-    uint64_t key[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c++) {
-        const int e = lane + 64 * c;
-        key[c] = 0;
-        if (e < E && l[c] > -INFINITY) key[c] = order_key(a.bias ? s[c] + (double)a.bias[e] : (double)l[c]);
-    }
-    if (a.topk_group < a.n_group) {
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-            if (lane + 64 * c < E) s_key[lane + 64 * c] = key[c];
-        if (a.group_top == 2 && !a.bias) {   // sums are of scores, not of logits
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int c = 0; c < NC; c++)
-                if (lane + 64 * c < E) s_key[lane + 64 * c] = key[c] ? order_key(s[c]) : 0;
-        }
-        __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_wave_barrier();
+    if (grouped) {
         for (int g = lane; g < a.n_group; g += 64) {
             uint64_t b1 = 0, b2 = 0;
 #pragma unroll 4
@@ -177,6 +205,7 @@ __device__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key
         }
         __builtin_amdgcn_wave_barrier();
         // keep the best groups: a kept group's key becomes all ones, which no key is
+#pragma unroll 1
         for (int r = 0; r < a.topk_group; r++) {
             uint64_t bk = 0;
             int bi = 0x7fffffff;
@@ -189,79 +218,69 @@ __device__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key
             }
             wave_best(bk, bi);
             if (bk && lane == (bi & 63)) s_grp[bi] = ~0ull;
+            __builtin_amdgcn_wave_barrier();
+        }
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) {
+            if (s_grp[e / per] != ~0ull) {
+                s_key[e] = 0;
+            } else if (two_orders) {
+                const float l = logit(e);
+                s_key[e] = l > -INFINITY ? order_key((double)l) : 0;
+            }
         }
         __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-            const int e = lane + 64 * c;
-            if (e < E && s_grp[e / per] != ~0ull) key[c] = 0;
-        }
     }
-    // picks: round r's logit and score are parked in lane r % 64 of slot r / 64
-    float pl[NC];
-    float ps[NC];
-#pragma unroll
-    for (int c = 0; c < NC; c++) {
-        pl[c] = -INFINITY;
-        ps[c] = 0.f;
-    }
+    int* s_pick = (int*)s_grp;
+#pragma unroll 1
     for (int r = 0; r < k; r++) {
         uint64_t bk = 0;
         int bi = 0x7fffffff;
-        float bl = -INFINITY, bs = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-            if (key[c] > bk) {
-                bk = key[c];
-                bi = lane + 64 * c;
-                bl = l[c];
-                bs = (float)s[c];
-            }
+#pragma unroll 4
+        for (int e = lane; e < E; e += 64) {
+            const uint64_t v = s_key[e];
+            bi = v > bk ? e : bi;
+            bk = v > bk ? v : bk;
+        }
         wave_best(bk, bi);
-        const int own = bi & 63;
-        const float vl = __shfl(bl, own), vs = __shfl(bs, own);
-        if (bk) {
-#pragma unroll
-            for (int c = 0; c < NC; c++)
-                if (bi == lane + 64 * c) key[c] = 0;
+        if (bk && lane == (bi & 63)) s_key[bi] = 0;
+        if (lane == 0) {
+            s_pick[r] = bk ? bi : -1;
+            a.ids[t * k + r] = bk ? bi : -1;
         }
-        if (lane == 0) a.ids[t * k + r] = bk ? bi : -1;
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-            if (bk && lane + 64 * c == r) {
-                pl[c] = vl;
-                ps[c] = vs;
-            }
+        __builtin_amdgcn_wave_barrier();
     }
+    // weights: renormalised ones from the logits, without 0 / 0
+    float m = -INFINITY, sum = 0.f;
+    auto weight = [&](int j) -> float {
+        const int e = s_pick[j];
+        if (e < 0) return 0.f;
+        const float l = logit(e);
+        if (!a.renorm) return (float)score(l);
+        if (m == INFINITY && !a.sigmoid) return l == m ? 1.f : 0.f;
+        return a.sigmoid ? sigmoid_ratio(l, m) : expf(l - m);
+    };
     if (a.renorm) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NC; c++) m = fmaxf(m, pl[c]);
+#pragma unroll 1
+        for (int j = lane; j < k; j += 64) m = fmaxf(m, s_pick[j] < 0 ? -INFINITY : logit(s_pick[j]));
         m = wave_max(m);
-        float sum = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-            if (!(pl[c] > -INFINITY)) ps[c] = 0.f;
-            else if (m == INFINITY && !a.sigmoid) ps[c] = pl[c] == m ? 1.f : 0.f;
-            else ps[c] = a.sigmoid ? sigmoid_ratio(pl[c], m) : expf(pl[c] - m);
-            sum += ps[c];
-        }
+#pragma unroll 1
+        for (int j = lane; j < k; j += 64) sum += weight(j);
         sum = wave_sum(sum);
-#pragma unroll
-        for (int c = 0; c < NC; c++) ps[c] = sum > 0.f ? ps[c] / sum : 0.f;
     }
-#pragma unroll
-    for (int c = 0; c < NC; c++)
-        if (lane + 64 * c < k) a.w[t * k + lane + 64 * c] = a.scale * ps[c];
+#pragma unroll 1
+    for (int j = lane; j < k; j += 64) {
+        const float w = weight(j);
+        a.w[t * k + j] = a.scale * (!a.renorm ? w : sum > 0.f ? w / sum : 0.f);
+    }
 }
 
-template <int NC>
 __global__ __launch_bounds__(64 * kWaves) void k_router_scored(RouterScoredArgs a) {
-    __shared__ uint64_t s_key[kWaves][64 * NC];
-    __shared__ uint64_t s_grp[kWaves][64 * NC];
+    extern __shared__ uint64_t s_dyn[];
     const int wv = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kWaves + wv;
-    if (t < a.T) route_wave<NC>(a, t, s_key[wv], s_grp[wv]);
+    uint64_t* mine = s_dyn + wv * (a.E + route_extra(a));
+    if (t < a.T) route_wave(a, t, mine, mine + a.E);
 }
 
 // ---------------------------------------------------------------- 16 lanes a token
@@ -320,10 +339,12 @@ __device__ __forceinline__ void sort_desc(double (&v)[C]) {
 // C: experts of a lane (a multiple of 4); KL: picks a call may take.
 template <int C, int KL>
 __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) {
-    constexpr int Q = C / 4, NC = (C * 16 + 63) / 64;
+    constexpr int Q = C / 4;
     constexpr int LIST = C < KL + 1 ? C : KL + 1;
-    // choices of the wave's tokens (float32, rows of 16 C + 4), or the fallback's keys and groups
-    __shared__ uint64_t s_mem[kWaves][(4 * (16 * C + 4) + 1) / 2 > 64 * NC + 16 ? (4 * (16 * C + 4) + 1) / 2 : 64 * NC + 16];
+    // choices of the wave's tokens (float32, four rows of 16 C + 4), or the fallback's keys and groups
+    // (at most 16 C + 16 words: kRowGroups)
+    static_assert(16 * C + kRowGroups <= 2 * (16 * C + 4), "room for the fallback");
+    __shared__ uint64_t s_mem[kWaves][2 * (16 * C + 4)];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, r = lane & 15, row = lane >> 4;
     const int64_t t0 = ((int64_t)blockIdx.x * kWaves + wv) * 4;
     if (t0 >= a.T) return;
@@ -553,7 +574,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
         const int which = __builtin_ctzll(again) >> 4;
         again &= ~(0xffffull << (16 * which));
         __builtin_amdgcn_wave_barrier();
-        route_wave<NC>(a, t0 + which, s_mem[wv], s_mem[wv] + 64 * NC);
+        route_wave(a, t0 + which, s_mem[wv], s_mem[wv] + E);
     }
 }
 
@@ -913,9 +934,9 @@ hipError_t launch_router_scored(const RouterScoredArgs& a, hipStream_t st) {
         if (a.E <= 256) return launch_rows<16>(a, st);
         return launch_rows<32>(a, st);
     }
-    return by_width(a, [&](auto nc, unsigned grid) {
-        k_router_scored<decltype(nc)::value><<<grid, 64 * kWaves, 0, st>>>(a);
-    });
+    const size_t lds = (size_t)kWaves * (a.E + route_extra(a)) * 8;   // 64 KB at most
+    k_router_scored<<<(unsigned)((a.T + kWaves - 1) / kWaves), 64 * kWaves, lds, st>>>(a);
+    return hipGetLastError();
 }
 
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t st) {
