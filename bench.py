@@ -34,6 +34,7 @@ sys.path.insert(0, ROOT)
 HBM_PEAK_GBS = 8000.0       # MI355X HBM3E
 BF16_PEAK_TFLOPS = 2500.0   # MI355X dense bf16 MFMA
 INT8_PEAK_TOPS = 5000.0     # MI355X dense int8 MFMA (the quantized-activation path)
+FP4_PEAK_TFLOPS = 10000.0   # MI355X dense FP4 MFMA (MXFP4 activations)
 Q8_BYTES = 34.0 / 32.0      # Q8_0: 32 int8 + one fp16 scale per 32 weights
 MXFP4_BYTES = 17.0 / 32.0   # MXFP4: 32 four-bit codes + one E8M0 scale byte per 32 weights
 IQ4NL_BYTES = 18.0 / 32.0   # IQ4_NL: 32 four-bit codes + one fp16 scale per 32 weights
@@ -41,7 +42,9 @@ IQ4XS_BYTES = 136.0 / 256.0  # IQ4_XS: 256 four-bit codes + one 8-byte record pe
 
 STAGES = {1: ["row_ids", "gemm_gate_up", "gemm_down", "reduce"],
           2: ["gemv_gate_up", "gemv_down", "reduce"],
-          3: ["row_ids", "quant_x", "gemm_gate_up", "quant_h", "gemm_down", "reduce"]}
+          3: ["row_ids", "quant_x", "gemm_gate_up", "quant_h", "gemm_down", "reduce"],
+          4: ["row_ids", "quant_x", "gemm_gate_up", "gemm_down", "reduce"],
+          5: ["gemv_gate_up", "gemv_down", "reduce"]}
 
 
 def parse():
@@ -57,7 +60,8 @@ def parse():
     p.add_argument("--rotate", type=int, default=0, help="weight copies (0 = auto)")
     p.add_argument("--path", type=int, default=0, help="0 auto, 1 GEMM, 2 GEMV")
     p.add_argument("--act-quant", type=int, default=0,
-                   help="1: quantized activations (int8 MFMA grouped GEMM, Q8_0 experts)")
+                   help="1: quantized activations (int8 MFMA grouped GEMM, Q8_0 experts); "
+                        "2: MXFP4 activations (FP4 MFMA, MXFP4 experts)")
     p.add_argument("--no-cpu", action="store_true", help="skip the CPU oracle baseline")
     p.add_argument("--graph", type=int, default=0,
                    help="1: time replays of one HIP graph per weight copy (each graph holds one "
@@ -391,7 +395,7 @@ def prepare_ffn_workload(args, name):
     aq = args.act_quant
     path = moe.moe_select_path_typed(T, k, cfg.n_experts, max(cfg.n_embd, cfg.n_ff), wtype,
                                      path=args.path, act_quant=aq)
-    st = workload_stats(inp, cfg, 4 if path == 2 else 2)
+    st = workload_stats(inp, cfg, 4 if path in (2, 5) else 17 / 32 if path == 4 else 2)
     R = args.rotate or (1 if st["bytes"] > 2e9 else max(4, int(np.ceil(1.2e9 / st["bytes"]))))
     sets = []
     base = [up(inp[n + "_qs"], inp[n + "_d"]) for n in ("gate", "up", "down")]
@@ -495,14 +499,16 @@ def finish_ffn_workload(raw):
     dom = max(stage_ms, key=stage_ms.get)
     kern = {"gemm_gate_up": "gate_up", "gemv_gate_up": "gate_up", "gemm_down": "down",
             "gemv_down": "down", "gemv_down_reduce": "down_reduce", "reduce": "reduce"}.get(dom)
-    mfma_bound = path in (1, 3) and st["flops"] / (BF16_PEAK_TFLOPS * 1e12) > st["bytes"] / (HBM_PEAK_GBS * 1e9)
+    peak = {3: INT8_PEAK_TOPS, 4: FP4_PEAK_TFLOPS}.get(path, BF16_PEAK_TFLOPS)
+    ridge = FP4_PEAK_TFLOPS if path == 4 else BF16_PEAK_TFLOPS
+    mfma_bound = path in (1, 3, 4) and st["flops"] / (ridge * 1e12) > st["bytes"] / (HBM_PEAK_GBS * 1e9)
     traffic = measured_traffic(name, dom)
     if kern is None:
         roof = {"bound": "hbm", "achieved": None, "peak": HBM_PEAK_GBS, "unit": "GB/s",
                 "frac": None, "traffic": None, "kernel": dom}
     elif mfma_bound:
         a = st[kern]["flops"] / (stage_ms[dom] * 1e-3) / 1e12
-        pk, unit = (INT8_PEAK_TOPS, "TOP/s") if path == 3 else (BF16_PEAK_TFLOPS, "TFLOP/s")
+        pk, unit = peak, "TOP/s" if path == 3 else "TFLOP/s"
         roof = {"bound": "mfma", "achieved": a, "peak": pk, "unit": unit,
                 "frac": a / pk, "traffic": traffic, "kernel": dom,
                 "algorithmic_bytes": st[kern]["bytes"], "intermediate_bytes": st[kern]["intermediate_bytes"]}
@@ -514,13 +520,14 @@ def finish_ffn_workload(raw):
 
     res = {
         "workload": cfg.desc, "name": name, "n_tokens": T,
-        "path": {1: "gemm", 2: "gemv", 3: "gemm, int8 activations"}[path],
+        "path": {1: "gemm", 2: "gemv", 3: "gemm, int8 activations", 4: "gemm, MXFP4 activations",
+                 5: "gemv, MXFP4 activations"}[path],
         "weight_copies": R, "steps": steps, "warmup": warmup, "ms_per_step": ms,
         "tokens_per_s": T / (ms * 1e-3),
         "tflops": st["flops"] / (ms * 1e-3) / 1e12,
         "gbps": st["bytes"] / (ms * 1e-3) / 1e9,
         "stage_ms": stage_ms, "roofline": roof,
-        "dtype": {1: "bf16", 2: "f32", 3: "int8"}[path],
+        "dtype": {1: "bf16", 2: "f32", 3: "int8", 4: "mxfp4", 5: "mxfp4"}[path],
         "cfg": cfg, "inp": inp, "stats": st, "stream": stream,
     }
     res["cpu_baseline"] = None

@@ -126,8 +126,14 @@ typedef struct {
      * 2: MXFP4 activations (MXFP4 experts only): activation rows are quantized to MXFP4
      * (moe_quantize_mxfp4's format) and multiplied with the experts' codes by the block
      * scaled FP4 MFMA, fp32 accumulation. The fused FFN quantizes x before gate/up and the
-     * float32 h before down. Kernel order for timing: row ids, quantize, grouped GEMM[, down
-     * grouped GEMM], reduce / fix-up. */
+     * float32 h before down. GEMV path (path 0 takes it where it can be forced): n_tokens *
+     * n_used <= 64, n_tokens * shared experts <= 64, every row at least 128 columns wide;
+     * tau is not read. The two paths add the same products in different orders. x / src1 and
+     * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows of
+     * activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's codes under 4 GiB
+     * (MOE_ELIMIT). Kernel order for timing: row ids, quantize, grouped GEMM[, down grouped
+     * GEMM], reduce / fix-up; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
+     * weighted calls too large to sum inside the GEMV. */
     int32_t act_quant;
     int32_t reserved[5];
     void *const *timing_events;
@@ -390,8 +396,10 @@ int32_t moe_select_path(int64_t n_tokens, int32_t n_used, int32_t n_experts, int
 
 /* The path moe_mul_mat_id / moe_ffn_fused take for experts of weight_type (MOE_Q8_0,
  * MOE_MXFP4, MOE_IQ4_NL or MOE_IQ4_XS) under opt: 1 grouped GEMM, 2 GEMV, 3 the grouped
- * GEMM over quantized activations (opt->act_quant = 1, Q8_0 only), 4 the grouped GEMM over
- * MXFP4 activations (opt->act_quant = 2, MXFP4 only), or a negative moe_status (MOE_EINVAL for other weight types, or for options the call would reject).
+ * GEMM over quantized activations (opt->act_quant = 1, Q8_0 only), 4 the grouped GEMM or 5
+ * the GEMV over MXFP4 activations (opt->act_quant = 2, MXFP4 only; act_width: the narrowest
+ * row, shared experts apart), or a negative moe_status (MOE_EINVAL for other weight types,
+ * or for options the call would reject).
  * Q8_0 gives the same answer as moe_select_path. Pure host function. */
 int32_t moe_select_path_typed(int64_t n_tokens, int32_t n_used, int32_t n_experts, int64_t act_width,
                               moe_dtype weight_type, const moe_options *opt);

@@ -8,8 +8,8 @@
 // each operand, 16 bytes of codes and one scale byte, and sums in float32. (The
 // 16x16x128 form runs at half its rate: 4.8 against 9.5 PFLOP/s from registers.)
 //
-// Block tile: up to 128 activation rows x 128 NT weight rows, 4 waves; wave w owns 32 NT
-// weight rows (gate/up mode: 32 gate rows and the 32 up rows of the same outputs) and all
+// Block tile: up to 128 activation rows x 256 weight rows, 4 waves; wave w owns 64 weight
+// rows (gate/up mode: 32 gate rows and the 32 up rows of the same outputs) and all
 // activation rows. A stage is 128 columns, 64 bytes of codes a row.
 //   * Codes go global -> LDS by direct copies into a ring of three slots, two stages
 //     ahead; the gather through the row map is the copies' addresses. Loading the weights
@@ -26,6 +26,16 @@
 //   * Gate/up mode quantizes h in its epilogue, from the float32 accumulators.
 //   * An expert's rows are split into equal tiles (of whole 32-row MFMA columns) rather
 //     than full ones and a rest: a block's time goes with its rows.
+//   * Output rows that no further kernel of the call reads are stored past the caches
+//     (1100 rows x 896: 35 -> 34 us, 32768 x 2048: 482 -> 474); before a weighted sum the
+//     plain stores are better, which leave part of the rows in the caches (sum: 40 against 43).
+//
+// Measured (this kernel alone): 4096 tokens x 8 slots, 128 experts of 2048 x 7168, 474 us, 2030
+// TFLOP/s; 4096 x 4, 32 experts of 2880 x 2880, 189 us, 1440 TFLOP/s. Bound by LDS and the
+// copies into it as much as by the MFMAs: without the copies 307 and 106 us, with the copies
+// and no MFMA 331 and 114. Tried and slower at these two sizes: 128 x 128 tiles 507 and 196;
+// weights from global memory straight into MFMA registers 604 and 210; 256 x 256 tiles with
+// 8 waves 497 and 183; persistent blocks 506 and 185.
 #include <type_traits>
 
 #include "lds_dma.h"
@@ -46,7 +56,12 @@ constexpr int kKS = 128;         // columns per stage
 constexpr int kRow = kKS / 2;    // code bytes of a row per stage
 constexpr int kNS = 3;           // ring slots
 constexpr int kSS = 4;           // stages whose scale bytes are in LDS
-constexpr int kMChunk = 4;       // M tiles sharing each weight slab in turn
+constexpr int kNT = 2;           // 32-row MFMA tiles of weight rows per wave
+constexpr int kBN = 32 * kNT * kW;       // weight rows per block tile
+constexpr int kRows = kBM + kBN;         // rows of a ring slot: activations, weights
+constexpr int kStage = kRows * kRow;     // bytes of a ring slot
+constexpr int kLds = kNS * kStage + kSS * kRows * 4;
+constexpr int kMChunk = 8;       // M tiles sharing each weight slab in turn (4: 195 against 186 us)
 
 __device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 __device__ __forceinline__ int swz(int r) { return (r >> 2) & 3; }
@@ -59,17 +74,11 @@ __device__ __forceinline__ V load_unaligned(const uint8_t* p) {
 }
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int MODE, int NT>
-constexpr int out_cols() { return MODE == 1 ? 64 * NT : 128 * NT; }
-template <int NT>
-constexpr int lds_bytes() { return kNS * (kBM + 128 * NT) * kRow + kSS * (kBM + 128 * NT) * 4; }
+constexpr int out_cols(int mode) { return mode == 1 ? kBN / 2 : kBN; }
 
-template <int MODE, int NT>
+template <int MODE>
 __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
-    constexpr int NTW = out_cols<MODE, NT>();
-    constexpr int BN = 128 * NT;                     // weight rows per block tile
-    constexpr int kRows = kBM + BN;                  // rows of a ring slot: activations, weights
-    constexpr int kStage = kRows * kRow;
+    constexpr int NTW = out_cols(MODE);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     uint32_t* s_scale = (uint32_t*)(smem + kNS * kStage);       // [kSS][kRows]
 
@@ -139,7 +148,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
         return P.a_rows ? (uint32_t)P.a_rows[m0 + j] : (uint32_t)j;
     };
     // ---- copies: copy i of wave w covers rows 16 (w * n + i) .. +15, 4 lanes a row
-    constexpr int CA = kBM / 16 / kW, CW = BN / 16 / kW;   // per wave and stage
+    constexpr int CA = kBM / 16 / kW, CW = kBN / 16 / kW;   // per wave and stage
     constexpr int kCopies = CA + CW;
     const uint32_t KH = (uint32_t)KB * 16, KHp = (uint32_t)fp4_code_row(P.K);
     const int64_t w0 = (int64_t)e * N + wrow(0);
@@ -170,10 +179,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
                   st + kBM * kRow + (wv * CW + i) * 1024);
         }
     };
-    // ---- scale bytes of kSS stages: weight row tid (the first BN threads) and activation row tid
-    const bool has_w = tid < BN, has_a = tid < kBM;
-    const uint8_t* sw = (const uint8_t*)(is_up(tid & (BN - 1)) ? P.d2 : P.d1) +
-                        ((int64_t)e * N + wrow(tid & (BN - 1))) * KB;
+    // ---- scale bytes of kSS stages: weight row tid (the first kBN threads) and activation row tid
+    const bool has_w = tid < kBN, has_a = tid < kBM;
+    const uint8_t* sw = (const uint8_t*)(is_up(tid & (kBN - 1)) ? P.d2 : P.d1) +
+                        ((int64_t)e * N + wrow(tid & (kBN - 1))) * KB;
     const uint8_t* sa = P.As + (act_row0 + act_row(tid & (kBM - 1))) * fp4_scale_row(P.K);
     i32x4 rw, ra;
     // Raw loads only: what depends on the row's end is done when the words are stored. Weight words
@@ -213,23 +222,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
 
     // ---- a wave's operands: MFMA step j of a stage, and the stage's scale words
     struct Frag {
-        i32x4 a[4], w[NT];
+        i32x4 a[4], w[kNT];
     };
     struct Scale {
-        int a[4], w[NT];
+        int a[4], w[kNT];
     };
-    f32x16 acc[4][NT];
+    f32x16 acc[4][kNT];
     auto read = [&](Frag& f, int slot, int j, auto n_c) __attribute__((always_inline)) {
         const uint8_t* st = smem + slot * kStage + (((2 * j + h) ^ swz(l32)) << 4) + l32 * kRow;
 #pragma unroll
-        for (int c = 0; c < NT; c++) f.w[c] = *(const i32x4*)(st + (kBM + wv * 32 * NT + c * 32) * kRow);
+        for (int c = 0; c < kNT; c++) f.w[c] = *(const i32x4*)(st + (kBM + wv * 32 * kNT + c * 32) * kRow);
 #pragma unroll
         for (int i = 0; i < decltype(n_c)::value; i++) f.a[i] = *(const i32x4*)(st + i * 32 * kRow);
     };
     auto read_scale = [&](Scale& v, int s, auto n_c) __attribute__((always_inline)) {
         const uint32_t* sc = s_scale + (s & (kSS - 1)) * kRows + l32;
 #pragma unroll
-        for (int c = 0; c < NT; c++) v.w[c] = (int)(sc[kBM + wv * 32 * NT + c * 32] >> (8 * h));
+        for (int c = 0; c < kNT; c++) v.w[c] = (int)(sc[kBM + wv * 32 * kNT + c * 32] >> (8 * h));
 #pragma unroll
         for (int i = 0; i < decltype(n_c)::value; i++) v.a[i] = (int)(sc[i * 32] >> (8 * h));
     };
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
 #pragma unroll
         for (int i = 0; i < decltype(n_c)::value; i++)
 #pragma unroll
-            for (int c = 0; c < NT; c++) {
+            for (int c = 0; c < kNT; c++) {
                 // gate/up: weights as the row operand, so that a lane holds one activation row's columns
                 if (MODE == 1)
                     acc[i][c] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
@@ -255,7 +264,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int c = 0; c < NT; c++) acc[i][c] = f32x16{};
+            for (int c = 0; c < kNT; c++) acc[i][c] = f32x16{};
         load_scales(0);
         issue(0, 0);
         if (nst > 1) issue(1, 1);
@@ -328,7 +337,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
 #pragma unroll
             for (int v = 0; v < 16; v++) {
                 const float gv = acc[i][0][v];
-                hv[v] = pad ? 0.f : gv / (1.0f + expf(-gv)) * acc[i][NT - 1][v];
+                hv[v] = pad ? 0.f : gv / (1.0f + expf(-gv)) * acc[i][kNT - 1][v];
                 top = max(top, __float_as_uint(hv[v]) & 0x7fffffffu);
             }
             top = max(top, (uint32_t)__shfl_xor((int)top, 32));
@@ -360,8 +369,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
         // this lane's rows are 4 h + constants: one base and one limit for all of them
         const int left = m_len - 4 * h;
         const int32_t* orow_h = s_orow + 4 * h;
-        float* o = (float*)P.out + nt * NTW + wv * 32 * NT + l32;
-        const int n_left = N - (nt * NTW + wv * 32 * NT + l32);
+        float* o = (float*)P.out + nt * NTW + wv * 32 * kNT + l32;
+        const int n_left = N - (nt * NTW + wv * 32 * kNT + l32);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             if (i * 32 >= m_len) continue;
@@ -371,24 +380,26 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_fp4(GemmArgs args) {
                 if (m >= left) continue;
                 float* r = o + orow_h[m] * P.ldo;
 #pragma unroll
-                for (int c = 0; c < NT; c++)
-                    if (32 * c < n_left) r[32 * c] = acc[i][c][v];
+                for (int c = 0; c < kNT; c++)
+                    if (32 * c < n_left) {
+                        if (args.stream_out) __builtin_nontemporal_store(acc[i][c][v], r + 32 * c);
+                        else r[32 * c] = acc[i][c][v];
+                    }
             }
         }
     }
 }
 
-template <int MODE, int NT>
+template <int MODE>
 hipError_t launch(const GemmArgs& a, int64_t total, hipStream_t st) {
-    constexpr int bytes = lds_bytes<NT>();
     static PerDeviceOnce lds_cap;
-    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_gemm_fp4<MODE, NT>, bytes)) return e;
-    k_gemm_fp4<MODE, NT><<<(unsigned)total, kThreads, bytes, st>>>(a);
+    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_gemm_fp4<MODE>, kLds)) return e;
+    k_gemm_fp4<MODE><<<(unsigned)total, kThreads, kLds, st>>>(a);
     return hipGetLastError();
 }
 
 int64_t grid_of(const GemmArgs& a) {
-    const int ntw = a.mode == 1 ? 128 : 128 * a.nt;
+    const int ntw = out_cols(a.mode);
     int64_t total = 0;
     for (int i = 0; i < a.n_prob; i++) {
         const GemmProblem& p = a.p[i];
@@ -405,8 +416,7 @@ hipError_t launch_gemm_fp4(const GemmArgs& a0, hipStream_t st) {
     const int64_t total = grid_of(a);
     if (total <= 0) return hipSuccess;
     a.grid_real = (int32_t)total;
-    if (a.mode == 1) return launch<1, 2>(a, total, st);
-    return a.nt == 2 ? launch<0, 2>(a, total, st) : launch<0, 1>(a, total, st);
+    return a.mode == 1 ? launch<1>(a, total, st) : launch<0>(a, total, st);
 }
 
 int64_t gemm_fp4_max_threads(const GemmArgs& a) { return grid_of(a) * kThreads; }

@@ -165,7 +165,7 @@ int select_path_fmt(int64_t T, int32_t k, int32_t E, int64_t act_width, bool fp4
 // grouped GEMM) or 5 (its GEMV), else the choice above; or a negative status. S: shared
 // experts; min_width: the narrowest activation row.
 int select_path_aq(int64_t T, int32_t k, int32_t E, int64_t act_width, int32_t wtype,
-                   const moe_options* o, int64_t S = 0, int64_t min_width = 1LL << 30) {
+                   const moe_options* o, int64_t S, int64_t min_width) {
     const int32_t aq = o ? o->act_quant : 0;
     if (aq < 0 || aq > 2) return fail(MOE_EINVAL, "options.act_quant must be 0, 1 or 2 (got %d)", aq);
     if (aq == 2) {
@@ -434,8 +434,10 @@ QuantPart qpart(const void* src, int64_t rows, int64_t K, int8_t* q, float* d) {
 // ---------------------------------------------------------------- MXFP4 activations
 constexpr int64_t kFp4MaxBlocks = 1LL << 31;   // 32-column blocks one quantization takes
 
-QuantFp4Part fp4_part(const void* src, int64_t rows, int64_t K, int8_t* q, uint8_t* s) {
-    QuantFp4Part p{};
+// Quantization of a call's bf16 activations into rows as the grouped GEMM reads them.
+QuantFp4Args fp4_act(const void* src, int64_t rows, int64_t K, int8_t* q, uint8_t* s) {
+    QuantFp4Args p{};
+    p.src_bf16 = 1;
     p.src = src;
     p.rows = rows;
     p.K = K;
@@ -521,13 +523,9 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
         return s;
     RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
     fp4_tiles(ra, p.r);
-    QuantFp4Args qx{};
-    qx.src_bf16 = 1;
-    qx.n_part = 1;
-    qx.part[0] = fp4_part(x, d.T, d.n_embd, p.xq, p.xs);
+    const QuantFp4Args qx = fp4_act(x, d.T, d.n_embd, p.xq, p.xs);
     GemmArgs g{}, g2{};
     g.mode = 1;
-    g.nt = g2.nt = 2;
     g.n_prob = g2.n_prob = shared ? 2 : 1;
     g.p[0] = fp4_routed(gate, up, p.r, n, p.xq, p.xs, p.hq);
     g.p[0].out_s = p.hs;
@@ -559,19 +557,17 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
 
 // moe_mul_mat_id up to the per-slot rows: row ids, src1 -> codes, grouped GEMM.
 moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, int32_t B,
-                    const int32_t* ids, int64_t T, int32_t k, float* slot_out, Timer& tm, hipStream_t st) {
+                    const int32_t* ids, int64_t T, int32_t k, float* slot_out, bool weighted, Timer& tm,
+                    hipStream_t st) {
     moe_status s;
     const int64_t n = T * k;
     if ((s = check_fp4_act(src1, "src1")) || (s = check_fp4_weights(w, "w"))) return s;
     RowIdsArgs ra = row_ids_args(ids, n, k, (int32_t)w->n_mat, B, p.r);
     fp4_tiles(ra, p.r);
-    QuantFp4Args qa{};
-    qa.src_bf16 = 1;
-    qa.n_part = 1;
-    qa.part[0] = fp4_part(src1, T * B, w->cols, p.aq, p.as);
+    const QuantFp4Args qa = fp4_act(src1, T * B, w->cols, p.aq, p.as);
     GemmArgs g{};
     g.n_prob = 1;
-    g.nt = 2;
+    g.stream_out = !weighted;
     g.p[0] = fp4_routed(w, nullptr, p.r, n, p.aq, p.as, slot_out);
     g.p[0].a_rows = p.r.ids_src1;
     g.p[0].out_rows = p.r.ids_dst;
@@ -734,7 +730,7 @@ int32_t moe_select_path_typed(int64_t n_tokens, int32_t n_used, int32_t n_expert
     if (weight_type != MOE_Q8_0 && weight_type != MOE_MXFP4 && weight_type != MOE_IQ4_NL &&
         weight_type != MOE_IQ4_XS)
         return fail(MOE_EINVAL, "weight_type must be Q8_0, MXFP4, IQ4_NL or IQ4_XS (got %d)", (int)weight_type);
-    return select_path_aq(n_tokens, n_used, n_experts, act_width, weight_type, opt);
+    return select_path_aq(n_tokens, n_used, n_experts, act_width, weight_type, opt, 0, act_width);
 }
 
 size_t moe_row_ids_workspace_size(int64_t n_tokens, int32_t n_used, int32_t n_experts) {
@@ -1233,7 +1229,7 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
         if ((s = hip_check(launch_gemm_q8a(g, st), "grouped GEMM (int8)"))) return s;
         tm.end();
     } else if (path == 4) {
-        if ((s = mmid_fp4(p, w, src1, B, ids, n_tokens, k, slot_out, tm, st))) return s;
+        if ((s = mmid_fp4(p, w, src1, B, ids, n_tokens, k, slot_out, weighted, tm, st))) return s;
     } else if (path == 5) {
         if ((s = mmid_dec_fp4(p, w, src1, B, ids, n_tokens, k, route_w, slot_out, dst, tm, st))) return s;
         if (p.fuse || !weighted) {   // written in full, rows of invalid slots too
@@ -1373,11 +1369,13 @@ moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_type, int64_t rows, int
     if (rows >= kFp4MaxBlocks || K / 32 >= kFp4MaxBlocks || rows * (K / 32) >= kFp4MaxBlocks)
         return fail(MOE_ELIMIT, "rows * K / 32 must be under 2^31");
     QuantFp4Args a{};
-    a.n_part = 1;
+    a.src = x;
+    a.rows = rows;
+    a.K = K;
+    a.q = codes;
+    a.s = scales;
+    a.values = values;
     a.src_bf16 = x_type == MOE_BF16;
-    a.part[0] = fp4_part(x, rows, K, (int8_t*)codes, scales);
-    a.part[0].values = values;
-    a.part[0].padded = 0;
     return hip_check(launch_quant_mxfp4(a, (hipStream_t)stream), "quantize to MXFP4");
 }
 

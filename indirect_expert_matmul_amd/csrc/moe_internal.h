@@ -140,7 +140,7 @@ struct GemmArgs {
     GemmProblem p[2];
     int32_t n_prob;
     int32_t mode;             // 0: fp32 out = acc; 1: bf16 out = silu(acc_gate) * acc_up
-    int32_t nt;               // MXFP4-activation GEMM: weight rows per wave / 32 (1 or 2; 2 in mode 1)
+    int32_t stream_out;       // MXFP4-activation GEMM, mode 0: no kernel of this call reads out again
     int32_t grid_real;        // blocks carrying tiles (before padding to a multiple of 8)
     // 0: Q8_0 experts; 1: MXFP4 -- qs1/qs2 hold two E2M1 codes per byte ([n_mat][N][K/2],
     // even column in the low nibble), d1/d2 the E8M0 scale bytes ([n_mat][N][K/32]);
@@ -195,7 +195,7 @@ constexpr int kQ8aTileM = 128;
 
 // ---------------------------------------------------------------- MXFP4 activations
 // Rows of 32-column blocks -> E2M1 codes and E8M0 scale bytes (moe_quantize_mxfp4).
-struct QuantFp4Part {
+struct QuantFp4Args {
     const void* src;   // [rows][K], bf16 bits (src_bf16) or float32
     int64_t rows, K;   // K % 32 == 0
     uint8_t* q;        // [rows][K/2]
@@ -204,17 +204,12 @@ struct QuantFp4Part {
     // 1: rows padded as the grouped GEMM reads them: fp4_code_row(K) code bytes (0 past K)
     // and fp4_scale_row(K) scale bytes (scale 1 up to the last code stage)
     int32_t padded;
+    int32_t src_bf16;
 };
 // Bytes of an activation row in the grouped GEMM's operands: codes padded to whole stages of
 // 128 columns, scale bytes to 16 (what one load takes).
 inline __host__ __device__ int64_t fp4_code_row(int64_t K) { return (K + 127) / 128 * 64; }
 inline __host__ __device__ int64_t fp4_scale_row(int64_t K) { return (K / 32 + 15) / 16 * 16; }
-struct QuantFp4Args {
-    QuantFp4Part part[2]; // one launch quantizes up to two tensors
-    int32_t n_part;
-    int32_t src_bf16;
-    int64_t blocks0;   // set by the launcher: thread blocks of part 0
-};
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
 // activations (Aq / As); tile_tab required for routed problems, tile height kFp4TileM.

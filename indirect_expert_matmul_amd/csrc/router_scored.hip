@@ -6,7 +6,7 @@
 //     token, four tokens a wave, so that every reduction is four row rotations and no LDS
 //     crossbar. Choices are float32 first: each is at most kErr from the exact one, so
 //     picks and groups whose neighbours in the order are further apart than twice that are
-//     the exact ones. The rest (about one token in a hundred of random logits) are routed
+//     the exact ones. The rest (about one token in a thousand of random logits) are routed
 //     again in float64 by the whole wave.
 //       - a lane holds chunks of four experts (chunk lane + 16 q), loaded 16 bytes at a time;
 //       - a choice and its expert become one float64 integer, key * 1024 + 1023 - e, whose
@@ -148,8 +148,8 @@ __device__ __forceinline__ float sigmoid_ratio(float l, float lmax) {
 
 // Routes token t with one wave, in float64. s_key: E words of LDS of this wave's own, s_grp:
 // max(n_group, (k + 1) / 2) more. Loops over a lane's experts stay loops: as the fallback of
-// k_route_rows this runs rarely and from a cold instruction cache, where 14 KB of unrolled code
-// made the last wave of a launch 11 us late.
+// k_route_rows this runs rarely and from a cold instruction cache: a launch that needs it for any
+// token ends 11 us later (65536 x 256: 67 against 56 us), so its loops are kept small.
 __device__ __forceinline__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key, uint64_t* s_grp) {
     const int lane = threadIdx.x & 63;
     const int E = a.E, k = a.k, per = E / a.n_group;

@@ -142,6 +142,16 @@ def test_mxfp4_act_validation():
             moe.moe_select_path_typed(4, 4, 32, 2880, typ, act_quant=2)
 
 
+def test_mxfp4_act_path_bounds():
+    def typed(T, k, width, path=moe.PATH_AUTO):
+        return moe.moe_select_path_typed(T, k, 32, width, moe.MOE_MXFP4, path=path, act_quant=2)
+    assert [typed(T, k, 128) for T, k in ((64, 1), (16, 4), (1, 64), (65, 1), (13, 5))] == [5, 5, 5, 4, 4]
+    assert typed(1, 1, 127) == 4 and typed(1, 1, 96) == 4
+    for T, k, width in ((1, 1, 96), (65, 1, 128)):
+        with pytest.raises(moe.MoeError):
+            typed(T, k, width, path=moe.PATH_GEMV)
+
+
 def test_quantize_mxfp4_validation():
     q = moe.lib.moe_quantize_mxfp4
     assert q(FAKE, moe.MOE_BF16, 4, 100, FAKE, FAKE, None, None) == moe.MOE_ELIMIT
