@@ -508,7 +508,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
         kept = (uint32_t)(__ballot(keep) >> (16 * row)) & 0xffffu;
         if (approx || sums) {                // the last one kept and the first one left too near to tell
             const float in = -row_max(keep ? -g : -INFINITY), out = row_max(!keep && r < a.n_group ? g : -INFINITY);
-            const float err = (a.sigmoid ? kErrSigmoid : kErrSoftmax) * 2.f + kErrSum * fabsf(in);
+            // both choices were rounded, and a sum can be far smaller than they are
+            const float size = (b1 > -INFINITY ? fabsf(b1) : 0.f) + (sums && b2 > -INFINITY ? fabsf(b2) : 0.f);
+            const float err = (a.sigmoid ? kErrSigmoid : kErrSoftmax) * 2.f + kErrSum * row_max(size);
             if (out > -INFINITY && !(in - out > err)) doubt = true;
         }
     }
@@ -518,7 +520,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
     for (int c = 0; c < C; c++) {
         const int e = 4 * (r + 16 * (c / 4)) + c % 4;
         uint32_t key = order_key(approx ? v[c] : l[c]);
-        if (grouped && !((kept >> (e / per)) & 1)) key = 0;
+        if (grouped && !((kept >> ((e / per) & 31)) & 1)) key = 0;   // past E: key is 0 as it is
         list[c] = key ? (double)key * 1024.0 + (double)(1023 - e) : 0.0;
     }
     sort_desc(list);

@@ -84,6 +84,19 @@ def test_route_ties_take_the_lower_index(score, bias):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("big", [2.0 ** 12, 2.0 ** 20, 1e30])
+def test_group_sums_that_cancel(score, big):
+    """Large balance biases of both signs: a group's two choices cancel, and the groups' order hangs
+    on what float32 sums have lost. (1e30: on nothing but the group index.)"""
+    T, E, G = 256, 64, 8
+    dev, l = _logits(T, E, 4, spread=2.0)
+    b = np.full(E, -big)
+    b[::E // G] = big
+    for keep in (1, 3):
+        _check_route(dev, l, keep, bias=b, score=score, n_group=G, topk_group=keep)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masks_and_extremes(score):
     nan, inf, low = np.nan, np.inf, np.finfo(np.float32).min
     E = 70
