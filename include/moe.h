@@ -327,7 +327,8 @@ moe_status moe_quantize_mxfp4(const void* x, moe_dtype x_type, int64_t rows, int
  *   bias     NULL or device float32 [n_experts]
  *   ids      device int32 [n_tokens][n_used] (written)
  *   route_w  device float32 [n_tokens][n_used] (written)
- *   scores   NULL or device float32 [n_tokens][n_experts] (written): s, for balance losses
+ *   scores   NULL or device float32 [n_tokens][n_experts] (written): s, for balance losses;
+ *            not in the place of logits (MOE_EINVAL)
  * Requires 1 <= n_used <= topk_group * n_experts / n_group, n_experts <= 1024,
  * n_experts % n_group == 0, 1 <= topk_group <= n_group (MOE_EINVAL / MOE_ELIMIT
  * otherwise), a finite scale, n_tokens < 2^22. No workspace. Deterministic.

@@ -356,7 +356,7 @@ hipError_t launch_decode_fp4(const DecFp4Args& a0, hipStream_t st) {
     a.kp = kp;
     const dim3 grid((unsigned)((n_rows + 16 * a.rg - 1) / (16 * a.rg)), (unsigned)(a.fuse ? 1 : units));
     const size_t lds = lds_of();
-    if (a.mode == 1) return a.f32 ? launch<1, true>(a, grid, waves, lds, st) : launch<1, false>(a, grid, waves, lds, st);
+    if (a.mode == 1) return launch<1, false>(a, grid, waves, lds, st);   // x is bf16
     if (a.fuse) return a.f32 ? launch<0, true, true>(a, grid, waves, lds, st) : launch<0, false, true>(a, grid, waves, lds, st);
     return a.f32 ? launch<0, true>(a, grid, waves, lds, st) : launch<0, false>(a, grid, waves, lds, st);
 }

@@ -1388,6 +1388,8 @@ moe_status moe_router_scored(const void* logits, moe_dtype logits_type, const fl
     if (logits_type != MOE_F32 && logits_type != MOE_BF16) return fail(MOE_EINVAL, "logits must be F32 or BF16");
     if ((s = check_router(cfg, n_tokens, n_experts, n_used, true))) return s;
     if (n_tokens > 0 && (!logits || !ids || !route_w)) return fail(MOE_EINVAL, "NULL pointer argument");
+    if (scores && (const void*)scores == logits)   // logits are read again after the scores
+        return fail(MOE_EINVAL, "scores must not be logits");
     RouterScoredArgs a{};
     a.logits = logits;
     a.bf16 = logits_type == MOE_BF16;

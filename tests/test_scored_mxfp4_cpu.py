@@ -170,14 +170,16 @@ def test_quantize_mxfp4_validation():
 
 
 def test_router_scored_validation():
-    def call(T=4, E=64, k=4, dt=moe.MOE_F32, score=0, G=1, keep=1, top=2, renorm=1, scale=1.0, lg=FAKE, cfg=True):
+    def call(T=4, E=64, k=4, dt=moe.MOE_F32, score=0, G=1, keep=1, top=2, renorm=1, scale=1.0, lg=FAKE, cfg=True,
+             scores=None):
         c = moe.c_moe_router_config(score, G, keep, top, renorm, scale)
         return moe.lib.moe_router_scored(lg, dt, None, T, E, k, ctypes.byref(c) if cfg else None, FAKE, FAKE,
-                                         None, None)
+                                         scores, None)
     assert call(T=0) == moe.MOE_OK
     assert call(dt=moe.MOE_Q8_0) == moe.MOE_EINVAL
     assert call(cfg=False) == moe.MOE_EINVAL
     assert call(lg=None) == moe.MOE_EINVAL
+    assert call(scores=FAKE) == moe.MOE_EINVAL            # in the place of logits
     assert call(k=0) == moe.MOE_EINVAL
     assert call(k=65) == moe.MOE_EINVAL
     assert call(E=1025) == moe.MOE_ELIMIT
