@@ -43,7 +43,7 @@ IQ4XS_BYTES = 136.0 / 256.0  # IQ4_XS: 256 four-bit codes + one 8-byte record pe
 STAGES = {1: ["row_ids", "gemm_gate_up", "gemm_down", "reduce"],
           2: ["gemv_gate_up", "gemv_down", "reduce"],
           3: ["row_ids", "quant_x", "gemm_gate_up", "quant_h", "gemm_down", "reduce"],
-          4: ["row_ids", "quant_x", "gemm_gate_up", "gemm_down", "reduce"],
+          4: ["row_ids_quant_x", "gemm_gate_up", "gemm_down", "reduce"],
           5: ["gemv_gate_up", "gemv_down", "reduce"]}
 
 

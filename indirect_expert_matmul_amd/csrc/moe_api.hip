@@ -541,10 +541,7 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
     if ((s = check_fp4_limits(g, d.T * (d.n_embd / 32), d.T, "gate/up"))) return s;
     if ((s = check_fp4_limits(g2, n * (d.n_ff / 32) + (int64_t)d.S * d.T * (d.n_ff_sh / 32), 0, "down"))) return s;
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
-    tm.end();
-    tm.begin();
-    if ((s = hip_check(launch_quant_mxfp4(qx, st), "quantize x"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &qx), "row ids, quantize x"))) return s;
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g, st), "gate/up grouped GEMM (MXFP4)"))) return s;
@@ -573,10 +570,7 @@ moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, i
     g.p[0].out_rows = p.r.ids_dst;
     if ((s = check_fp4_limits(g, T * B * (w->cols / 32), T * B, "mul_mat_id"))) return s;
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
-    tm.end();
-    tm.begin();
-    if ((s = hip_check(launch_quant_mxfp4(qa, st), "quantize src1"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &qa), "row ids, quantize src1"))) return s;
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g, st), "grouped GEMM (MXFP4)"))) return s;

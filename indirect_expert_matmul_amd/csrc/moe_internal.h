@@ -93,7 +93,8 @@ struct RowIdsArgs {
 };
 size_t row_ids_scratch_bytes(int64_t n, int32_t E);
 void row_ids_carve_scratch(RowIdsArgs& a, void* scratch);
-hipError_t launch_row_ids(const RowIdsArgs& a, hipStream_t st, int* n_launches);
+struct QuantFp4Args;
+hipError_t launch_row_ids(const RowIdsArgs& a, hipStream_t st, int* n_launches, const QuantFp4Args* q = nullptr);
 
 // ---------------------------------------------------------------- grouped GEMM (K3/K4)
 // One "problem" = a set of expert segments that share weight shapes. Rows of the

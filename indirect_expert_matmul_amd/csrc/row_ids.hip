@@ -19,6 +19,9 @@
 //     position; a second walk over the same range places every entry. Entries keep
 //     their (t, s) order inside a bucket, so the result is unique.
 //   * Bucket E collects ids outside [0, E): they land after all expert segments.
+//   * MXFP4 activations: the first launch also quantizes the call's activation rows, in
+//     thread blocks of its own behind the row-id ones (a small pass has most of the chip to
+//     spare, and a launch of its own took 6 to 18 us more).
 //   * Inputs up to kRowIdsOneBlockMax entries run as one 1024-thread workgroup (one
 //     launch); larger ones use count / scan-over-chunks / place, where every place
 //     block scans the bucket totals itself (with at most kLocalScanChunks chunks it
@@ -27,6 +30,7 @@
 //     stores that rank (16 bits) and each wave's counts, so the place pass needs no
 //     ballots: position = bucket start + chunk offset + wave offset + rank.
 #include "moe_internal.h"
+#include "quant_mxfp4.h"
 
 namespace moe {
 namespace {
@@ -282,9 +286,13 @@ size_t single_lds_bytes(int NB, bool mask) {
 // lanes of a bucket are found with one ballot per bit of the bucket id.
 constexpr int kSingleMaskBuckets = 512;
 
-template <bool MASK>
-__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a) {
+template <bool MASK, bool QUANT>
+__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, QuantFp4Args qa) {
     constexpr int NW = kSingleWaves, NT = NW * 64;
+    if (QUANT && blockIdx.x > 0) {
+        quantize_mxfp4_blocks<true, NT>(qa, (int64_t)blockIdx.x - 1);
+        return;
+    }
     extern __shared__ __attribute__((aligned(16))) uint64_t lds_single[];
     __shared__ int32_t wsum[NW];
     const int NB = a.E + 1, nbits = bucket_bits(NB);
@@ -368,7 +376,12 @@ __global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs
 // wcnt (chunk-major) for the place pass, the chunk's totals to chunk_cnt (bucket-major)
 // for the scan over chunks. Registers are held to 64 per lane so that four blocks (eight
 // waves per SIMD) fit a CU: 1024 chunks then run in one round instead of one and a third.
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a) {
+template <bool QUANT>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, QuantFp4Args qa) {
+    if (QUANT && (int)blockIdx.x >= a.n_chunks) {
+        quantize_mxfp4_blocks<true, kThreads>(qa, (int64_t)blockIdx.x - a.n_chunks);
+        return;
+    }
     // LDS, sized for this launch: per wave, a group mask per bucket [kWaves][NB] and the
     // running count per bucket [kWaves][NB]
     extern __shared__ __attribute__((aligned(16))) uint64_t count_lds[];
@@ -632,33 +645,45 @@ void row_ids_carve_scratch(RowIdsArgs& a, void* scratch) {
     a.rank16 = (uint16_t*)p;
 }
 
-hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches) {
+namespace {
+
+template <bool MASK, bool QUANT>
+hipError_t launch_single(const RowIdsArgs& a, const QuantFp4Args& q, hipStream_t st) {
+    static PerDeviceOnce lds_cap;   // dynamic LDS cap, once per device
+    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_single<MASK, QUANT>,
+                                         (int)single_lds_bytes(MASK ? kSingleMaskBuckets : kMaxBuckets, MASK)))
+        return e;
+    const unsigned grid = 1 + (QUANT ? (unsigned)quant_fp4_grid(q, kSingleWaves * 64) : 0);
+    k_row_ids_single<MASK, QUANT><<<grid, kSingleWaves * 64, single_lds_bytes(a.E + 1, MASK), st>>>(a, q);
+    return hipGetLastError();
+}
+
+template <bool QUANT>
+hipError_t launch_count(const RowIdsArgs& a, const QuantFp4Args& q, size_t lds, hipStream_t st) {
+    static PerDeviceOnce cap;   // the count kernel's dynamic LDS cap, once per device
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count<QUANT>,
+                                         kWaves * kMaxBuckets * (int)(sizeof(uint64_t) + sizeof(int32_t))))
+        return e;
+    const unsigned grid = (unsigned)(a.n_chunks + (QUANT ? quant_fp4_grid(q, kThreads) : 0));
+    k_row_ids_count<QUANT><<<grid, kThreads, lds, st>>>(a, q);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// q: activations (bf16) that the first launch also quantizes, or nullptr.
+hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches, const QuantFp4Args* q) {
     RowIdsArgs a = a0;
+    const QuantFp4Args qa = q ? *q : QuantFp4Args{};
     if (a.n <= kRowIdsOneBlockMax) {
-        static PerDeviceOnce lds_cap_mask, lds_cap_ballot;   // dynamic LDS caps, once per device
-        if (a.E + 1 <= kSingleMaskBuckets) {
-            if (const hipError_t e = set_lds_cap(lds_cap_mask, (const void*)k_row_ids_single<true>,
-                                                 (int)single_lds_bytes(kSingleMaskBuckets, true)))
-                return e;
-            k_row_ids_single<true><<<1, kSingleWaves * 64, single_lds_bytes(a.E + 1, true), st>>>(a);
-        } else {
-            if (const hipError_t e = set_lds_cap(lds_cap_ballot, (const void*)k_row_ids_single<false>,
-                                                 (int)single_lds_bytes(kMaxBuckets, false)))
-                return e;
-            k_row_ids_single<false><<<1, kSingleWaves * 64, single_lds_bytes(a.E + 1, false), st>>>(a);
-        }
         if (n_launches) *n_launches = 1;
-        return hipGetLastError();
+        if (a.E + 1 <= kSingleMaskBuckets)
+            return q ? launch_single<true, true>(a, qa, st) : launch_single<true, false>(a, qa, st);
+        return q ? launch_single<false, true>(a, qa, st) : launch_single<false, false>(a, qa, st);
     }
     a.chunk = chunk_len(a.n);
     a.n_chunks = (a.n + a.chunk - 1) / a.chunk;
     const size_t count_lds = (size_t)kWaves * (a.E + 1) * (sizeof(uint64_t) + sizeof(int32_t));
-    {
-        static PerDeviceOnce cap;   // the count kernel's dynamic LDS cap, once per device
-        if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count,
-                                             kWaves * kMaxBuckets * (int)(sizeof(uint64_t) + sizeof(int32_t))))
-            return e;
-    }
     // ii / k as a multiply-high: M = floor(2^(31 + l) / k) + 1 with l = ceil(log2 k) is
     // exact for every ii < 2^31
     {
@@ -675,14 +700,16 @@ hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches)
     if (a.n_chunks <= kLocalScanChunks) {
         static PerDeviceOnce lds_cap;
         if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<true>, kCap)) return e;
-        k_row_ids_count<<<(unsigned)a.n_chunks, kThreads, count_lds, st>>>(a);
+        if (const hipError_t e = q ? launch_count<true>(a, qa, count_lds, st) : launch_count<false>(a, qa, count_lds, st))
+            return e;
         k_row_ids_place<true><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);
         if (n_launches) *n_launches = 2;
         return hipGetLastError();
     }
     static PerDeviceOnce lds_cap;
     if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<false>, kCap)) return e;
-    k_row_ids_count<<<(unsigned)a.n_chunks, kThreads, count_lds, st>>>(a);
+    if (const hipError_t e = q ? launch_count<true>(a, qa, count_lds, st) : launch_count<false>(a, qa, count_lds, st))
+        return e;
     k_row_ids_scan_chunks<<<(unsigned)(a.E + 1), kThreads, 0, st>>>(a);
     k_row_ids_place<false><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);
     if (n_launches) *n_launches = 3;
