@@ -131,8 +131,8 @@ typedef struct {
      * tau is not read. The two paths add the same products in different orders. x / src1 and
      * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows of
      * activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's codes under 4 GiB
-     * (MOE_ELIMIT). Kernel order for timing: row ids with quantize, grouped GEMM[, down grouped
-     * GEMM], reduce / fix-up; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
+     * (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
+     * grouped GEMM][, reduce]; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
      * weighted calls too large to sum inside the GEMV. */
     int32_t act_quant;
     int32_t reserved[5];

@@ -523,7 +523,8 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
         return s;
     RowIdsArgs ra = row_ids_args(ids, n, d.k, d.E, 1, p.r);
     fp4_tiles(ra, p.r);
-    const QuantFp4Args qx = fp4_act(x, d.T, d.n_embd, p.xq, p.xs);
+    BesideRowIds beside{};
+    beside.quant = fp4_act(x, d.T, d.n_embd, p.xq, p.xs);
     GemmArgs g{}, g2{};
     g.mode = 1;
     g.n_prob = g2.n_prob = shared ? 2 : 1;
@@ -541,7 +542,7 @@ moe_status ffn_fp4(const FfnDims& d, const FfnPlan& p, const moe_weights* gate, 
     if ((s = check_fp4_limits(g, d.T * (d.n_embd / 32), d.T, "gate/up"))) return s;
     if ((s = check_fp4_limits(g2, n * (d.n_ff / 32) + (int64_t)d.S * d.T * (d.n_ff_sh / 32), 0, "down"))) return s;
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &qx), "row ids, quantize x"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids, quantize x"))) return s;
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g, st), "gate/up grouped GEMM (MXFP4)"))) return s;
@@ -561,7 +562,9 @@ moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, i
     if ((s = check_fp4_act(src1, "src1")) || (s = check_fp4_weights(w, "w"))) return s;
     RowIdsArgs ra = row_ids_args(ids, n, k, (int32_t)w->n_mat, B, p.r);
     fp4_tiles(ra, p.r);
-    const QuantFp4Args qa = fp4_act(src1, T * B, w->cols, p.aq, p.as);
+    BesideRowIds beside{};
+    beside.quant = fp4_act(src1, T * B, w->cols, p.aq, p.as);
+    if (!weighted) beside.zero = ZeroSlots{ids, slot_out, n, (int32_t)w->n_mat, (int32_t)w->rows};
     GemmArgs g{};
     g.n_prob = 1;
     g.stream_out = !weighted;
@@ -570,7 +573,7 @@ moe_status mmid_fp4(const MmidPlan& p, const moe_weights* w, const void* src1, i
     g.p[0].out_rows = p.r.ids_dst;
     if ((s = check_fp4_limits(g, T * B * (w->cols / 32), T * B, "mul_mat_id"))) return s;
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &qa), "row ids, quantize src1"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids, quantize src1"))) return s;
     tm.end();
     tm.begin();
     if ((s = hip_check(launch_gemm_fp4(g, st), "grouped GEMM (MXFP4)"))) return s;
@@ -1226,10 +1229,6 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
         if ((s = mmid_fp4(p, w, src1, B, ids, n_tokens, k, slot_out, weighted, tm, st))) return s;
     } else if (path == 5) {
         if ((s = mmid_dec_fp4(p, w, src1, B, ids, n_tokens, k, route_w, slot_out, dst, tm, st))) return s;
-        if (p.fuse || !weighted) {   // written in full, rows of invalid slots too
-            g_stages = tm.stage;
-            return MOE_OK;
-        }
     } else if (!q8 || path == 1) {
         const int bm = gemm_tile_m(p.msub);
         RowIdsArgs ra = row_ids_args(ids, n, k, E, B, p.r);
@@ -1314,6 +1313,10 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
             g_stages = tm.stage;
             return MOE_OK;
         }
+    }
+    if ((path == 4 || path == 5) && (p.fuse || !weighted)) {   // written in full, rows of invalid slots too
+        g_stages = tm.stage;
+        return MOE_OK;
     }
     ReduceArgs rd{};
     rd.ids = ids;

@@ -93,8 +93,8 @@ struct RowIdsArgs {
 };
 size_t row_ids_scratch_bytes(int64_t n, int32_t E);
 void row_ids_carve_scratch(RowIdsArgs& a, void* scratch);
-struct QuantFp4Args;
-hipError_t launch_row_ids(const RowIdsArgs& a, hipStream_t st, int* n_launches, const QuantFp4Args* q = nullptr);
+struct BesideRowIds;
+hipError_t launch_row_ids(const RowIdsArgs& a, hipStream_t st, int* n_launches, const BesideRowIds* beside = nullptr);
 
 // ---------------------------------------------------------------- grouped GEMM (K3/K4)
 // One "problem" = a set of expert segments that share weight shapes. Rows of the
@@ -211,6 +211,19 @@ struct QuantFp4Args {
 // 128 columns, scale bytes to 16 (what one load takes).
 inline __host__ __device__ int64_t fp4_code_row(int64_t K) { return (K + 127) / 128 * 64; }
 inline __host__ __device__ int64_t fp4_scale_row(int64_t K) { return (K / 32 + 15) / 16 * 16; }
+// Per-slot output rows [n][N] of which those of slots with an id outside [0, E) become zero.
+struct ZeroSlots {
+    const int32_t* ids;
+    float* out;
+    int64_t n;   // 0: none
+    int32_t E, N;
+};
+// Work that the row-id pass's first launch does in thread blocks of its own behind its own ones.
+struct BesideRowIds {
+    QuantFp4Args quant;   // bf16
+    ZeroSlots zero;
+    int32_t quant_blocks;   // set by the launcher
+};
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
 // activations (Aq / As); tile_tab required for routed problems, tile height kFp4TileM.

@@ -9,6 +9,7 @@
 // order (the grouped GEMM and the GEMV write row ids_dst[j] = t*k + s), so the
 // reads of one token are k consecutive rows.
 #include "moe_internal.h"
+#include "zero_slots.h"
 
 namespace moe {
 namespace {
@@ -99,21 +100,8 @@ __global__ __launch_bounds__(kThreads) void k_reduce_weighted(ReduceArgs a) {
     }
 }
 
-// Per-slot output: rows of slots whose id is out of range are zero. One wave looks at kZ
-// slots, a lane each, and writes the rows that need it (one thread per output element
-// spent 75 us on 32768 x 2048 just reading ids: 6 us now).
-constexpr int kZ = 8;
-__global__ __launch_bounds__(kThreads) void k_zero_invalid(ReduceArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t n = (int64_t)a.T * a.k;
-    const int64_t s0 = ((int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) * kZ;
-    if (s0 >= n) return;
-    const int32_t e = lane < kZ && s0 + lane < n ? a.ids[s0 + lane] : 0;
-    uint64_t bad = __ballot(e < 0 || e >= a.E);
-    for (; bad; bad &= bad - 1) {
-        float* o = a.out + (s0 + __builtin_ctzll(bad)) * a.N;
-        for (int c = lane; c < a.N; c += 64) o[c] = 0.f;
-    }
+__global__ __launch_bounds__(kThreads) void k_zero_invalid(ZeroSlots a) {
+    zero_invalid_slots<kThreads>(a, blockIdx.x);
 }
 
 }  // namespace
@@ -129,8 +117,8 @@ hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st) {
     } else {
         const int64_t n = (int64_t)a.T * a.k;
         if (n == 0 || a.N == 0) return hipSuccess;
-        const int64_t per = kThreads / 64 * kZ;   // slots per block
-        k_zero_invalid<<<(unsigned)((n + per - 1) / per), kThreads, 0, st>>>(a);
+        const ZeroSlots z{a.ids, a.out, n, a.E, a.N};
+        k_zero_invalid<<<(unsigned)zero_slots_grid(n, kThreads), kThreads, 0, st>>>(z);
     }
     return hipGetLastError();
 }

@@ -19,9 +19,9 @@
 //     position; a second walk over the same range places every entry. Entries keep
 //     their (t, s) order inside a bucket, so the result is unique.
 //   * Bucket E collects ids outside [0, E): they land after all expert segments.
-//   * MXFP4 activations: the first launch also quantizes the call's activation rows, in
-//     thread blocks of its own behind the row-id ones (a small pass has most of the chip to
-//     spare, and a launch of its own took 6 to 18 us more).
+//   * MXFP4 activations: the first launch also quantizes the call's activation rows and zeroes
+//     the output rows of invalid slots, in thread blocks of their own behind the row-id ones (a
+//     small pass has most of the chip to spare; launches of their own took 6 to 18 us and 6 us more).
 //   * Inputs up to kRowIdsOneBlockMax entries run as one 1024-thread workgroup (one
 //     launch); larger ones use count / scan-over-chunks / place, where every place
 //     block scans the bucket totals itself (with at most kLocalScanChunks chunks it
@@ -31,6 +31,7 @@
 //     ballots: position = bucket start + chunk offset + wave offset + rank.
 #include "moe_internal.h"
 #include "quant_mxfp4.h"
+#include "zero_slots.h"
 
 namespace moe {
 namespace {
@@ -286,11 +287,18 @@ size_t single_lds_bytes(int NB, bool mask) {
 // lanes of a bucket are found with one ballot per bit of the bucket id.
 constexpr int kSingleMaskBuckets = 512;
 
-template <bool MASK, bool QUANT>
-__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, QuantFp4Args qa) {
+// Thread block `block` behind the row-id ones.
+template <int THREADS>
+__device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int block) {
+    if (block < b.quant_blocks) quantize_mxfp4_blocks<true, THREADS>(b.quant, block);
+    else zero_invalid_slots<THREADS>(b.zero, block - b.quant_blocks);
+}
+
+template <bool MASK, bool BESIDE>
+__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, BesideRowIds beside) {
     constexpr int NW = kSingleWaves, NT = NW * 64;
-    if (QUANT && blockIdx.x > 0) {
-        quantize_mxfp4_blocks<true, NT>(qa, (int64_t)blockIdx.x - 1);
+    if (BESIDE && blockIdx.x > 0) {
+        beside_row_ids<NT>(beside, (int)blockIdx.x - 1);
         return;
     }
     extern __shared__ __attribute__((aligned(16))) uint64_t lds_single[];
@@ -376,10 +384,10 @@ __global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs
 // wcnt (chunk-major) for the place pass, the chunk's totals to chunk_cnt (bucket-major)
 // for the scan over chunks. Registers are held to 64 per lane so that four blocks (eight
 // waves per SIMD) fit a CU: 1024 chunks then run in one round instead of one and a third.
-template <bool QUANT>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, QuantFp4Args qa) {
-    if (QUANT && (int)blockIdx.x >= a.n_chunks) {
-        quantize_mxfp4_blocks<true, kThreads>(qa, (int64_t)blockIdx.x - a.n_chunks);
+template <bool BESIDE>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, BesideRowIds beside) {
+    if (BESIDE && (int)blockIdx.x >= (int)a.n_chunks) {
+        beside_row_ids<kThreads>(beside, (int)blockIdx.x - (int)a.n_chunks);
         return;
     }
     // LDS, sized for this launch: per wave, a group mask per bucket [kWaves][NB] and the
@@ -647,39 +655,46 @@ void row_ids_carve_scratch(RowIdsArgs& a, void* scratch) {
 
 namespace {
 
-template <bool MASK, bool QUANT>
-hipError_t launch_single(const RowIdsArgs& a, const QuantFp4Args& q, hipStream_t st) {
+// Thread blocks of THREADS threads for the work beside the row ids.
+template <int THREADS>
+unsigned beside_grid(BesideRowIds& b) {
+    b.quant_blocks = (int32_t)quant_fp4_grid(b.quant, THREADS);
+    return (unsigned)(b.quant_blocks + zero_slots_grid(b.zero.n, THREADS));
+}
+
+template <bool MASK, bool BESIDE>
+hipError_t launch_single(const RowIdsArgs& a, BesideRowIds b, hipStream_t st) {
     static PerDeviceOnce lds_cap;   // dynamic LDS cap, once per device
-    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_single<MASK, QUANT>,
+    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_single<MASK, BESIDE>,
                                          (int)single_lds_bytes(MASK ? kSingleMaskBuckets : kMaxBuckets, MASK)))
         return e;
-    const unsigned grid = 1 + (QUANT ? (unsigned)quant_fp4_grid(q, kSingleWaves * 64) : 0);
-    k_row_ids_single<MASK, QUANT><<<grid, kSingleWaves * 64, single_lds_bytes(a.E + 1, MASK), st>>>(a, q);
+    const unsigned grid = 1 + (BESIDE ? beside_grid<kSingleWaves * 64>(b) : 0);
+    k_row_ids_single<MASK, BESIDE><<<grid, kSingleWaves * 64, single_lds_bytes(a.E + 1, MASK), st>>>(a, b);
     return hipGetLastError();
 }
 
-template <bool QUANT>
-hipError_t launch_count(const RowIdsArgs& a, const QuantFp4Args& q, size_t lds, hipStream_t st) {
+template <bool BESIDE>
+hipError_t launch_count(const RowIdsArgs& a, BesideRowIds b, size_t lds, hipStream_t st) {
     static PerDeviceOnce cap;   // the count kernel's dynamic LDS cap, once per device
-    if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count<QUANT>,
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count<BESIDE>,
                                          kWaves * kMaxBuckets * (int)(sizeof(uint64_t) + sizeof(int32_t))))
         return e;
-    const unsigned grid = (unsigned)(a.n_chunks + (QUANT ? quant_fp4_grid(q, kThreads) : 0));
-    k_row_ids_count<QUANT><<<grid, kThreads, lds, st>>>(a, q);
+    const unsigned grid = (unsigned)a.n_chunks + (BESIDE ? beside_grid<kThreads>(b) : 0);
+    k_row_ids_count<BESIDE><<<grid, kThreads, lds, st>>>(a, b);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// q: activations (bf16) that the first launch also quantizes, or nullptr.
-hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches, const QuantFp4Args* q) {
+// beside: what the first launch also does, or nullptr.
+hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches, const BesideRowIds* beside) {
     RowIdsArgs a = a0;
-    const QuantFp4Args qa = q ? *q : QuantFp4Args{};
+    const BesideRowIds b = beside ? *beside : BesideRowIds{};
     if (a.n <= kRowIdsOneBlockMax) {
         if (n_launches) *n_launches = 1;
         if (a.E + 1 <= kSingleMaskBuckets)
-            return q ? launch_single<true, true>(a, qa, st) : launch_single<true, false>(a, qa, st);
-        return q ? launch_single<false, true>(a, qa, st) : launch_single<false, false>(a, qa, st);
+            return beside ? launch_single<true, true>(a, b, st) : launch_single<true, false>(a, b, st);
+        return beside ? launch_single<false, true>(a, b, st) : launch_single<false, false>(a, b, st);
     }
     a.chunk = chunk_len(a.n);
     a.n_chunks = (a.n + a.chunk - 1) / a.chunk;
@@ -700,7 +715,7 @@ hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches,
     if (a.n_chunks <= kLocalScanChunks) {
         static PerDeviceOnce lds_cap;
         if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<true>, kCap)) return e;
-        if (const hipError_t e = q ? launch_count<true>(a, qa, count_lds, st) : launch_count<false>(a, qa, count_lds, st))
+        if (const hipError_t e = beside ? launch_count<true>(a, b, count_lds, st) : launch_count<false>(a, b, count_lds, st))
             return e;
         k_row_ids_place<true><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);
         if (n_launches) *n_launches = 2;
@@ -708,7 +723,7 @@ hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches,
     }
     static PerDeviceOnce lds_cap;
     if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<false>, kCap)) return e;
-    if (const hipError_t e = q ? launch_count<true>(a, qa, count_lds, st) : launch_count<false>(a, qa, count_lds, st))
+    if (const hipError_t e = beside ? launch_count<true>(a, b, count_lds, st) : launch_count<false>(a, b, count_lds, st))
         return e;
     k_row_ids_scan_chunks<<<(unsigned)(a.E + 1), kThreads, 0, st>>>(a);
     k_row_ids_place<false><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);

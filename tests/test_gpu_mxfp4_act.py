@@ -129,6 +129,9 @@ def _mul_mat_id(E, k, T, K, N, B, ids, path, lo=118, hi=122):
     (5, 2, 600, 2880, 96, False, "uniform"),
     (2, 1, 33, 7168, 64, False, "uniform"),
     (8, 2, 30, 128, 64, False, "none"),     # every id invalid
+    (8, 4, 2600, 160, 72, False, "bad"),    # row ids over several thread blocks
+    (700, 3, 40, 128, 33, True, "bad"),     # more experts than the row-id pass's mask words
+    (900, 5, 1900, 96, 24, False, "bad"),
 ])
 def test_mul_mat_id_grouped(E, k, T, K, N, B_is_k, routing):
     rng = np.random.default_rng(T * 31 + E)
@@ -258,7 +261,7 @@ def test_narrow_rows_take_the_grouped_gemm():
     """Rows under 128 columns: the automatic choice is the grouped GEMM, the forced GEMV is refused."""
     ids = synth.draw_ids_uniform(3, 2, 4, 2)
     _mul_mat_id(4, 2, 2, 96, 40, 1, ids, moe.PATH_AUTO)
-    assert moe.last_stage_count() == 3      # row ids with the quantization, GEMM, sum over the slots
+    assert moe.last_stage_count() == 2      # row ids with the quantization, GEMM
     with pytest.raises(moe.MoeError):
         _mul_mat_id(4, 2, 2, 96, 40, 1, ids, moe.PATH_GEMV)
 
