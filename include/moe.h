@@ -126,9 +126,9 @@ typedef struct {
      * 2: MXFP4 activations (MXFP4 experts only): activation rows are quantized to MXFP4
      * (moe_quantize_mxfp4's format) and multiplied with the experts' codes by the block
      * scaled FP4 MFMA, fp32 accumulation. The fused FFN quantizes x before gate/up and the
-     * float32 h before down. GEMV path (path 0 takes it where it can be forced): n_tokens *
-     * n_used <= 64, n_tokens * shared experts <= 64, every row at least 128 columns wide;
-     * tau is not read. The two paths add the same products in different orders. x / src1 and
+     * float32 h before down. GEMV path: n_tokens * n_used <= 64, n_tokens * shared experts <=
+     * 64, every row at least 128 columns wide; path 0 takes it there while n_tokens * n_used <=
+     * 16 * n_experts; tau is not read. The two paths add the same products in different orders. x / src1 and
      * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows of
      * activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's codes under 4 GiB
      * (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down

@@ -17,6 +17,9 @@
 //     maximum over 4 lanes, and puts the codes and scale bytes into LDS, from where they come
 //     back in the MFMA's layout. (Each lane reading its own blocks took 16 loads a superstep,
 //     four of them one after the other.)
+//   * A block that does not sum keeps the partial sums of one pass (up to 16 slots of its expert)
+//     in LDS, so that two to four blocks share a CU (room for every slot of the call left one: 64
+//     slots of 2048 x 7168 took 130 us, now 106; 64 of 4096 x 4096, 8 experts, 32, now 23).
 //   * The weighted sum over a token's slots is fused where one block can take all the experts
 //     of its 16 rows in a few rounds of its waves; else the per-slot rows go through the
 //     workspace to the reduce kernel.
@@ -112,7 +115,8 @@ __device__ __forceinline__ int piece_scale(const Piece& p, int j, int b, int g, 
 
 template <int MODE, bool F32, bool FUSE>
 __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
-    // partial sums [slots][kp][rg][16 rows] (gate/up: twice), then each wave's quantized activations
+    // partial sums [slots][kp][rg][16 rows] (gate/up: twice), then each wave's quantized activations;
+    // slots: all of them in a block that sums, else those of one pass
     extern __shared__ __attribute__((aligned(16))) float s_part[];
     __shared__ int s_list[kWaves][kDecFp4Slots];                 // per wave: the unit's slots
     __shared__ uint8_t s_mine[FUSE ? kDecFp4Slots : 1];              // routed slots with an expert
@@ -122,7 +126,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
     const int row_first = (int)blockIdx.x * 16 * a.rg;
     const int y = (int)blockIdx.y;
     constexpr int kRows = MODE == 1 ? 32 : 16;
-    uint8_t* s_x = (uint8_t*)(s_part + n_all * a.kp * a.rg * kRows) + wv * 2 * a.xs * kXRow;   // [2 supersteps][xs slots]
+    uint8_t* s_x = (uint8_t*)(s_part + (FUSE ? n_all : a.xs) * a.kp * a.rg * kRows) +
+                   wv * 2 * a.xs * kXRow;   // [2 supersteps][xs slots]
+    // row r (of the block's 16 rg) of a slot's product
+    auto total = [&](int at, int r, int m) -> float {
+        float v = 0.f;
+        for (int p = 0; p < a.kp; p++)
+            v += s_part[(((int64_t)at * a.kp + p) * a.rg + (r >> 4)) * kRows + 16 * m + (r & 15)];
+        return v;
+    };
+    const int rows = 16 * a.rg, shift = a.rg == 1 ? 4 : a.rg == 2 ? 5 : 6;   // rg: 1, 2 or 4
 
     // each lane its slot's expert; lanes with the same one; the first lane of each distinct expert
     int my_e = lane < n ? a.ids[lane] : -1;
@@ -142,15 +155,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
         for (int i = tid; i < n; i += (int)blockDim.x) s_mine[i] = (valid >> i) & 1;
     }
     const int units = FUSE ? nd + a.sw.n_mat : (y < a.d_max ? (y < nd) : 1);
-    uint64_t mask = 0;   // the unit's slots (shared: tokens)
-    bool sh = false;
-    int sj = 0;          // shared expert
     for (int it = wv; it < units * a.kp; it += waves) {
         const int u = FUSE ? it / a.kp : y, p = FUSE ? it - u * a.kp : it;
-        sh = FUSE ? u >= nd : y >= a.d_max;
-        sj = u - (FUSE ? nd : a.d_max);
+        const bool sh = FUSE ? u >= nd : y >= a.d_max;
+        const int sj = u - (FUSE ? nd : a.d_max);   // shared expert
         const DecFp4Weights& W = sh ? a.sw : a.rw;
         int e;
+        uint64_t mask;   // the unit's slots (shared: tokens)
         if (sh) {
             e = sj;
             mask = a.T >= 64 ? ~0ull : (1ull << a.T) - 1;
@@ -186,7 +197,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
             const int some = min(cnt - sg, a.xs);
             const bool on = r16 < some;
             const int slot = on ? s_list[wv][sg + r16] : 0;
-            const int at = sh ? n + sj * a.T + slot : slot;
+            const int at = !FUSE ? r16 : sh ? n + sj * a.T + slot : slot;
             float* part = s_part + ((int64_t)at * a.kp + p) * a.rg * kRows + 4 * g4;
             uint64_t here = left;
             // two supersteps at a time: all of the wave's up to K = 8192
@@ -270,19 +281,21 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
                 __builtin_amdgcn_wave_barrier();
             }
             left = here;
+            if (!FUSE) {   // all the block's waves are at this pass of the one unit
+                __syncthreads();
+                for (int i = tid; i < some * rows; i += (int)blockDim.x) {
+                    const int z = i >> shift, r = i & (rows - 1), s = s_list[wv][sg + z];
+                    if (row_first + r >= N) continue;
+                    float v = total(z, r, 0);
+                    if (MODE == 1) v = v / (1.0f + expf(-v)) * total(z, r, MODE);
+                    ((sh ? a.sout + ((int64_t)sj * a.T + s) * N : a.out + (int64_t)s * N) + row_first)[r] = v;
+                }
+                __syncthreads();
+            }
         }
     }
-    __syncthreads();
-
-    // row r (of the block's 16 rg) of a slot's product
-    auto total = [&](int at, int r, int m) -> float {
-        float v = 0.f;
-        for (int p = 0; p < a.kp; p++)
-            v += s_part[(((int64_t)at * a.kp + p) * a.rg + (r >> 4)) * kRows + 16 * m + (r & 15)];
-        return v;
-    };
-    const int rows = 16 * a.rg, shift = a.rg == 1 ? 4 : a.rg == 2 ? 5 : 6;   // rg: 1, 2 or 4
     if (FUSE) {   // out_tok[t] = sum over s ascending of route_w * row, then the shared experts
+        __syncthreads();
         for (int i = tid; i < a.T * rows; i += (int)blockDim.x) {
             const int t = i >> shift, r = i & (rows - 1);
             if (row_first + r >= a.rw.N) continue;
@@ -293,18 +306,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
             a.out_tok[(int64_t)t * a.rw.N + row_first + r] = v;
         }
         return;
-    }
-    const int N = sh ? a.sw.N : a.rw.N;
-    if (units) {   // wave 0's list serves all: one unit
-        const int cnt = __popcll(mask);
-        for (int i = tid; i < cnt * rows; i += (int)blockDim.x) {
-            const int slot = s_list[0][i >> shift], r = i & (rows - 1);
-            if (row_first + r >= N) continue;
-            const int at = sh ? n + sj * a.T + slot : slot;
-            float v = total(at, r, 0);
-            if (MODE == 1) v = v / (1.0f + expf(-v)) * total(at, r, MODE);
-            ((sh ? a.sout + (int64_t)(at - n) * N : a.out + (int64_t)at * N) + row_first)[r] = v;
-        }
     }
     if (MODE == 0 && y == 0) {   // rows of slots whose id is out of range are zero
         uint64_t bad = ~valid & (n >= 64 ? ~0ull : (1ull << n) - 1);
@@ -331,7 +332,7 @@ hipError_t launch_decode_fp4(const DecFp4Args& a0, hipStream_t st) {
     const int nss = (K + 511) / 512;   // supersteps
     const int d_max = n < a.E ? n : a.E;
     // slots of one expert at a time: those of distinct ids (others take another round)
-    a.xs = a.T < 16 ? a.T : 16;
+    a.xs = a.T < kDecFp4Pass ? a.T : kDecFp4Pass;
     const size_t per_wave = (size_t)2 * a.xs * kXRow;
     const int units = d_max + a.sw.n_mat;
     // two supersteps a wave; rows per unit: up to four groups of 16 while that leaves enough waves
@@ -345,7 +346,7 @@ hipError_t launch_decode_fp4(const DecFp4Args& a0, hipStream_t st) {
         waves = units * kp < kWaves ? units * kp : kWaves;
     }
     auto lds_of = [&]() {
-        return (size_t)n_all * a.rg * 16 * 4 * (a.mode == 1 ? 2 : 1) * kp + per_wave * waves;
+        return (size_t)(a.fuse ? n_all : a.xs) * a.rg * 16 * 4 * (a.mode == 1 ? 2 : 1) * kp + per_wave * waves;
     };
     while (lds_of() > (size_t)kDecFp4Lds) {
         if (a.fuse && waves > 4) waves--;

@@ -27,7 +27,7 @@
 //   * An expert's rows are split into equal tiles (of whole 32-row MFMA columns) rather
 //     than full ones and a rest: a block's time goes with its rows.
 //   * Output rows that no further kernel of the call reads are stored past the caches
-//     (1100 rows x 896: 35 -> 34 us, 32768 x 2048: 482 -> 474); before a weighted sum the
+//     (32768 rows x 2048: 482 -> 474 us); before a weighted sum the
 //     plain stores are better, which leave part of the rows in the caches (sum: 40 against 43).
 //
 // Measured (this kernel alone): 4096 tokens x 8 slots, 128 experts of 2048 x 7168, 474 us, 2030

@@ -234,6 +234,7 @@ constexpr int kFp4TileM = 128;
 
 // GEMV (decode) path of MXFP4 activations: T * k and S * T slots of at most kDecFp4Slots each.
 constexpr int kDecFp4Slots = 64;
+constexpr int kDecFp4Pass = 16;   // slots of one expert that a pass multiplies
 constexpr int kDecFp4Lds = 128 * 1024;
 struct DecFp4Weights {
     const uint8_t *q1, *s1;   // codes [n_mat][N][K/2], scale bytes [n_mat][N][K/32]

@@ -146,6 +146,9 @@ def test_mxfp4_act_path_bounds():
     def typed(T, k, width, path=moe.PATH_AUTO):
         return moe.moe_select_path_typed(T, k, 32, width, moe.MOE_MXFP4, path=path, act_quant=2)
     assert [typed(T, k, 128) for T, k in ((64, 1), (16, 4), (1, 64), (65, 1), (13, 5))] == [5, 5, 5, 4, 4]
+    def few(T, path=moe.PATH_AUTO):
+        return moe.moe_select_path_typed(T, 1, 2, 128, moe.MOE_MXFP4, path=path, act_quant=2)
+    assert few(32) == 5 and few(33) == 4 and few(33, moe.PATH_GEMV) == 5    # 16 slots an expert on average
     assert typed(1, 1, 127) == 4 and typed(1, 1, 96) == 4
     for T, k, width in ((1, 1, 96), (65, 1, 128)):
         with pytest.raises(moe.MoeError):
