@@ -19,7 +19,10 @@
 //     four of them one after the other.)
 //   * A block that does not sum keeps the partial sums of one pass (up to 16 slots of its expert)
 //     in LDS, so that two to four blocks share a CU (room for every slot of the call left one: 64
-//     slots of 2048 x 7168 took 130 us, now 106; 64 of 4096 x 4096, 8 experts, 32, now 23).
+//     slots of 2048 x 7168 took 130 us, then 106; 64 of 4096 x 4096, 8 experts, 32, then 23).
+//   * A wave holds one group's codes and no next ones: other waves cover the loads. (Loading a
+//     group ahead took 141 and 221 registers instead of 109 and 156: gate/up of one token, 2880 x
+//     2880, 4 experts, 21 us instead of 15; 64 slots of 2048 x 7168 106 instead of 92.)
 //   * The weighted sum over a token's slots is fused where one block can take all the experts
 //     of its 16 rows in a few rounds of its waves; else the per-slot rows go through the
 //     workspace to the reduce kernel.
@@ -38,7 +41,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 constexpr int kWaves = 8;        // waves of a block at most
 constexpr int kFuseItems = 16;   // work items of a block that sums the slots at most
 constexpr int kXRow = 256 + 16;  // a slot's superstep in LDS: codes, scale bytes
-constexpr int kManyWaves = 2048; // waves that fill the chip (8 a CU)
+// Waves that fill the chip (8 a CU): units of more rows once there are so many (with 4096 for it,
+// 64 slots of 4096 x 4096, 8 experts, took 28 us instead of 23.7; with 1024 one token 10.1 for 9.1).
+constexpr int kManyWaves = 2048;
 
 __device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
@@ -202,7 +207,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
             uint64_t here = left;
             // two supersteps at a time: all of the wave's up to K = 8192
             for (int ss = ss0; ss < ss1 || ss == ss0; ss += 2) {
-                Weights w, w_next;
+                Weights w;
                 if (ss0 < ss1) load(w, 0, ss);
                 here = left;
                 for (int i = 0; i < some; i += 2) {   // two slots' activations at a time
@@ -240,7 +245,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
                 }
                 __builtin_amdgcn_wave_barrier();
                 for (int rg = 0; rg < groups; rg++) {
-                    if (rg + 1 < groups && ss0 < ss1) load(w_next, rg + 1, ss);
+                    if (rg > 0 && ss0 < ss1) load(w, rg, ss);
                     f32x4 acc[MODE + 1];
 #pragma unroll
                     for (int m = 0; m <= MODE; m++) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -276,7 +281,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_decode_fp4(DecFp4Args a) {
                             *(f32x4*)(d + 16 * m) = acc[m];
                         }
                     }
-                    w = w_next;
                 }
                 __builtin_amdgcn_wave_barrier();
             }
