@@ -24,8 +24,12 @@
 //     group ahead took 141 and 221 registers instead of 109 and 156: gate/up of one token, 2880 x
 //     2880, 4 experts, 21 us instead of 15; 64 slots of 2048 x 7168 106 instead of 92.)
 //   * The weighted sum over a token's slots is fused where one block can take all the experts
-//     of its 16 rows in a few rounds of its waves; else the per-slot rows go through the
-//     workspace to the reduce kernel.
+//     of its 16 rows in a few rounds of its waves (one token 2880 x 2880, 4 experts: 11.8 us, against
+//     9.1 and 4 for the sum's launch); else the per-slot rows go through the workspace to the
+//     reduce kernel.
+// Measured: 4 experts of 2880 x 2880 9.1 us (17.6 MB: the launch and one memory round trip), 8
+// tokens x 4 of 32 28 us (3.3 TB/s, one round of blocks), 64 slots of 128 experts of 2048 x 7168
+// 92 us (4.4 TB/s).
 #include <algorithm>
 
 #include "moe_internal.h"

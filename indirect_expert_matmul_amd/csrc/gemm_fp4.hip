@@ -27,13 +27,13 @@
 //   * An expert's rows are split into equal tiles (of whole 32-row MFMA columns) rather
 //     than full ones and a rest: a block's time goes with its rows.
 //   * Output rows that no further kernel of the call reads are stored past the caches
-//     (32768 rows x 2048: 482 -> 474 us); before a weighted sum the
-//     plain stores are better, which leave part of the rows in the caches (sum: 40 against 43).
+//     (32768 rows x 2048: 482 -> 474 us); before a weighted sum the plain stores are better,
+//     which leave part of the rows in the caches (sum: 40 us against 43).
 //
 // Measured (this kernel alone): 4096 tokens x 8 slots, 128 experts of 2048 x 7168, 474 us, 2030
-// TFLOP/s; 4096 x 4, 32 experts of 2880 x 2880, 189 us, 1440 TFLOP/s. Bound by LDS and the
-// copies into it as much as by the MFMAs: without the copies 307 and 106 us, with the copies
-// and no MFMA 331 and 114. Tried and slower at these two sizes: 128 x 128 tiles 507 and 196;
+// TFLOP/s; 4096 x 4, 32 experts of 2880 x 2880, 189 us, 1440 TFLOP/s. Bound by the copies: the
+// first takes 297 us without them and 450 with them and one MFMA in eight (3.5 GB from L2 to
+// LDS in requests of 64 bytes, 1.4 GB from HBM). Tried and slower at these two sizes: 128 x 128 tiles 507 and 196;
 // weights from global memory straight into MFMA registers 604 and 210; 256 x 256 tiles with
 // 8 waves 497 and 183; persistent blocks 506 and 185.
 #include <type_traits>
