@@ -512,6 +512,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
             const float size = (b1 > -INFINITY ? fabsf(b1) : 0.f) + (sums && b2 > -INFINITY ? fabsf(b2) : 0.f);
             const float err = (a.sigmoid ? kErrSigmoid : kErrSoftmax) * 2.f + kErrSum * row_max(size);
             if (out > -INFINITY && !(in - out > err)) doubt = true;
+            // a sum past float32's range: no order against the others, and none against an empty group
+            if (sums && b2 > -INFINITY && !(fabsf(g) < INFINITY)) doubt = true;
         }
     }
     // one number per expert: its choice's key and itself, in the order of picking
