@@ -118,7 +118,7 @@ hipError_t launch_reduce(const ReduceArgs& a, hipStream_t st) {
         const int64_t n = (int64_t)a.T * a.k;
         if (n == 0 || a.N == 0) return hipSuccess;
         const ZeroSlots z{a.ids, a.out, n, a.E, a.N};
-        k_zero_invalid<<<(unsigned)zero_slots_grid(n, kThreads), kThreads, 0, st>>>(z);
+        k_zero_invalid<<<(unsigned)zero_slots_grid(z, kThreads), kThreads, 0, st>>>(z);
     }
     return hipGetLastError();
 }

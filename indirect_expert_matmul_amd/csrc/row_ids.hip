@@ -659,7 +659,7 @@ namespace {
 template <int THREADS>
 unsigned beside_grid(BesideRowIds& b) {
     b.quant_blocks = (int32_t)quant_fp4_grid(b.quant, THREADS);
-    return (unsigned)(b.quant_blocks + zero_slots_grid(b.zero.n, THREADS));
+    return (unsigned)(b.quant_blocks + zero_slots_grid(b.zero, THREADS));
 }
 
 template <bool MASK, bool BESIDE>
