@@ -101,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void k_reduce_weighted(ReduceArgs a) {
 }
 
 __global__ __launch_bounds__(kThreads) void k_zero_invalid(ZeroSlots a) {
-    zero_invalid_slots<kThreads>(a, blockIdx.x);
+    zero_invalid_slots<kThreads>(a, blockIdx.x, gridDim.x);
 }
 
 }  // namespace

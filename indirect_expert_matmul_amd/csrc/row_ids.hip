@@ -287,18 +287,19 @@ size_t single_lds_bytes(int NB, bool mask) {
 // lanes of a bucket are found with one ballot per bit of the bucket id.
 constexpr int kSingleMaskBuckets = 512;
 
-// Thread block `block` behind the row-id ones.
+// Thread block `block` behind the `own` row-id ones.
 template <int THREADS>
-__device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int block) {
+__device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int own) {
+    const int block = (int)blockIdx.x - own;
     if (block < b.quant_blocks) quantize_mxfp4_blocks<true, THREADS>(b.quant, block);
-    else zero_invalid_slots<THREADS>(b.zero, block - b.quant_blocks);
+    else zero_invalid_slots<THREADS>(b.zero, block - b.quant_blocks, gridDim.x - own - b.quant_blocks);
 }
 
 template <bool MASK, bool BESIDE>
 __global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, BesideRowIds beside) {
     constexpr int NW = kSingleWaves, NT = NW * 64;
     if (BESIDE && blockIdx.x > 0) {
-        beside_row_ids<NT>(beside, (int)blockIdx.x - 1);
+        beside_row_ids<NT>(beside, 1);
         return;
     }
     extern __shared__ __attribute__((aligned(16))) uint64_t lds_single[];
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs
 template <bool BESIDE>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, BesideRowIds beside) {
     if (BESIDE && (int)blockIdx.x >= (int)a.n_chunks) {
-        beside_row_ids<kThreads>(beside, (int)blockIdx.x - (int)a.n_chunks);
+        beside_row_ids<kThreads>(beside, (int)a.n_chunks);
         return;
     }
     // LDS, sized for this launch: per wave, a group mask per bucket [kWaves][NB] and the

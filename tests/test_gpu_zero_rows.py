@@ -44,3 +44,20 @@ def test_rows_of_invalid_slots(kind, path, aq, T, k, N, bad):
     assert np.all(o[off] == 0) and np.all(np.isfinite(o))
     assert N < 100 or np.all((o[~off] != 0).any(axis=1))
     assert (buf[:64] == 7).all() and (buf[64 + T * k * N:] == 7).all()
+
+
+@pytest.mark.parametrize("kind,path,aq", [("f32", 0, 0), ("q8", moe.PATH_GEMM, 0), ("mxfp4", moe.PATH_GEMM, 2)])
+def test_more_slots_than_one_group_a_thread_block(kind, path, aq):
+    """Past 2^21 slots each thread block takes several groups of them."""
+    E, K, N, T, k = 5, 32, 3, 300007, 9
+    assert T * k > 2 ** 21
+    w = _experts(kind, E, N, K)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.randint(-2, E + 2, (T, k), dtype=torch.int32, device="cuda", generator=g)
+    x = torch.randn((T, K), device="cuda", generator=g) + 0.5
+    x = x if kind == "f32" else x.to(torch.bfloat16)
+    out = torch.full((T, k, N), float("nan"), device="cuda")
+    moe.moe_mul_mat_id(w, x, ids, out=out, path=path, act_quant=aq)
+    off = (ids < 0) | (ids >= E)
+    assert (out[off] == 0).all() and torch.isfinite(out).all()
+    assert (out[~off] != 0).any(dim=1).float().mean() > 0.99
