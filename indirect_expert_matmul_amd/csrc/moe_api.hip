@@ -489,14 +489,15 @@ moe_status check_fp4_act(const void* x, const char* name) {
     return MOE_OK;
 }
 moe_status check_fp4_weights(const moe_weights* w, const char* name) {
-    if (w && w->n_mat && (uintptr_t)w->data % 16)
+    if (!w || !w->n_mat) return MOE_OK;
+    if ((uintptr_t)w->data % 16)
         return fail(MOE_EINVAL, "MXFP4 activations: the codes of %s must be 16-byte aligned", name);
+    if (w->cols >= (1 << 24))
+        return fail(MOE_ELIMIT, "MXFP4 activations: %s must have cols < 2^24 (got %lld)", name, (long long)w->cols);
     return MOE_OK;
 }
 // gathered_rows: rows of the activation tensor that is addressed through the row map.
 moe_status check_fp4_limits(const GemmArgs& g, int64_t act_blocks, int64_t gathered_rows, const char* what) {
-    for (int i = 0; i < g.n_prob; i++)
-        if (g.p[i].K >= (1 << 24)) return fail(MOE_ELIMIT, "%s: MXFP4 activations need cols < 2^24", what);
     if (gathered_rows * fp4_code_row(g.p[0].K) > k4GiB - 256)
         return fail(MOE_ELIMIT, "%s: the gathered MXFP4 activation codes must be under 4 GiB", what);
     if (act_blocks >= kFp4MaxBlocks)
