@@ -129,9 +129,9 @@ typedef struct {
      * float32 h before down. GEMV path: n_tokens * n_used <= 64, n_tokens * shared experts <=
      * 64, every row at least 128 columns wide; path 0 takes it there while n_tokens * n_used <=
      * 16 * n_experts; tau is not read. The two paths add the same products in different orders. x / src1 and
-     * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows of
-     * activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's codes under 4 GiB
-     * (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
+     * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows <
+     * 2^31 - 512, rows of activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's
+     * codes under 4 GiB (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
      * grouped GEMM][, reduce]; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
      * weighted calls too large to sum inside the GEMV. */
     int32_t act_quant;

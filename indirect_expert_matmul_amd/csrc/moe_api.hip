@@ -492,8 +492,9 @@ moe_status check_fp4_weights(const moe_weights* w, const char* name) {
     if (!w || !w->n_mat) return MOE_OK;
     if ((uintptr_t)w->data % 16)
         return fail(MOE_EINVAL, "MXFP4 activations: the codes of %s must be 16-byte aligned", name);
-    if (w->cols >= (1 << 24))
-        return fail(MOE_ELIMIT, "MXFP4 activations: %s must have cols < 2^24 (got %lld)", name, (long long)w->cols);
+    if (w->cols >= (1 << 24) || w->rows > INT32_MAX - 512)   // row numbers of the last tile stay in int32
+        return fail(MOE_ELIMIT, "MXFP4 activations: %s must have cols < 2^24 and rows < 2^31 - 512 (got %lld, %lld)",
+                    name, (long long)w->cols, (long long)w->rows);
     return MOE_OK;
 }
 // gathered_rows: rows of the activation tensor that is addressed through the row map.

@@ -30,3 +30,14 @@ def test_cols_limit(path):
         assert moe.lib.moe_ffn_fused(r(g), r(g), r(g), r(sg), r(sg), r(sd), FAKE, moe.MOE_BF16, FAKE, FAKE, 1, 1,
                                      FAKE, r(opt), FAKE, 1 << 60, None) == moe.MOE_ELIMIT
         assert "2^24" in moe.last_error()
+
+
+@pytest.mark.parametrize("path", [moe.PATH_GEMV, moe.PATH_GEMM])
+def test_rows_limit(path):
+    """Row numbers past the last row, up to a whole tile, must not leave int32."""
+    opt = moe._options(path, act_quant=2)
+    for rows in ((1 << 31) - 1, (1 << 31) - 512):
+        m = moe.c_moe_weights(moe.MOE_MXFP4, FAKE, FAKE, 1, rows, 128)
+        assert moe.lib.moe_mul_mat_id(ctypes.byref(m), FAKE, moe.MOE_BF16, 1, FAKE, 1, 1, None, FAKE,
+                                      ctypes.byref(opt), FAKE, 1 << 60, None) == moe.MOE_ELIMIT
+        assert "2^31" in moe.last_error()
