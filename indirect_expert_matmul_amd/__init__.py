@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from operator import index as _int
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -194,12 +195,15 @@ def _options(path: int = PATH_AUTO, tau: float = 0.0, events: Optional[Sequence[
 
 @functools.lru_cache(maxsize=64)
 def _fixed_options(path: int, tau: float, act_quant: int):
-    """_options without events: a struct that the calls only read, made once per set of values."""
+    """_options without events: a struct that the calls only read, made once per set of plain numbers (a
+    tensor or array among them would be looked up by its identity, not by its value)."""
     return _options(path, tau, None, act_quant)
 
 
 def _call_options(path, tau, events, act_quant):
-    return _options(path, tau, events, act_quant) if events else _fixed_options(path, tau, act_quant)
+    if events:
+        return _options(path, tau, events, act_quant)
+    return _fixed_options(_int(path), float(tau), _int(act_quant))
 
 
 def _stream(stream) -> int:
@@ -371,11 +375,16 @@ def moe_quantize_mxfp4(x: torch.Tensor, return_values: bool = False, stream=None
 
 
 @functools.lru_cache(maxsize=64)
+def _fixed_router_config(*values) -> c_moe_router_config:
+    """The struct of these plain numbers (the calls only read it)."""
+    return c_moe_router_config(*values)
+
+
 def _router_config(score, n_group, topk_group, group_top, renorm, scale) -> c_moe_router_config:
-    """The struct for these values (the calls only read it)."""
     if score not in SCORES:
         raise ValueError("score must be one of %s (got %r)" % (", ".join(sorted(SCORES)), score))
-    return c_moe_router_config(SCORES[score], n_group, topk_group, group_top, int(bool(renorm)), scale)
+    return _fixed_router_config(SCORES[score], _int(n_group), _int(topk_group), _int(group_top), int(bool(renorm)),
+                                float(scale))
 
 
 def _check_logits(logits: torch.Tensor, stream) -> int:
