@@ -395,15 +395,24 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
     float den = 0.f;
     float v[C];                              // scores, then choices
     if (all_scores) {
+        // scores that leave the kernel, and a sum that weights are divided by, with full exponentials;
+        // choices alone with the short ones (z = exp(-|l|) off by |l| 2^-23), which their bound covers
+        if (a.scores || (!a.renorm && !a.sigmoid)) {
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            if (a.sigmoid) {
-                const float z = __expf(-fabsf(l[c])), f = __builtin_amdgcn_rcpf(1.f + z);
-                v[c] = l[c] > 0.f ? f : z * f;
-            } else {
-                v[c] = __expf(l[c] - base);
-                den += v[c];
+            for (int c = 0; c < C; c++) {
+                const float z = expf(a.sigmoid ? -fabsf(l[c]) : l[c] - base);
+                v[c] = !a.sigmoid ? z : (l[c] > 0.f ? 1.f : z) / (1.f + z);
             }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const float z = __expf(a.sigmoid ? -fabsf(l[c]) : l[c] - base);
+                v[c] = !a.sigmoid ? z : (l[c] > 0.f ? 1.f : z) * __builtin_amdgcn_rcpf(1.f + z);
+            }
+        }
+        if (!a.sigmoid) {
+#pragma unroll
+            for (int c = 0; c < C; c++) den += v[c];
         }
         if (!a.sigmoid) {
             den = row_sum(den);

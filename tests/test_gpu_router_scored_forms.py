@@ -29,3 +29,35 @@ def test_group_sums_past_float32(score, dtype):
         ids, w = moe.moe_router_scored(l.cuda(), k, bias=dev_f32(bias), **kw)
         ri, _, _ = ref64.route(l.double().numpy(), k, bias=np.float32(bias), **kw)
         assert np.array_equal(ids.cpu().numpy(), ri), (keep, k)
+
+
+def _whole_logits(T, E, lo, hi):
+    """Whole numbers: differences of them are exact, so that no bound has a term for their rounding."""
+    l = np.random.default_rng(T + E).integers(lo, hi + 1, size=(T, E)).astype(np.float64)
+    l[:, :2] = lo, hi
+    return l
+
+
+def _lane(E):
+    """Experts of a lane in the kernels of 16 lanes a token: the length of its sum."""
+    return next(c for c in (4, 8, 16, 32, 64) if 16 * c >= E)
+
+
+@pytest.mark.parametrize("E", [40, 128, 160, 512, 600])
+def test_scores_to_the_last_bits(E):
+    """Roundings of the formulas, an exponential counted as two (1 ulp) at any size of its argument.
+    Sigmoid z / (1 + z): 2 + 1 + 1. Softmax: 2 for the numerator, 2 and its additions (one fewer than a
+    lane's experts, 4 across the lanes) for the sum, 2 for the quotient."""
+    T, k = 50, 5
+    for score, l in (("sigmoid", _whole_logits(T, E, -80, 80)), ("softmax", _whole_logits(T, E, -85, 0))):
+        n = 4 if score == "sigmoid" else 2 + 2 + _lane(E) + 3 + 2
+        tol = n * (1 + 1e-5) * ref64.EPS
+        ri, rw, rs = ref64.route(l, k, score=score, renorm=False)
+        for bias in (None, dev_f32(np.zeros(E))):
+            ids, w, s = moe.moe_router_scored(dev_f32(l), k, bias=bias, score=score, renorm=False, return_scores=True)
+            ids2, w2 = moe.moe_router_scored(dev_f32(l), k, bias=bias, score=score, renorm=False)
+            assert torch.equal(ids, ids2) and torch.equal(w, w2)
+            err = np.abs(s.double().cpu().numpy() - rs) / rs
+            assert err.max() <= tol, (score, err.max() / ref64.EPS, n)
+            werr = np.abs(w.double().cpu().numpy() - rw) / rw
+            assert werr.max() <= tol, (score, werr.max() / ref64.EPS, n)
