@@ -786,11 +786,11 @@ __global__ __launch_bounds__(64 * kWaves) void k_grad_rows(RouterGradArgs a) {
 #pragma unroll
         for (int c = 0; c < C; c++) {
             if (a.sigmoid) {
-                const float z = __expf(-fabsf(l[c])), f = 1.f / (1.f + z);
+                const float z = expf(-fabsf(l[c])), f = 1.f / (1.f + z);
                 s[c] = l[c] > 0.f ? f : z * f;
                 rest[c] = l[c] > 0.f ? z * f : f;
             } else {
-                s[c] = inf ? (l[c] == INFINITY ? 1.f : 0.f) : __expf(l[c] - base);
+                s[c] = inf ? (l[c] == INFINITY ? 1.f : 0.f) : expf(l[c] - base);
                 den += s[c];
             }
         }

@@ -61,3 +61,33 @@ def test_scores_to_the_last_bits(E):
             assert err.max() <= tol, (score, err.max() / ref64.EPS, n)
             werr = np.abs(w.double().cpu().numpy() - rw) / rw
             assert werr.max() <= tol, (score, werr.max() / ref64.EPS, n)
+
+
+@pytest.mark.parametrize("E", [40, 128, 160, 512, 600])
+def test_score_gradient_to_the_last_bits(E):
+    """The gradient through the scores alone. Sigmoid d s (1 - s): one of s and 1 - s is 1 / (1 + z) with
+    3 roundings, the other z / (1 + z) with 4 or, as a product, 5; 2 for the products. Softmax
+    s d - s sum(s d): n for s as above, 1 for s d, n + 1 and the sum's additions for the sum, 1 each for
+    the product and the difference."""
+    T = 50
+    ids = dev_i32(np.full((T, 2), -1))
+    dw = torch.ones((T, 2), device="cuda")
+    d = np.random.default_rng(E).uniform(0.5, 2, size=(T, E)).astype(np.float32)
+    d[:, ::3] *= -1
+    adds = _lane(E) + 3
+    n = 2 + 2 + adds + 2
+    for score, l in (("sigmoid", _whole_logits(T, E, -80, 80)), ("softmax", _whole_logits(T, E, -85, 0))):
+        got = moe.moe_router_scored_backward(dev_f32(l), ids, dw, d_scores=dev_f32(d), score=score)
+        s = ref64.scores(l, score)
+        d64 = d.astype(np.float64)
+        if score == "sigmoid":
+            ref = s / (1 + np.exp(l)) * d64
+            bound = 10 * np.abs(ref)
+        else:
+            q = s * d64
+            mag = np.abs(q).sum(axis=1, keepdims=True)
+            ref = q - s * q.sum(axis=1, keepdims=True)
+            bound = (n + 2) * np.abs(q) + (n + (n + 1 + adds) + 2) * s * mag
+        err = np.abs(got.double().cpu().numpy() - ref)
+        worst = (err / (bound * ref64.EPS)).max()
+        assert worst <= 1 + 1e-5, (score, worst)
