@@ -146,11 +146,12 @@ __device__ __forceinline__ float sigmoid_ratio(float l, float lmax) {
     return expf(l - lmax) * ((1.f + expf(lmax)) / (1.f + expf(l)));
 }
 
-// Routes token t with one wave, in float64. s_key: E words of LDS of this wave's own, s_grp:
-// max(n_group, (k + 1) / 2) more. Loops over a lane's experts stay loops: as the fallback of
+// Routes token t with one wave, in float64; writes its scores if asked to. s_key: E words of LDS of
+// this wave's own, s_grp: max(n_group, (k + 1) / 2) more. Loops over a lane's experts stay loops: as the fallback of
 // k_route_rows this runs rarely and from a cold instruction cache: a launch that needs it for any
 // token ends 11 us later (65536 x 256: 67 against 56 us), so its loops are kept small.
-__device__ __forceinline__ void route_wave(const RouterScoredArgs& a, int64_t t, uint64_t* s_key, uint64_t* s_grp) {
+__device__ __forceinline__ void route_wave(const RouterScoredArgs& a, int64_t t, bool scores, uint64_t* s_key,
+                                           uint64_t* s_grp) {
     const int lane = threadIdx.x & 63;
     const int E = a.E, k = a.k, per = E / a.n_group;
     auto logit = [&](int e) -> float {   // NaN taken as -inf
@@ -184,8 +185,8 @@ __device__ __forceinline__ void route_wave(const RouterScoredArgs& a, int64_t t,
 #pragma unroll 1
     for (int e = lane; e < E; e += 64) {
         const float l = __uint_as_float((uint32_t)s_key[e]);
-        const double s = a.bias || two_orders || a.scores ? score(l) : 0.0;
-        if (a.scores) a.scores[t * E + e] = (float)s;
+        const double s = a.bias || two_orders || scores ? score(l) : 0.0;
+        if (scores) a.scores[t * E + e] = (float)s;
         s_key[e] = !(l > -INFINITY) ? 0 : order_key(a.bias ? s + (double)a.bias[e] : two_orders ? s : (double)l);
     }
     __builtin_amdgcn_wave_barrier();
@@ -280,7 +281,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_scored(RouterScoredArgs 
     const int wv = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * kWaves + wv;
     uint64_t* mine = s_dyn + wv * (a.E + route_extra(a));
-    if (t < a.T) route_wave(a, t, mine, mine + a.E);
+    if (t < a.T) route_wave(a, t, a.scores != nullptr, mine, mine + a.E);
 }
 
 // ---------------------------------------------------------------- 16 lanes a token
@@ -400,7 +401,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
         top = fmaxf(top, l[c]);
     }
     top = row_max(top);
-    bool doubt = top == INFINITY;            // limits are left to the exact form
+    const bool limit = top == INFINITY;      // limits are left to the exact form
+    bool doubt = limit;
     const float base = top > -INFINITY ? top : 0.f;
     float den = 0.f;
     float v[C];                              // scores, then choices
@@ -437,7 +439,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
 #pragma unroll
             for (int c = 0; c < C; c++) v[c] *= f;
         }
-        if (a.scores && live) {
+        if (a.scores && live && !limit) {
 #pragma unroll
             for (int q = 0; q < Q; q++) {
                 const int e = 4 * (r + 16 * q);
@@ -594,17 +596,19 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
     } else {
         w = pick ? expf(pl - base) / den : 0.f;
     }
-    if (live && r < k) {
+    // the exact form for tokens in doubt, one after the other: their picks, and scores only where they
+    // are a limit, so that no score depends on the bias and nothing is written twice
+    uint64_t again = __ballot(doubt && live);
+    const uint64_t limits = a.scores ? __ballot(limit) : 0;
+    if (live && r < k && ((again >> (16 * row)) & 0xffff) == 0) {
         a.ids[t * k + r] = pick ? pe : -1;
         a.w[t * k + r] = a.scale * w;
     }
-    // the exact form for tokens in doubt, one after the other
-    uint64_t again = __ballot(doubt && live);
     while (again) {
         const int which = __builtin_ctzll(again) >> 4;
         again &= ~(0xffffull << (16 * which));
         __builtin_amdgcn_wave_barrier();
-        route_wave(a, t0 + which, s_mem[wv], s_mem[wv] + E);
+        route_wave(a, t0 + which, (limits >> (16 * which)) & 1, s_mem[wv], s_mem[wv] + E);
     }
 }
 

@@ -91,3 +91,24 @@ def test_score_gradient_to_the_last_bits(E):
         err = np.abs(got.double().cpu().numpy() - ref)
         worst = (err / (bound * ref64.EPS)).max()
         assert worst <= 1 + 1e-5, (score, worst)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(40, 5), (256, 8), (512, 15)])
+def test_scores_do_not_depend_on_the_bias(E, k, score):
+    """Tokens whose choices are too near each other are routed again in float64; their scores stay those of
+    the same logits without a bias, bit for bit, infinite logits among them."""
+    T = 45
+    l = np.random.default_rng(E).integers(-3, 3, size=(T, E)).astype(np.float64) / 7     # many ties
+    l = l.astype(np.float32).astype(np.float64)
+    l[0], l[1] = 0.3, -np.inf
+    l[2, 5], l[3, :3] = np.inf, np.inf
+    l[4, ::2] = np.nan
+    dev = dev_f32(l)
+    plain = moe.moe_router_scored(dev, k, score=score, return_scores=True)
+    zero = moe.moe_router_scored(dev, k, bias=torch.zeros(E, device="cuda"), score=score, return_scores=True)
+    small = moe.moe_router_scored(dev, k, bias=dev_f32(np.random.default_rng(1).standard_normal(E) * 1e-7), score=score,
+                                  return_scores=True)
+    for got in (zero, small):
+        assert torch.equal(got[2].view(torch.int32), plain[2].view(torch.int32))
+    assert np.array_equal(zero[0].cpu().numpy(), ref64.route(l, k, bias=np.zeros(E), score=score)[0])
