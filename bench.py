@@ -372,6 +372,15 @@ def bench_gather(args):
     print(json.dumps(res), flush=True)
 
 
+def ffn_path(moe, cfg, T, k, wtype, path, act_quant):
+    """The path a layer call takes. The library's choice reads the widest row, with MXFP4
+    activations the narrowest one, whose GEMV also wants at most 64 rows of shared experts."""
+    width = (min if act_quant == 2 else max)(cfg.n_embd, cfg.n_ff)
+    if act_quant == 2 and path == 0 and cfg.n_shared * T > 64:
+        path = 1
+    return moe.moe_select_path_typed(T, k, cfg.n_experts, width, wtype, path=path, act_quant=act_quant)
+
+
 def prepare_ffn_workload(args, name):
     """Inputs of one FFN workload drawn and made resident in HBM: the weights in R
     copies (rotated through by the steps, so the set a step reads is not served from
@@ -393,8 +402,7 @@ def prepare_ffn_workload(args, name):
     wtype = {"q8_0": moe.MOE_Q8_0, "mxfp4": moe.MOE_MXFP4, "iq4_nl": moe.MOE_IQ4_NL,
              "iq4_xs": moe.MOE_IQ4_XS}[cfg.wtype]
     aq = args.act_quant
-    path = moe.moe_select_path_typed(T, k, cfg.n_experts, max(cfg.n_embd, cfg.n_ff), wtype,
-                                     path=args.path, act_quant=aq)
+    path = ffn_path(moe, cfg, T, k, wtype, args.path, aq)
     st = workload_stats(inp, cfg, 4 if path in (2, 5) else 17 / 32 if path == 4 else 2)
     R = args.rotate or (1 if st["bytes"] > 2e9 else max(4, int(np.ceil(1.2e9 / st["bytes"]))))
     sets = []

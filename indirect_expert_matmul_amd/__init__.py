@@ -288,6 +288,8 @@ def moe_select_path(n_tokens: int, n_used: int, n_experts: int, act_width: int,
 
 def moe_select_path_typed(n_tokens: int, n_used: int, n_experts: int, act_width: int, weight_type: int,
                           path: int = PATH_AUTO, tau: float = 0.0, act_quant: int = 0) -> int:
+    """The path a call takes: 1 to 5, as in moe.h. ``act_width`` is the widest activation row, with
+    ``act_quant=2`` the narrowest."""
     r = lib.moe_select_path_typed(n_tokens, n_used, n_experts, act_width, weight_type,
                                   ctypes.byref(_options(path, tau, act_quant=act_quant)))
     if r < 0:
