@@ -29,6 +29,9 @@ pytestmark = pytest.mark.gpu
     (13, 512, 16, 16, 1, 2, True),           # past the picks of 16 lanes a token
     (9, 511, 9, 7, 3, 2, True),              # rows that start anywhere
     (5, 1024, 9, 1024, 700, 1, True),        # as many groups as experts
+    (19, 16, 5, 16, 5, 2, True),
+    (19, 16, 3, 16, 9, 2, False),
+    (19, 30, 7, 15, 4, 2, False),            # groups of two
 ])
 def test_route_instances(T, E, k, G, keep, top, bias, score, dtype):
     dev, l = _logits(T, E, T + E + k, dtype)
@@ -139,6 +142,28 @@ def test_gemv_with_several_row_groups_and_passes():
 ])
 def test_ffn_gemv_with_several_row_groups(E, k, T, n_embd, n_ff, S):
     _ffn_case(E, k, T, n_embd, n_ff, S, _spread(T, k, max(E, T * k), n_ff) % (E + 1), path=moe.PATH_GEMV)
+
+
+@pytest.mark.parametrize("path", [moe.PATH_GEMV, moe.PATH_GEMM])
+@pytest.mark.parametrize("T,n_embd,n_ff,n_ff_sh,S", [
+    (7, 256, 128, 1184, 2),           # shared experts wider than the routed ones: parts of the columns are theirs alone
+    (7, 256, 1184, 128, 2),           # and narrower
+    (1, 192, 160, 2080, 1),           # one token, the slots summed by the down product
+    (1, 192, 2080, 160, 3),
+    (60, 352, 320, 704, 1),
+    (12, 544, 1696, 2720, 1),
+])
+def test_shared_experts_of_another_width(T, n_embd, n_ff, n_ff_sh, S, path):
+    E, k = 5, 1 if T == 60 else 2
+    st = [_experts(E, n_ff, n_embd, 1), _experts(E, n_ff, n_embd, 2), _experts(E, n_embd, n_ff, 3)]
+    sh = [_experts(S, n_ff_sh, n_embd, 4), _experts(S, n_ff_sh, n_embd, 5), _experts(S, n_embd, n_ff_sh, 6)]
+    dx, x = _act(T, n_embd, T)
+    rng = np.random.default_rng(T + n_ff)
+    ids = rng.integers(-1, E, size=(T, k)).astype(np.int32)
+    rw = rng.uniform(0, 1, size=(T, k)).astype(np.float32)
+    up = lambda ws: [moe.Weights(torch.from_numpy(c).cuda(), torch.from_numpy(s).cuda()) for c, s, _ in ws]
+    got = moe.moe_ffn_fused(*up(st), dx, dev_i32(ids), dev_f32(rw), shared=up(sh), act_quant=2, path=path)
+    _check(got, *ref64.ffn(x, *(v for _, _, v in st), ids, rw, [v for _, _, v in sh]))
 
 
 @pytest.mark.parametrize("path", [moe.PATH_GEMV, moe.PATH_GEMM])
