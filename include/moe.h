@@ -133,7 +133,9 @@ typedef struct {
      * 2^31 - 512, rows of activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's
      * codes under 4 GiB (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
      * grouped GEMM][, reduce]; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
-     * weighted calls too large to sum inside the GEMV. */
+     * weighted calls too large to sum inside the GEMV. For the FFN of a single token this is
+     * slower than bf16 activations (27 against 22 us on 4 experts of 2880 x 2880): every
+     * thread block quantizes the row again. */
     int32_t act_quant;
     int32_t reserved[5];
     void *const *timing_events;

@@ -27,7 +27,8 @@
 //     of its 16 rows in a few rounds of its waves (one token 2880 x 2880, 4 experts: 11.8 us, against
 //     9.1 and 4 for the sum's launch); else the per-slot rows go through the workspace to the
 //     reduce kernel.
-// Measured: 4 experts of 2880 x 2880 9.1 us (17.6 MB: the launch and one memory round trip), 8
+// Measured: 4 experts of 2880 x 2880 9.3 us (17.6 MB: the launch and two memory
+// round trips, the ids and then codes and activations), 8
 // tokens x 4 of 32 28 us (3.3 TB/s, one round of blocks), 64 slots of 128 experts of 2048 x 7168
 // 92 us (4.4 TB/s).
 #include <algorithm>

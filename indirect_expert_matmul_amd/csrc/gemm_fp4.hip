@@ -31,9 +31,13 @@
 //     which leave part of the rows in the caches (sum: 40 us against 43).
 //
 // Measured (this kernel alone): 4096 tokens x 8 slots, 128 experts of 2048 x 7168, 474 us, 2030
-// TFLOP/s; 4096 x 4, 32 experts of 2880 x 2880, 189 us, 1440 TFLOP/s. Bound by the copies: the
-// first takes 297 us without them and 450 with them and one MFMA in eight (3.5 GB from L2 to
-// LDS in requests of 64 bytes, 1.4 GB from HBM). Tried and slower at these two sizes: 128 x 128 tiles 507 and 196;
+// TFLOP/s; 4096 x 4, 32 experts of 2880 x 2880, 189 us, 1440 TFLOP/s. No pipe is full in the first: MFMA
+// pipes busy 23 % of the cycles, LDS 12 %, L2 to LDS 15 bytes a clock and CU of the 57 that such rows
+// reach (3.5 GB in requests of 64 bytes, 1.4 GB from HBM). It takes 297 us without the copies and 450 with
+// them and one MFMA in eight: what bounds it is waiting for them, once per 128 columns, with 512 cycles
+// of MFMA per wave between two waits. Segments of a few rows over a multiple of 128 take one more tile, with
+// all of its weight copies (uniform ids: 320 tiles for 256, 146 for 128). Tried and slower at these two
+// sizes: 128 x 128 tiles 507 and 196;
 // weights from global memory straight into MFMA registers 604 and 210; 256 x 256 tiles with
 // 8 waves 497 and 183; persistent blocks 506 and 185.
 #include <type_traits>

@@ -165,10 +165,11 @@ int select_path_fmt(int64_t T, int32_t k, int32_t E, int64_t act_width, bool fp4
 // grouped GEMM) or 5 (its GEMV), else the choice above; or a negative status. S: shared
 // experts; min_width: the narrowest activation row.
 // With MXFP4 activations the GEMV is taken wherever it can run, up to 16 slots an expert on
-// average, which is one of its passes (mul_mat_id, GEMV against GEMM in us on one MI355X: E32 k4
-// 2880 x 2880 T = 1 9.2 / 20.7, T = 16 42 / 51; E64 k6 1408 x 2048 T = 10 17.5 / 22.5; E128 k8
-// 2048 x 7168 T = 1 18.5 / 37, T = 8 92 / 99; E8 k2 4096 x 4096 T = 32 23.8 / 33; 16 slots an
-// expert, E4 k1 2880 x 2880 T = 64, 23.7 / 23.4; 32 of them, E2 k2 1024 x 1024 T = 32, 19.7 / 13.3).
+// average, which is one of its passes (mul_mat_id, GEMV against GEMM in us per call on one MI355X, weight
+// copies in turn: E32 k4 2880 x 2880 T = 1 10.9 / 21.7, T = 16 42.8 / 51.0; E64 k6 1408 x 2048 T = 10
+// 18.1 / 24.7; E128 k8 2048 x 7168 T = 1 20.2 / 47.4, T = 8 98 / 104; E8 k2 4096 x 4096 T = 32
+// 23.2 / 32.3; 16 slots an expert, E4 k1 2880 x 2880 T = 64, 23.7 / 30.6; 32 of them, E2 k2 1024 x 1024
+// T = 32, 20.9 / 14.4).
 int select_path_aq(int64_t T, int32_t k, int32_t E, int64_t act_width, int32_t wtype,
                    const moe_options* o, int64_t S, int64_t min_width) {
     const int32_t aq = o ? o->act_quant : 0;

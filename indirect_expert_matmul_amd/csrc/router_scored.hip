@@ -6,8 +6,11 @@
 //     token, four tokens a wave, so that every reduction is four row rotations and no LDS
 //     crossbar. Choices are float32 first: each is at most kErr from the exact one, so
 //     picks and groups whose neighbours in the order are further apart than twice that are
-//     the exact ones. The rest (about one token in a thousand of random logits) are routed
-//     again in float64 by the whole wave.
+//     the exact ones. The rest are routed again in float64 by the whole wave: about one token
+//     in a thousand of random float32 logits; with a bias also every token whose last pick ties
+//     with the first expert left, or whose last group does, exactly (65536 x 256 bf16 with a
+//     bias of zeros 69 us against 44 with a random one, 8 groups 100 against 67; all logits
+//     equal 189 and 277).
 //       - a lane holds chunks of four experts (chunk lane + 16 q), loaded 16 bytes at a time;
 //       - a choice and its expert become one float64 integer, key * 1024 + 1023 - e, whose
 //         order is that of the choices, lower expert first: one v_max_f64 compares both;
@@ -32,9 +35,12 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;  // waves per block
 // Twice how far a float32 choice may be from the exact one (k_route_rows). Sigmoid: z = exp(-|l|) is
 // off by |l| 2^-23 + 2^-22 relative, which moves the score by s (1 - s) of that, and the quotient
-// rounds three times: under 2^-21 in all. Softmax: exp(l - top) likewise, s (top - l) < 0.4, and a
-// sum of up to 36 additions in a row of lanes, 36 * 2^-24 relative, the same for all scores of a
-// token: under 2^-18.7. Adding the bias rounds once more, relative to the sum.
+// rounds three times: under 2^-21 in all. Softmax, in units of 2^-23 relative: exp(x), x = l - top, off
+// by 1.13 |x| + 1 (the difference, the product with log2(e) and that constant, 2^x); the sum by the mean
+// of that over the scores, where the mean of |x| is under 3.9 for 512 experts, so 5.4, and by half a unit
+// for each of 35 additions (31 of a lane's 32 experts, 4 across the lanes), 17.5; reciprocal and product
+// 1; the score's own s (1.13 |x| + 1) at most 1.1. In all 25, or 2^-18.3, of which twice is 0.78 of
+// kErrSoftmax. Adding the bias rounds once more, relative to the sum.
 constexpr float kErrSigmoid = 0x1p-20f, kErrSoftmax = 0x1p-17f, kErrSum = 0x1p-22f;
 
 template <int N>
@@ -286,6 +292,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_router_scored(RouterScoredArgs 
 
 // ---------------------------------------------------------------- 16 lanes a token
 constexpr int kRowExperts = 512, kRowPicks = 15, kRowGroups = 16;
+static_assert(kRowExperts <= 512, "kErrSoftmax counts the additions and the mean for 512 experts");
 
 // No NaN comes here, so the instructions need no quieting of their inputs before them.
 __device__ __forceinline__ double bigger(double a, double b) {
