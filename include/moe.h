@@ -128,10 +128,10 @@ typedef struct {
      * scaled FP4 MFMA, fp32 accumulation. The fused FFN quantizes x before gate/up and the
      * float32 h before down. GEMV path: n_tokens * n_used <= 64, n_tokens * shared experts <=
      * 64, every row at least 128 columns wide; path 0 takes it there while n_tokens * n_used <=
-     * 16 * n_experts; tau is not read. The two paths add the same products in different orders. x / src1 and
-     * the experts' codes must be 16-byte aligned (MOE_EINVAL); cols < 2^24, rows <
-     * 2^31 - 512, rows of activations * cols / 32 < 2^31 and, on the grouped GEMM, src1's
-     * codes under 4 GiB (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
+     * 16 * n_experts; tau is not read. The two paths add the same products in different orders. x / src1,
+     * the experts' codes and the workspace must be 16-byte aligned (MOE_EINVAL); cols < 2^24,
+     * rows < 2^31 - 512, rows of activations * cols / 32 < 2^31 and, on the grouped GEMM,
+     * src1's codes under 4 GiB (MOE_ELIMIT). Kernel order for timing: row ids with quantize and fix-up, grouped GEMM[, down
      * grouped GEMM][, reduce]; GEMV path: GEMV[, down GEMV][, reduce], the reduce only in
      * weighted calls too large to sum inside the GEMV. For the FFN of a single token this is
      * slower than bf16 activations (27 against 22 us on 4 experts of 2880 x 2880): every

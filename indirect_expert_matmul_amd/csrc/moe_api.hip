@@ -831,6 +831,7 @@ moe_status moe_ffn_fused(const moe_weights* gate, const moe_weights* up, const m
     Carve sz(nullptr);
     carve_ffn(sz, d, path);
     if (sz.off > ws_bytes || !ws) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
+    if ((path == 4 || path == 5) && (s = check_fp4_act(ws, "the workspace"))) return s;
     Carve c(ws);
     const FfnPlan p = carve_ffn(c, d, path);
     const hipStream_t st = (hipStream_t)stream;
@@ -1182,6 +1183,7 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
     Carve sz(nullptr);
     carve_mmid(sz, n_tokens, k, E, N, weighted, q8, path, B, K);
     if (sz.off > ws_bytes || (sz.off && !ws)) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
+    if ((path == 4 || path == 5) && (s = check_fp4_act(ws, "the workspace"))) return s;
     Carve c(ws);
     const MmidPlan p = carve_mmid(c, n_tokens, k, E, N, weighted, q8, path, B, K);
     const hipStream_t st = (hipStream_t)stream;

@@ -41,3 +41,17 @@ def test_rows_limit(path):
         assert moe.lib.moe_mul_mat_id(ctypes.byref(m), FAKE, moe.MOE_BF16, 1, FAKE, 1, 1, None, FAKE,
                                       ctypes.byref(opt), FAKE, 1 << 60, None) == moe.MOE_ELIMIT
         assert "2^31" in moe.last_error()
+
+
+@pytest.mark.parametrize("path", [moe.PATH_GEMV, moe.PATH_GEMM])
+def test_workspace_alignment(path):
+    """The codes of activations and of h lie in the workspace and are copied 16 bytes at a time."""
+    m = moe.c_moe_weights(moe.MOE_MXFP4, FAKE, FAKE, 4, 128, 128)
+    opt, r = moe._options(path, act_quant=2), ctypes.byref
+    for off in (1, 4, 8):
+        assert moe.lib.moe_mul_mat_id(r(m), FAKE, moe.MOE_BF16, 1, FAKE, 9, 2, FAKE, FAKE, r(opt), FAKE + off, 1 << 40,
+                                      None) == moe.MOE_EINVAL
+        assert "workspace" in moe.last_error()
+        assert moe.lib.moe_ffn_fused(r(m), r(m), r(m), None, None, None, FAKE, moe.MOE_BF16, FAKE, FAKE, 9, 2, FAKE,
+                                     r(opt), FAKE + off, 1 << 40, None) == moe.MOE_EINVAL
+        assert "workspace" in moe.last_error()
