@@ -321,13 +321,20 @@ __device__ __forceinline__ float row_sum(float v) {   // the same bits in every 
 }
 // exp of x <= 0 to an ulp, subnormal results included: x log2(e) = n + t with n whole and |t| <= 1/2,
 // then 2^t and n into the exponent. 8 instructions (expf: 13, for the range that does not come here;
-// 65536 x 256 gradients 45 us with this, 47 with expf); __expf rounds x log2(e), which is off by
+// 65536 x 256 sigmoid gradients 45 us with this, 47 with expf); __expf rounds x log2(e), which is off by
 // |x| 2^-24 relative.
 __device__ __forceinline__ float exp_neg(float x) {
     x = fmaxf(x, -110.f);   // 0 from here on
     const float n = __builtin_rintf(x * 0x1.715476p+0f);
     const float t = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -n));   // log2(e) in two parts
     return ldexpf(__builtin_amdgcn_exp2f(t), (int)n);
+}
+// 1 / d of d in [1, 2]: v_rcp (an ulp) and a Newton step, which leaves the rounding of the last fma. (A
+// quotient takes 10 instructions, for operands that do not come here: 65536 x 256 sigmoid gradients 45.3
+// us, with this 43.6.)
+__device__ __forceinline__ float recip_1_2(float d) {
+    const float f = __builtin_amdgcn_rcpf(d);
+    return fmaf(f, fmaf(-d, f, 1.f), f);
 }
 // Order key of a float32 choice as above; float of a key.
 __device__ __forceinline__ uint32_t order_key(float c) {
@@ -814,7 +821,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_grad_rows(RouterGradArgs a) {
 #pragma unroll
         for (int c = 0; c < C; c++) {
             if (a.sigmoid) {
-                const float z = exp_neg(-fabsf(l[c])), f = 1.f / (1.f + z);
+                const float z = exp_neg(-fabsf(l[c])), f = recip_1_2(1.f + z);
                 s[c] = l[c] > 0.f ? f : z * f;
                 rest[c] = l[c] > 0.f ? z * f : f;
             } else {
