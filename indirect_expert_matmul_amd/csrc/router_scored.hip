@@ -9,8 +9,8 @@
 //     the exact ones. The rest are routed again in float64 by the whole wave: about one token
 //     in a thousand of random float32 logits; with a bias also every token whose last pick ties
 //     with the first expert left, or whose last group does, exactly (65536 x 256 bf16 with a
-//     bias of zeros 69 us against 44 with a random one, 8 groups 100 against 67; all logits
-//     equal 189 and 277).
+//     bias of zeros 67 us against 42 with a random one, 8 groups 98 against 65; all logits
+//     equal 186 and 273).
 //       - a lane holds chunks of four experts (chunk lane + 16 q), loaded 16 bytes at a time;
 //       - a choice and its expert become one float64 integer, key * 1024 + 1023 - e, whose
 //         order is that of the choices, lower expert first: one v_max_f64 compares both;
@@ -638,7 +638,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_route_rows(RouterScoredArgs a) 
 // j has pick j; picks of one expert are added up by the first of them (in a fixed order) and
 // each pick's value goes to its expert through a row of LDS. Without dS only the picks of a
 // sigmoid or of renormalised weights have a gradient, so the logits' rows are not read.
-// Bound by memory: 65536 x 256 float32 with a full dS move 206 MB in 47 us, 4.4 TB/s (one wave
+// Bound by memory: 65536 x 256 float32 with a full dS move 206 MB in 44 us, 4.7 TB/s (one wave
 // a token with the experts strided over its lanes took 88).
 // k_router_grad (other sizes): one wave a token.
 template <int NC>
