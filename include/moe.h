@@ -35,6 +35,10 @@
  *            (bytes 4-7); block j (0..7) of the 256 has the 6-bit sub-scale ls = (nibble
  *            j%2 of scales_l[j/2], low nibble first) | ((scales_h >> 2j) & 3) << 4, and
  *            value = d * (ls - 32) * level(code). cols % 256 == 0.
+ *            BF16, F16 (moe_mul_mat_id and its gradients): 16-bit values as they are,
+ *            cols % 8 == 0, 16-byte aligned. I8 (moe_mul_mat_id; what moe_quantize_rows
+ *            makes): int8 q[n_mat][rows][cols] and float32 d[n_mat][rows], value = d * q,
+ *            cols % 16 == 0, cols <= 131072, 16-byte aligned.
  *   ids      int32 [n_tokens][n_used]; route_w float32 [n_tokens][n_used].
  *   src1     [n_tokens][B][K] with B = src1_rows_per_token in {1, n_used}:
  *            slot s of token t reads row t*B + (s mod B).
@@ -64,9 +68,10 @@
  *
  * Limits (MOE_ELIMIT): n_tokens < 2^22 and n_used < 2^10 (the bounds the page
  * above quotes for safe 32-bit packing, section 2.1), n_tokens * n_used < 2^31,
- * n_experts <= 1024, Q8_0, MXFP4 and IQ4_NL cols % 32 == 0, IQ4_XS cols % 256 == 0. On the grouped GEMM path the
+ * n_experts <= 1024, Q8_0, MXFP4 and IQ4_NL cols % 32 == 0, IQ4_XS cols % 256 == 0, BF16 and
+ * F16 cols % 8 == 0, I8 cols % 16 == 0 and <= 131072. On the grouped GEMM path the
  * activation tensor whose rows are gathered through the row map (moe_ffn_fused: x;
- * moe_mul_mat_id: src1) must be under 4 GiB, and each GEMM launch must hold fewer
+ * moe_mul_mat_id with quantized experts: src1) must be under 4 GiB, and each GEMM launch must hold fewer
  * than 2^32 work-items; float32 moe_mul_mat_id needs n_tokens * n_used * N < 2^32.
  */
 #ifndef MOE_H
@@ -87,16 +92,23 @@ typedef enum {
     MOE_EHIP = -4        /* a HIP launch failed                                    */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_Q8_0 = 2, MOE_MXFP4 = 3, MOE_IQ4_NL = 4, MOE_IQ4_XS = 5 } moe_dtype;
+typedef enum {
+    MOE_F32 = 0, MOE_BF16 = 1, MOE_Q8_0 = 2, MOE_MXFP4 = 3, MOE_IQ4_NL = 4, MOE_IQ4_XS = 5,
+    MOE_F16 = 6, /* IEEE half: activations, experts, gradients                     */
+    MOE_I8 = 7   /* experts: int8 with one float32 scale per output row            */
+} moe_dtype;
 
 /* n_mat stacked matrices of rows x cols. */
 typedef struct {
-    moe_dtype type;     /* MOE_F32, MOE_Q8_0, MOE_MXFP4, MOE_IQ4_NL, MOE_IQ4_XS  */
+    moe_dtype type;     /* MOE_F32, MOE_Q8_0, MOE_MXFP4, MOE_IQ4_NL, MOE_IQ4_XS; */
+                        /* moe_mul_mat_id also MOE_BF16, MOE_F16, MOE_I8         */
     const void *data;   /* F32: float[n_mat][rows][cols]; Q8_0: int8 qs[...];    */
+                        /* BF16, F16: 16-bit [n_mat][rows][cols]; I8: int8 [...]; */
                         /* MXFP4, IQ4_NL, IQ4_XS: uint8 codes[n_mat][rows][cols/2] */
     const void *scales; /* Q8_0, IQ4_NL: uint16 (fp16) d[n_mat][rows][cols/32];  */
                         /* MXFP4: uint8 E8M0 x[n_mat][rows][cols/32];            */
-                        /* IQ4_XS: uint8 records[n_mat][rows][cols/256][8]; F32: NULL */
+                        /* IQ4_XS: uint8 records[n_mat][rows][cols/256][8];      */
+                        /* I8: float d[n_mat][rows]; F32, BF16, F16: NULL        */
     int64_t n_mat, rows, cols;
 } moe_weights;
 
@@ -183,7 +195,13 @@ moe_status moe_gather_rows(const void *src1, moe_dtype src1_type, int64_t src1_r
  *            n_used <= 64 and K <= 4096, else the GEMM path is taken, and forcing the
  *            GEMV path is MOE_EINVAL); (F32 w, F32
  *            src1), which has one path, the fp32 grouped product: opt->path must be
- *            0 or 1 (else MOE_EINVAL).
+ *            0 or 1 (else MOE_EINVAL); (BF16 w, BF16 src1) and (F16 w, F16 src1), products
+ *            of the 16-bit values summed in float32; (I8 w; BF16, F16 or F32 src1): each row of
+ *            src1 is quantized as moe_quantize_rows does and
+ *              row[n] = d_row * d_w[n] * sum over the columns of q_row * q_w[n]
+ *            with the sum exact in int32 (rows of src1 with an infinity or a NaN give NaN).
+ *            BF16, F16 and I8: src1, w's data and the workspace 16-byte aligned
+ *            (MOE_EINVAL), rows and cols < 2^30, opt->act_quant 0.
  *   src1     device [n_tokens][B][K], B = src1_rows_per_token in {1, n_used}
  *   ids      device int32 [n_tokens][n_used]
  *   route_w  NULL: dst = float32 [n_tokens][n_used][N], dst[t][s] = W_{ids[t][s]} src1_row;
@@ -195,6 +213,36 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
                           int32_t src1_rows_per_token, const int32_t *ids, int64_t n_tokens,
                           int32_t n_used, const float *route_w, float *dst, const moe_options *opt,
                           void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_mul_mat_id_backward -- the gradients of moe_mul_mat_id with BF16 or F16 experts. With slot
+ * i = (t, s) of expert e, r = t*B + (s mod B) its src1 row, w_i = route_w[t][s] (1 without
+ * route_w) and dy_i = d_dst[t][s] (with route_w: d_dst[t]):
+ *   d_src1[r]    = sum over r's slots, ascending, of w_i * g_i,   g_i[k] = sum_n dy_i[n] W_e[n][k]
+ *   d_w[e]       = sum over e's slots of w_i * dy_i (outer) src1[r]
+ *   d_route_w[i] = sum_k g_i[k] * src1[r][k]   ( = the inner product of d_dst[t] and slot i's row)
+ * Slots with invalid ids have no part in any sum: their d_route_w is 0, and with B = n_used their
+ * d_src1 rows; experts without slots get a d_w of zeros, also with n_tokens = 0.
+ *   w            BF16 or F16, n_mat = n_experts, rows = N, cols = K
+ *   src1         device [n_tokens][B][K] of w's type; ids, route_w as in the forward call
+ *   d_dst        device [n_tokens][n_used][N], with route_w [n_tokens][N]; of w's type, or F32,
+ *                which is rounded once to w's type
+ *   d_src1       NULL (not wanted), or device [n_tokens][B][K] of w's type (written, summed in
+ *                float32 and rounded once)
+ *   d_w          NULL, or device [n_experts][N][K] (written), d_w_type: w's type or F32. With route_w
+ *                the rows w_i * dy_i are rounded to w's type before they are multiplied
+ *   d_route_w    NULL, or device float32 [n_tokens][n_used] (written); needs route_w
+ * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
+ * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
+ * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids[, round d_dst][, rows of g]
+ * [, join or zero rows][, experts' gradient].
+ */
+moe_status moe_mul_mat_id_backward(const moe_weights *w, const void *src1, moe_dtype src1_type,
+                                   int32_t src1_rows_per_token, const int32_t *ids,
+                                   int64_t n_tokens, int32_t n_used, const float *route_w,
+                                   const void *d_dst, moe_dtype d_dst_type, void *d_src1, void *d_w,
+                                   moe_dtype d_w_type, float *d_route_w, const moe_options *opt,
+                                   void *ws, size_t ws_bytes, void *stream);
 
 /*
  * moe_ffn_fused -- MoE FFN layer on the indirect matmul: the gate and up projections
@@ -261,6 +309,19 @@ moe_status moe_ffn_fused_noalloc(const moe_weights *gate, const moe_weights *up,
  */
 moe_status moe_quantize_act(const void *x, moe_dtype x_type, int64_t rows, int64_t K, int8_t *q,
                             float *d, void *stream);
+
+/*
+ * moe_quantize_rows -- rows to int8 with one float32 scale each: the activation format of
+ * moe_mul_mat_id with I8 experts, and the way to make such experts from float32 or 16-bit ones
+ * (rows = n_mat * rows of the matrices). d = max|x| / 127 over the row and q = x / d rounded to the
+ * nearest integer, ties to even (float32 division and rounding; clamped to [-127, 127]); d = 0 and
+ * q = 0 for a row of zeros, d = NaN and q = 0 for one with an infinity or a NaN. Value = d * q.
+ *   x   device BF16, F16 or F32 [rows][K], any K > 0
+ *   q   device int8 [rows][K] (written); d device float32 [rows] (written)
+ * rows = 0 is a no-op. No workspace. Deterministic.
+ */
+moe_status moe_quantize_rows(const void *x, moe_dtype x_type, int64_t rows, int64_t K, int8_t *q,
+                             float *d, void *stream);
 
 /*
  * moe_router_topk -- the step ahead of the op: the ids table the op consumes (section
@@ -381,6 +442,11 @@ size_t moe_row_ids_workspace_size(int64_t n_tokens, int32_t n_used, int32_t n_ex
 size_t moe_mul_mat_id_workspace_size(const moe_weights *w, moe_dtype src1_type,
                                      int32_t src1_rows_per_token, int64_t n_tokens,
                                      int32_t n_used, const moe_options *opt);
+/* want: 1 d_src1, 2 d_w, 4 d_route_w, added up; weighted: route_w is given */
+size_t moe_mul_mat_id_backward_workspace_size(const moe_weights *w, moe_dtype d_dst_type,
+                                              int32_t src1_rows_per_token, int64_t n_tokens,
+                                              int32_t n_used, int32_t weighted, int32_t want,
+                                              const moe_options *opt);
 size_t moe_ffn_fused_workspace_size(const moe_weights *gate, const moe_weights *sh_gate,
                                     moe_dtype x_type, int64_t n_tokens, int32_t n_used,
                                     const moe_options *opt);

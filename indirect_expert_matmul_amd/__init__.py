@@ -24,7 +24,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_EINVAL, MOE_ELIMIT, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4
-MOE_F32, MOE_BF16, MOE_Q8_0, MOE_MXFP4, MOE_IQ4_NL, MOE_IQ4_XS = 0, 1, 2, 3, 4, 5
+MOE_F32, MOE_BF16, MOE_Q8_0, MOE_MXFP4, MOE_IQ4_NL, MOE_IQ4_XS, MOE_F16, MOE_I8 = 0, 1, 2, 3, 4, 5, 6, 7
 PATH_AUTO, PATH_GEMM, PATH_GEMV = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}   # moe_score
 
@@ -34,7 +34,8 @@ EXPORTS = ("moe_row_ids", "moe_mul_mat_id", "moe_ffn_fused", "moe_router_topk",
            "moe_ffn_fused_workspace_size", "moe_select_path", "moe_select_path_typed",
            "moe_status_string", "moe_last_error",
            "moe_last_stage_count", "moe_ffn_fused_noalloc", "moe_quantize_act", "moe_gather_rows",
-           "moe_quantize_mxfp4", "moe_router_scored", "moe_router_scored_backward")
+           "moe_quantize_mxfp4", "moe_router_scored", "moe_router_scored_backward",
+           "moe_mul_mat_id_backward", "moe_mul_mat_id_backward_workspace_size", "moe_quantize_rows")
 
 NOALLOC_SCRATCH_BYTES = 64 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 
@@ -81,7 +82,13 @@ def _load():
     lib.moe_quantize_mxfp4.argtypes = [P, ctypes.c_int, I64, I64, P, P, P, P]
     lib.moe_router_scored.argtypes = [P, ctypes.c_int, P, I64, I32, I32, C, P, P, P, P]
     lib.moe_router_scored_backward.argtypes = [P, ctypes.c_int, P, P, P, I64, I64, I32, I32, C, P, P]
-    for f in (lib.moe_row_ids, lib.moe_mul_mat_id, lib.moe_ffn_fused, lib.moe_router_topk,
+    lib.moe_mul_mat_id_backward.argtypes = [W, P, ctypes.c_int, I32, P, I64, I32, P, P, ctypes.c_int, P, P,
+                                            ctypes.c_int, P, O, P, SZ, P]
+    lib.moe_quantize_rows.argtypes = [P, ctypes.c_int, I64, I64, P, P, P]
+    lib.moe_mul_mat_id_backward_workspace_size.argtypes = [W, ctypes.c_int, I32, I64, I32, I32, I32, O]
+    lib.moe_mul_mat_id_backward_workspace_size.restype = SZ
+    for f in (lib.moe_mul_mat_id_backward, lib.moe_quantize_rows,
+              lib.moe_row_ids, lib.moe_mul_mat_id, lib.moe_ffn_fused, lib.moe_router_topk,
               lib.moe_ffn_fused_noalloc, lib.moe_quantize_act, lib.moe_gather_rows,
               lib.moe_quantize_mxfp4, lib.moe_router_scored, lib.moe_router_scored_backward):
         f.restype = ctypes.c_int
@@ -133,15 +140,19 @@ class Weights:
     [n_mat][rows][cols/2] (two E2M1 codes per byte, even column in the low nibble) and
     ``scales`` uint8 E8M0 [n_mat][rows][cols/32]; IQ4_NL: ``data`` uint8 codes packed as
     MXFP4's and ``scales`` float16 (or its 16 bits) [n_mat][rows][cols/32]; IQ4_XS: ``data``
-    as IQ4_NL's and ``scales`` uint8 super-block records [n_mat][rows][cols/256][8]; F32:
-    ``data`` float32 [n_mat][rows][cols] and ``scales`` None."""
+    as IQ4_NL's and ``scales`` uint8 super-block records [n_mat][rows][cols/256][8]; F32, BF16
+    and F16: ``data`` float32, bfloat16 or float16 [n_mat][rows][cols] and ``scales`` None; I8:
+    ``data`` int8 [n_mat][rows][cols] and ``scales`` float32 [n_mat][rows] (moe_quantize_rows
+    makes both). BF16, F16 and I8 are experts of moe_mul_mat_id, not of the fused FFN."""
     data: torch.Tensor
     scales: Optional[torch.Tensor] = None
 
     @property
     def type(self) -> int:
         if self.scales is None:
-            return MOE_F32
+            return {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}.get(self.data.dtype, MOE_F32)
+        if self.data.dtype == torch.int8 and self.scales.dtype == torch.float32:
+            return MOE_I8
         if self.data.dtype == torch.uint8:
             if self.scales.element_size() != 1:
                 return MOE_IQ4_NL
@@ -157,8 +168,11 @@ class Weights:
         if d.dim() != 3:
             raise ValueError("weights must be [n_mat][rows][cols]")
         if self.scales is None:
-            if d.dtype != torch.float32:
-                raise ValueError("float weights must be float32")
+            if d.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+                raise ValueError("float weights must be float32, bfloat16 or float16")
+        elif self.type == MOE_I8:
+            if tuple(self.scales.shape) != tuple(d.shape[:2]) or not self.scales.is_contiguous():
+                raise ValueError("int8 weights: contiguous float32 scales [n_mat][rows]")
         else:
             if d.dtype == torch.uint8:
                 if self.scales.dtype != torch.uint8 and self.scales.element_size() != 2:
@@ -169,7 +183,8 @@ class Weights:
                                                                             2 * d.shape[2] // 256, 8)):
                     raise ValueError("IQ4_XS records must be uint8 [n_mat][rows][cols/256][8]")
             elif d.dtype != torch.int8 or self.scales.element_size() != 2:
-                raise ValueError("Q8_0 weights: int8 qs with 16-bit scales")
+                raise ValueError("Q8_0 weights: int8 qs with 16-bit scales (int8 weights with a scale a row: "
+                                 "float32 scales)")
             if not self.scales.is_contiguous():
                 raise ValueError("scales must be contiguous")
         if not d.is_contiguous():
@@ -224,6 +239,11 @@ def _xtype(t: torch.Tensor) -> int:
     if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
         return MOE_BF16
     raise ValueError("activations must be float32 or bfloat16 (or its 16-bit patterns)")
+
+
+def _elem_type(t: torch.Tensor) -> int:
+    """_xtype, float16 too."""
+    return MOE_F16 if t.dtype == torch.float16 else _xtype(t)
 
 
 def _workspace(nbytes: int, device, ws: Optional[torch.Tensor], stream=None):
@@ -352,6 +372,23 @@ def moe_quantize_act(x: torch.Tensor, stream=None):
     _keep_alive(stream, q, d)
     _check(lib.moe_quantize_act(x.data_ptr(), _xtype(x), rows, K, q.data_ptr(), d.data_ptr(),
                                 _stream(stream)), "moe_quantize_act")
+    return q, d
+
+
+def moe_quantize_rows(x: torch.Tensor, stream=None):
+    """(q int8 [..., K], d float32 [...]) of the rows of x [..., K] (float32, bfloat16 or its 16-bit
+    patterns, or float16): int8 codes with one scale a row, d = max|x| / 127; a 3-D x gives the two
+    tensors of int8 ``Weights``."""
+    if x.dim() < 2 or x.shape[-1] == 0:
+        raise ValueError("x must be [..., K]")
+    _dev_check(x)
+    _check_device(stream, x)
+    K = x.shape[-1]
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    d = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _keep_alive(stream, q, d)
+    _check(lib.moe_quantize_rows(x.data_ptr(), _elem_type(x), x.numel() // K, K, q.data_ptr(), d.data_ptr(),
+                                 _stream(stream)), "moe_quantize_rows")
     return q, d
 
 
@@ -515,7 +552,9 @@ def moe_mul_mat_id(w: Weights, src1: torch.Tensor, ids: torch.Tensor,
                    path: int = PATH_AUTO, tau: float = 0.0, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None, events=None,
                    act_quant: int = 0):
-    """GGML_OP_MUL_MAT_ID: float32 [T][k][N] per slot, or [T][N] weighted by route_w.
+    """GGML_OP_MUL_MAT_ID: float32 [T][k][N] per slot, or [T][N] weighted by route_w. Experts may be
+    quantized, float32, bfloat16 or float16 (src1 of their dtype) or int8 with a scale a row (src1
+    bfloat16, float16 or float32, quantized row by row).
     ``act_quant=1``: the quantized-activation (int8 MFMA) grouped GEMM, Q8_0 experts;
     ``act_quant=2``: MXFP4 activations (FP4 MFMA), MXFP4 experts."""
     _check_ids(ids, route_w)
@@ -531,7 +570,10 @@ def moe_mul_mat_id(w: Weights, src1: torch.Tensor, ids: torch.Tensor,
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=ids.device)
         _keep_alive(stream, out)
-    st = _xtype(src1)
+    elem = cw.type in (MOE_BF16, MOE_F16, MOE_I8)
+    if elem:
+        _check_device(stream, w.data, w.scales, src1, ids, route_w, out)
+    st = _elem_type(src1) if elem else _xtype(src1)
     opt = _call_options(path, tau, events, act_quant)
     need = lib.moe_mul_mat_id_workspace_size(ctypes.byref(cw), st, src1_rows_per_token, T, k,
                                              ctypes.byref(opt))
@@ -543,6 +585,83 @@ def moe_mul_mat_id(w: Weights, src1: torch.Tensor, ids: torch.Tensor,
                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
            "moe_mul_mat_id")
     return out
+
+
+def moe_mul_mat_id_backward_workspace_size(w: Weights, d_dst_type: int, src1_rows_per_token: int, n_tokens: int,
+                                           n_used: int, weighted: bool, want: Sequence[str] = ("src1", "w"),
+                                           path: int = PATH_AUTO) -> int:
+    """Bytes that moe_mul_mat_id_backward needs for the gradients named in ``want``."""
+    cw = w.c()
+    return lib.moe_mul_mat_id_backward_workspace_size(ctypes.byref(cw), d_dst_type, src1_rows_per_token, n_tokens,
+                                                      n_used, int(bool(weighted)), _wanted(want),
+                                                      ctypes.byref(_options(path)))
+
+
+_WANT = {"src1": 1, "w": 2, "route_w": 4}
+
+
+def _wanted(want) -> int:
+    bad = [n for n in want if n not in _WANT]
+    if bad or isinstance(want, str):
+        raise ValueError("want must be names out of %s (got %r)" % (", ".join(_WANT), want))
+    return sum(_WANT[n] for n in set(want))
+
+
+def moe_mul_mat_id_backward(w: Weights, src1: torch.Tensor, ids: torch.Tensor, d_dst: torch.Tensor,
+                            route_w: Optional[torch.Tensor] = None, src1_rows_per_token: int = 1,
+                            want: Optional[Sequence[str]] = None, d_src1: Optional[torch.Tensor] = None,
+                            d_w: Optional[torch.Tensor] = None, d_w_dtype: Optional[torch.dtype] = None,
+                            d_route_w: Optional[torch.Tensor] = None, path: int = PATH_AUTO,
+                            workspace: Optional[torch.Tensor] = None, stream=None, events=None):
+    """(d_src1, d_w, d_route_w) of moe_mul_mat_id with bfloat16 or float16 experts, from the gradient
+    ``d_dst`` of its result: [T][k][N], with ``route_w`` [T][N]; the experts' dtype, or float32, which is
+    rounded to it. ``want`` names the gradients to compute, by default "src1", "w" and, with route_w,
+    "route_w"; the others come back as None. d_src1 has src1's shape and dtype, d_w the experts' shape
+    and dtype or float32 (``d_w_dtype``), d_route_w is float32 [T][k]."""
+    _check_ids(ids, route_w)
+    T, k = ids.shape
+    cw = w.c()
+    E, N, K = cw.n_mat, cw.rows, cw.cols
+    if want is None:
+        want = ("src1", "w") if route_w is None else ("src1", "w", "route_w")
+    flags = _wanted(want)
+    if src1.dim() < 2 or src1.numel() != T * src1_rows_per_token * K:
+        raise ValueError("src1 must hold [n_tokens][src1_rows_per_token][K] = %d x %d x %d elements"
+                         % (T, src1_rows_per_token, K))
+    shape = (T, k, N) if route_w is None else (T, N)
+    if tuple(d_dst.shape) != shape:
+        raise ValueError("d_dst must be of shape %s (got %s)" % (shape, tuple(d_dst.shape)))
+    _dev_check(src1, ids, route_w, d_dst, d_src1, d_w, d_route_w)
+    dev = ids.device
+    _check_device(stream, w.data, src1, ids, route_w, d_dst, d_src1, d_w, d_route_w)
+    outs, made = {}, []
+    for name, given, dtype, like in (("src1", d_src1, src1.dtype, tuple(src1.shape)),
+                                     ("w", d_w, d_w_dtype or (w.data.dtype if d_w is None else d_w.dtype), (E, N, K)),
+                                     ("route_w", d_route_w, torch.float32, (T, k))):
+        if not flags & _WANT[name]:
+            if given is not None:
+                raise ValueError("d_%s is given, but want does not name %r" % (name, name))
+            outs[name] = None
+        elif given is None:
+            outs[name] = torch.empty(like, dtype=dtype, device=dev)
+            made.append(outs[name])
+        else:
+            _check_tensor(given, "d_" + name, dtype, like, dev)
+            outs[name] = given
+    if made and stream is not None:
+        _keep_alive(stream, *made)
+    opt = _call_options(path, 0.0, events, 0)
+    dt = _elem_type(d_dst)
+    need = lib.moe_mul_mat_id_backward_workspace_size(ctypes.byref(cw), dt, src1_rows_per_token, T, k,
+                                                      int(route_w is not None), flags, ctypes.byref(opt))
+    ws = _workspace(need, dev, workspace, stream)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _check(lib.moe_mul_mat_id_backward(ctypes.byref(cw), src1.data_ptr(), _elem_type(src1), src1_rows_per_token,
+                                       ids.data_ptr(), T, k, ptr(route_w), d_dst.data_ptr(), dt, ptr(outs["src1"]),
+                                       ptr(outs["w"]), cw.type if outs["w"] is None else _elem_type(outs["w"]),
+                                       ptr(outs["route_w"]), ctypes.byref(opt), ws.data_ptr(),
+                                       ws.numel() * ws.element_size(), _stream(stream)), "moe_mul_mat_id_backward")
+    return outs["src1"], outs["w"], outs["route_w"]
 
 
 def moe_ffn_fused_workspace_size(gate: Weights, sh_gate: Optional[Weights], n_tokens: int,

@@ -1,0 +1,105 @@
+// What the gradients of mul_mat_id do besides the grouped products: the gradient rows of dst in the
+// element type, and the joining of the slots' gradient rows g:
+//   d_src1[r] = sum over r's slots, ascending, of route_w * g   (float32, rounded once)
+//   d_route_w[i] = sum over the columns of g[i] * src1[r]
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int64_t kMaxGrid = 1 << 22;   // blocks take several rows past it
+
+template <class Elem>
+__global__ __launch_bounds__(kThreads) void k_cast_rows(CastRowsArgs a) {
+    typedef Elem Vec __attribute__((ext_vector_type(8)));
+    const int64_t chunks = a.ld / 8;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.rows * chunks; i += (int64_t)gridDim.x * kThreads) {
+        const int64_t row = i / chunks, c = (i - row * chunks) * 8;
+        Vec v;
+#pragma unroll
+        for (int u = 0; u < 8; u++) {
+            if (c + u >= a.N) v[u] = (Elem)0.f;
+            else if (a.f32) v[u] = (Elem)((const float*)a.src)[row * a.N + c + u];
+            else v[u] = ((const Elem*)a.src)[row * a.N + c + u];
+        }
+        *(Vec*)((Elem*)a.dst + row * a.ld + c) = v;
+    }
+}
+
+// One block a row of d_src1 and its k slots; the dot products' parts of a wave are in LDS.
+template <class Elem>
+__global__ __launch_bounds__(kThreads) void k_grad_rows(GradRowsArgs a) {
+    extern __shared__ float s_dot[];   // [kWaves][k]
+    typedef Elem Vec __attribute__((ext_vector_type(4)));
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        if (a.d_route_w) {
+            for (int i = tid; i < kWaves * a.k; i += kThreads) s_dot[i] = 0.f;
+            __syncthreads();
+        }
+        for (int c0 = 0; c0 < a.K; c0 += 4 * kThreads) {
+            const int c = c0 + 4 * tid;
+            const bool in = c < a.K;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f}, x = acc;
+            if (in && a.d_route_w) {
+                const Vec v = *(const Vec*)((const Elem*)a.x + r * a.K + c);
+#pragma unroll
+                for (int u = 0; u < 4; u++) x[u] = (float)v[u];
+            }
+            for (int s = 0; s < a.k; s++) {
+                const int64_t i = r * a.k + s;
+                const int32_t e = a.ids[i];
+                if (e < 0 || e >= a.E) continue;
+                const f32x4 g = in ? *(const f32x4*)(a.g + i * a.K + c) : f32x4{0.f, 0.f, 0.f, 0.f};
+                const float w = a.route_w ? a.route_w[i] : 1.f;
+#pragma unroll
+                for (int u = 0; u < 4; u++) acc[u] = fmaf(w, g[u], acc[u]);
+                if (a.d_route_w) {
+                    float d = in ? g[0] * x[0] + g[1] * x[1] + g[2] * x[2] + g[3] * x[3] : 0.f;
+                    for (int m = 32; m; m >>= 1) d += __shfl_xor(d, m);
+                    if (lane == 0) s_dot[wv * a.k + s] += d;
+                }
+            }
+            if (in && a.d_x) {
+                Vec v;
+#pragma unroll
+                for (int u = 0; u < 4; u++) v[u] = (Elem)acc[u];
+                *(Vec*)((Elem*)a.d_x + r * a.K + c) = v;
+            }
+        }
+        if (a.d_route_w) {
+            __syncthreads();
+            for (int s = tid; s < a.k; s += kThreads) {
+                float d = 0.f;
+                for (int w = 0; w < kWaves; w++) d += s_dot[w * a.k + s];
+                a.d_route_w[r * a.k + s] = d;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st) {
+    const int64_t n = a.rows * (a.ld / 8);
+    if (n <= 0) return hipSuccess;
+    const int64_t blocks = (n + kThreads - 1) / kThreads;
+    const unsigned grid = (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid);
+    if (a.type == kElemBf16) k_cast_rows<__bf16><<<grid, kThreads, 0, st>>>(a);
+    else k_cast_rows<_Float16><<<grid, kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_rows(const GradRowsArgs& a, hipStream_t st) {
+    if (a.rows <= 0) return hipSuccess;
+    const unsigned grid = (unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid);
+    const size_t lds = a.d_route_w ? (size_t)kWaves * a.k * 4 : 0;
+    if (a.type == kElemBf16) k_grad_rows<__bf16><<<grid, kThreads, lds, st>>>(a);
+    else k_grad_rows<_Float16><<<grid, kThreads, lds, st>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -84,6 +84,36 @@ moe_status check_experts(int64_t E) {
     return MOE_OK;
 }
 
+// Experts of the 16-bit and int8 products.
+bool is_elem(moe_dtype t) { return t == MOE_BF16 || t == MOE_F16 || t == MOE_I8; }
+ElemType elem_of(moe_dtype t) {
+    return t == MOE_BF16 ? kElemBf16 : t == MOE_F16 ? kElemF16 : t == MOE_I8 ? kElemI8 : kElemF32;
+}
+const char* type_name(moe_dtype t) {
+    return t == MOE_BF16 ? "BF16" : t == MOE_F16 ? "F16" : t == MOE_I8 ? "I8" : t == MOE_F32 ? "F32" : "another type";
+}
+constexpr int64_t kElemMaxSize = 1 << 30;   // rows, cols: tile ends stay in int32
+constexpr int64_t kI8MaxCols = 131072;      // 128 * 127 * cols < 2^31
+moe_status check_aligned(const void* p, const char* name) {
+    if ((uintptr_t)p % 16) return fail(MOE_EINVAL, "%s must be 16-byte aligned", name);
+    return MOE_OK;
+}
+moe_status check_elem_weights(const moe_weights* w, const char* name) {
+    moe_status s;
+    const int64_t unit = w->type == MOE_I8 ? 16 : 8;
+    if (w->type == MOE_I8 && !w->scales) return fail(MOE_EINVAL, "%s: I8 scales are NULL", name);
+    if (w->cols % unit)
+        return fail(MOE_ELIMIT, "%s: %s needs cols %% %lld == 0 (got %lld)", name, type_name(w->type),
+                    (long long)unit, (long long)w->cols);
+    if (w->rows >= kElemMaxSize || w->cols >= kElemMaxSize)
+        return fail(MOE_ELIMIT, "%s: rows and cols must be < 2^30", name);
+    if (w->type == MOE_I8 && w->cols > kI8MaxCols)
+        return fail(MOE_ELIMIT, "%s: I8 needs cols <= %lld (got %lld)", name, (long long)kI8MaxCols, (long long)w->cols);
+    if ((s = check_aligned(w->data, name))) return s;
+    if (w->type == MOE_I8 && (uintptr_t)w->scales % 4) return fail(MOE_EINVAL, "%s: I8 scales must be 4-byte aligned", name);
+    return MOE_OK;
+}
+
 moe_status check_weights(const moe_weights* w, const char* name, bool allow_f32) {
     if (!w) return fail(MOE_EINVAL, "%s: weights struct is NULL", name);
     if (!w->data) return fail(MOE_EINVAL, "%s: data is NULL", name);
@@ -103,6 +133,8 @@ moe_status check_weights(const moe_weights* w, const char* name, bool allow_f32)
             return fail(MOE_EINVAL, "%s: IQ4_XS super-block records must be 8-byte aligned", name);
     } else if (w->type == MOE_F32) {
         if (!allow_f32) return fail(MOE_EINVAL, "%s: float32 weights are not supported here", name);
+    } else if (allow_f32 && is_elem(w->type)) {
+        return check_elem_weights(w, name);
     } else {
         return fail(MOE_EINVAL, "%s: unsupported weight type %d", name, (int)w->type);
     }
@@ -384,6 +416,10 @@ moe_status validate_mmid(const moe_weights* w, moe_dtype st, int32_t B, int64_t 
     if (w->type == MOE_IQ4_NL && st != MOE_BF16) return fail(MOE_EINVAL, "IQ4_NL weights need BF16 src1");
     if (w->type == MOE_IQ4_XS && st != MOE_BF16) return fail(MOE_EINVAL, "IQ4_XS weights need BF16 src1");
     if (w->type == MOE_F32 && st != MOE_F32) return fail(MOE_EINVAL, "F32 weights need F32 src1");
+    if ((w->type == MOE_BF16 || w->type == MOE_F16) && st != w->type)
+        return fail(MOE_EINVAL, "%s weights need %s src1", type_name(w->type), type_name(w->type));
+    if (w->type == MOE_I8 && st != MOE_BF16 && st != MOE_F16 && st != MOE_F32)
+        return fail(MOE_EINVAL, "I8 weights need BF16, F16 or F32 src1");
     return MOE_OK;
 }
 
@@ -675,6 +711,170 @@ moe_status mmid_dec_fp4(const MmidPlan& p, const moe_weights* w, const void* src
     return MOE_OK;
 }
 
+// ---------------------------------------------------------------- 16-bit and int8 experts
+// Options of their calls: act_quant 0, a path the call has.
+moe_status check_elem_options(const moe_options* o, int max_path, const char* what) {
+    if (o && o->act_quant)
+        return fail(MOE_EINVAL, "%s with BF16, F16 or I8 experts: options.act_quant must be 0 (got %d)", what, o->act_quant);
+    if (o && (o->path < 0 || o->path > max_path))
+        return fail(MOE_EINVAL, "%s with BF16, F16 or I8 experts: options.path must be 0 to %d (got %d)", what, max_path,
+                    o->path);
+    return MOE_OK;
+}
+
+// 1 grouped GEMM, 2 GEMV, or a negative status.
+int elem_path(int64_t, int32_t, int32_t, int64_t, moe_dtype, const moe_options* o) {
+    const moe_status s = check_elem_options(o, 1, "mul_mat_id");
+    return s ? (int)s : 1;
+}
+
+struct ElemPlan {
+    RowIdsPlan r;
+    int tile_m;
+    int8_t* q;    // I8: src1 codes and row scales
+    float* d;
+    float* y;     // weighted: per-slot rows
+};
+ElemPlan carve_elem(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted) {
+    ElemPlan p{};
+    const int64_t n = T * k;
+    p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
+    p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
+    if (w->type == MOE_I8) {
+        p.q = (int8_t*)c.take((size_t)(T * B) * w->cols);
+        p.d = (float*)c.take((size_t)(T * B) * 4);
+    }
+    if (weighted) p.y = (float*)c.take((size_t)n * w->rows * 4);
+    return p;
+}
+ExpertGemm elem_gemm(const moe_weights* w, const RowIdsPlan& r, int tile_m, int64_t n) {
+    ExpertGemm g{};
+    g.type = elem_of(w->type);
+    g.W = w->data;
+    g.w_scale = w->type == MOE_I8 ? (const float*)w->scales : nullptr;
+    g.N = (int32_t)w->rows;
+    g.K = (int32_t)w->cols;
+    g.E = (int32_t)w->n_mat;
+    g.tile_off = r.tile_a;
+    g.tile_tab = r.tile_tab;
+    g.tile_m = tile_m;
+    g.m_tiles_max = (int32_t)m_tiles_bound(n, w->n_mat, tile_m);
+    return g;
+}
+void elem_tiles(RowIdsArgs& ra, const RowIdsPlan& r, int tile_m) {
+    ra.tile_off[0] = r.tile_a;
+    ra.tile_m[0] = tile_m;
+    ra.tile_tab[0] = r.tile_tab;
+    ra.tile_cap[0] = r.tile_cap;
+}
+moe_status check_grid(int64_t blocks, const char* what) {
+    if (blocks * 512 >= k4GiB) return fail(MOE_ELIMIT, "%s: the grid exceeds 2^32 work-items", what);
+    return MOE_OK;
+}
+
+// moe_mul_mat_id up to the per-slot rows (slot_out, those of invalid slots not written).
+moe_status mmid_elem(const ElemPlan& p, const moe_weights* w, const void* src1, moe_dtype src1_type, int32_t B,
+                     const int32_t* ids, int64_t T, int32_t k, float* slot_out, Timer& tm, hipStream_t st) {
+    moe_status s;
+    const int64_t n = T * k;
+    RowIdsArgs ra = row_ids_args(ids, n, k, (int32_t)w->n_mat, B, p.r);
+    elem_tiles(ra, p.r, p.tile_m);
+    ExpertGemm g = elem_gemm(w, p.r, p.tile_m, n);
+    g.A = w->type == MOE_I8 ? (const void*)p.q : src1;
+    g.lda = w->cols;
+    g.a_scale = p.d;
+    g.a_rows = p.r.ids_src1;
+    g.out = slot_out;
+    g.out_rows = p.r.ids_dst;
+    if ((s = check_grid(expert_gemm_grid(g, 0), "mul_mat_id"))) return s;
+    tm.begin();
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    tm.end();
+    if (w->type == MOE_I8) {
+        const QuantRowsArgs q{src1, elem_of(src1_type), T * B, w->cols, p.q, p.d};
+        tm.begin();
+        if ((s = hip_check(launch_quant_rows(q, st), "quantize src1"))) return s;
+        tm.end();
+    }
+    tm.begin();
+    if ((s = hip_check(launch_expert_gemm(g, st), "grouped GEMM"))) return s;
+    tm.end();
+    return MOE_OK;
+}
+
+moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src1_type, int32_t B, const int32_t* ids,
+                           int64_t T, int32_t k, const float* route_w, float* dst, const moe_options* opt, void* ws,
+                           size_t ws_bytes, hipStream_t st) {
+    moe_status s;
+    const int path = elem_path(T, k, (int32_t)w->n_mat, w->cols, w->type, opt);
+    if (path < 0) return (moe_status)path;
+    const bool weighted = route_w != nullptr;
+    if ((s = check_aligned(src1, "src1"))) return s;
+    Carve sz(nullptr);
+    carve_elem(sz, w, T, k, B, weighted);
+    if (sz.off > ws_bytes || (sz.off && !ws)) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
+    if ((s = check_aligned(ws, "the workspace"))) return s;
+    Carve c(ws);
+    const ElemPlan p = carve_elem(c, w, T, k, B, weighted);
+    Timer tm(opt, st);
+    float* slot_out = weighted ? p.y : dst;
+    if ((s = mmid_elem(p, w, src1, src1_type, B, ids, T, k, slot_out, tm, st))) return s;
+    ReduceArgs rd{};
+    rd.ids = ids;
+    rd.route_w = route_w;
+    rd.T = (int32_t)T;
+    rd.k = k;
+    rd.E = (int32_t)w->n_mat;
+    rd.N = (int32_t)w->rows;
+    rd.y = slot_out;
+    rd.out = dst;
+    rd.mode = weighted ? 0 : 1;
+    tm.begin();
+    if ((s = hip_check(launch_reduce(rd, st), weighted ? "reduce" : "zero invalid slots"))) return s;
+    tm.end();
+    g_stages = tm.stage;
+    return MOE_OK;
+}
+
+enum Want { kWantX = 1, kWantW = 2, kWantR = 4 };
+struct GradPlan {
+    RowIdsPlan r;
+    int tile_m;
+    bool direct;    // the row gradients go to d_src1 as they are
+    int64_t ld;     // row length of dY
+    void* dy;       // d_dst in the experts' type, rows of ld (nullptr: d_dst itself)
+    float* g;       // per-slot rows of g
+};
+// dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
+GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int want,
+                    bool dy_as_is) {
+    GradPlan p{};
+    const int64_t n = T * k;
+    p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
+    p.direct = B == k && !(want & kWantR);
+    p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
+    p.ld = (w->rows + 7) / 8 * 8;
+    if (!dy_as_is) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
+    if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
+    return p;
+}
+moe_status validate_grad(const moe_weights* w, moe_dtype src1_type, moe_dtype d_dst_type, int32_t B, int64_t T,
+                         int32_t k, bool weighted, int want, const moe_options* opt) {
+    moe_status s;
+    if ((s = check_tokens(T, k))) return s;
+    if ((s = check_weights(w, "w", true))) return s;
+    if (w->type != MOE_BF16 && w->type != MOE_F16)
+        return fail(MOE_EINVAL, "gradients of mul_mat_id need BF16 or F16 experts");
+    if ((s = check_experts(w->n_mat))) return s;
+    if (B != 1 && B != k) return fail(MOE_EINVAL, "src1_rows_per_token must be 1 or n_used (got %d)", B);
+    if (src1_type != w->type) return fail(MOE_EINVAL, "src1 must be of the experts' type (%s)", type_name(w->type));
+    if (d_dst_type != w->type && d_dst_type != MOE_F32)
+        return fail(MOE_EINVAL, "d_dst must be of the experts' type (%s) or F32", type_name(w->type));
+    if (!want || (want & ~7)) return fail(MOE_EINVAL, "at least one of d_src1, d_w and d_route_w is needed");
+    if ((want & kWantR) && !weighted) return fail(MOE_EINVAL, "d_route_w needs route_w");
+    return check_elem_options(opt, 1, "gradients of mul_mat_id");
+}
+
 moe_status check_router(const moe_router_config* c, int64_t T, int32_t E, int32_t k, bool choose) {
     moe_status s;
     if ((s = check_tokens(T, k))) return s;
@@ -732,9 +932,10 @@ int32_t moe_select_path_typed(int64_t n_tokens, int32_t n_used, int32_t n_expert
     if ((s = check_tokens(n_tokens, n_used))) return s;
     if ((s = check_experts(n_experts))) return s;
     if (act_width <= 0) return fail(MOE_EINVAL, "act_width must be > 0");
+    if (is_elem(weight_type)) return elem_path(n_tokens, n_used, n_experts, act_width, weight_type, opt);
     if (weight_type != MOE_Q8_0 && weight_type != MOE_MXFP4 && weight_type != MOE_IQ4_NL &&
         weight_type != MOE_IQ4_XS)
-        return fail(MOE_EINVAL, "weight_type must be Q8_0, MXFP4, IQ4_NL or IQ4_XS (got %d)", (int)weight_type);
+        return fail(MOE_EINVAL, "weight_type must be Q8_0, MXFP4, IQ4_NL, IQ4_XS, BF16, F16 or I8 (got %d)", (int)weight_type);
     return select_path_aq(n_tokens, n_used, n_experts, act_width, weight_type, opt, 0, act_width);
 }
 
@@ -1144,6 +1345,12 @@ size_t moe_mul_mat_id_workspace_size(const moe_weights* w, moe_dtype src1_type,
                                      int32_t src1_rows_per_token, int64_t n_tokens,
                                      int32_t n_used, const moe_options* opt) {
     if (validate_mmid(w, src1_type, src1_rows_per_token, n_tokens, n_used)) return 0;
+    if (is_elem(w->type)) {   // the weighted call's, which is the larger
+        if (elem_path(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt) < 0) return 0;
+        Carve c(nullptr);
+        carve_elem(c, w, n_tokens, n_used, src1_rows_per_token, true);
+        return c.off;
+    }
     const bool q8 = w->type != MOE_F32;   // quantized experts
     if (!q8 && opt && ((opt->path != 0 && opt->path != 1) || opt->act_quant)) return 0;
     const int path = q8 ? select_path_aq(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt, 0, w->cols) : 1;
@@ -1170,6 +1377,8 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
     const bool q8 = w->type != MOE_F32;   // quantized experts
     const int32_t E = (int32_t)w->n_mat, N = (int32_t)w->rows, K = (int32_t)w->cols;
     const int32_t B = src1_rows_per_token, k = n_used;
+    if (is_elem(w->type))
+        return mul_mat_id_elem(w, src1, src1_type, B, ids, n_tokens, k, route_w, dst, opt, ws, ws_bytes, (hipStream_t)stream);
     if (!q8 && opt && opt->path != 0 && opt->path != 1)
         return fail(MOE_EINVAL, "float32 experts run the grouped fp32 product only: options.path "
                     "must be 0 or 1 (got %d)", opt->path);
@@ -1343,6 +1552,143 @@ moe_status moe_mul_mat_id(const moe_weights* w, const void* src1, moe_dtype src1
     tm.end();
     g_stages = tm.stage;
     return MOE_OK;
+}
+
+size_t moe_mul_mat_id_backward_workspace_size(const moe_weights* w, moe_dtype d_dst_type,
+                                              int32_t src1_rows_per_token, int64_t n_tokens,
+                                              int32_t n_used, int32_t weighted, int32_t want,
+                                              const moe_options* opt) {
+    if (!w || validate_grad(w, w->type, d_dst_type, src1_rows_per_token, n_tokens, n_used, weighted != 0, want, opt))
+        return 0;
+    Carve c(nullptr);   // room for a copy of d_dst also where its address alone asks for one
+    carve_grad(c, w, n_tokens, n_used, src1_rows_per_token, weighted != 0, want, false);
+    return c.off;
+}
+
+moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_dtype src1_type,
+                                   int32_t src1_rows_per_token, const int32_t* ids,
+                                   int64_t n_tokens, int32_t n_used, const float* route_w,
+                                   const void* d_dst, moe_dtype d_dst_type, void* d_src1, void* d_w,
+                                   moe_dtype d_w_type, float* d_route_w, const moe_options* opt,
+                                   void* ws, size_t ws_bytes, void* stream) {
+    g_err.clear();
+    moe_status s;
+    const int want = (d_src1 ? kWantX : 0) | (d_w ? kWantW : 0) | (d_route_w ? kWantR : 0);
+    const bool weighted = route_w != nullptr;
+    const int32_t B = src1_rows_per_token, k = n_used;
+    const int64_t T = n_tokens, n = T * (int64_t)k;
+    if ((s = validate_grad(w, src1_type, d_dst_type, B, T, k, weighted, want, opt))) return s;
+    if (d_w && d_w_type != w->type && d_w_type != MOE_F32)
+        return fail(MOE_EINVAL, "d_w must be of the experts' type (%s) or F32", type_name(w->type));
+    if (T == 0 && !d_w) {
+        g_stages = 0;
+        return MOE_OK;
+    }
+    if (T > 0 && (!src1 || !ids || !d_dst)) return fail(MOE_EINVAL, "NULL pointer argument");
+    if ((s = check_aligned(src1, "src1")) || (s = check_aligned(d_src1, "d_src1")) || (s = check_aligned(d_w, "d_w")))
+        return s;
+    const int32_t E = (int32_t)w->n_mat;
+    const bool as_is = d_dst_type == w->type && w->rows % 8 == 0 && (uintptr_t)d_dst % 16 == 0;
+    Carve sz(nullptr);
+    carve_grad(sz, w, T, k, B, weighted, want, as_is);
+    if (sz.off > ws_bytes || !ws) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
+    if ((s = check_aligned(ws, "the workspace"))) return s;
+    Carve c(ws);
+    const GradPlan p = carve_grad(c, w, T, k, B, weighted, want, as_is);
+    const hipStream_t st = (hipStream_t)stream;
+    const void* dy = as_is ? d_dst : p.dy;
+    // positions' tokens (ids_src1 of one row a token) and slots (ids_dst)
+    RowIdsArgs ra = row_ids_args(ids, n, k, E, 1, p.r);
+    elem_tiles(ra, p.r, p.tile_m);
+    ExpertGemm g = elem_gemm(w, p.r, p.tile_m, n);
+    g.A = dy;
+    g.lda = p.ld;
+    g.a_rows = weighted ? p.r.ids_src1 : p.r.ids_dst;
+    g.out16 = p.direct;
+    g.out = p.direct ? d_src1 : (void*)p.g;
+    g.out_rows = p.r.ids_dst;
+    g.row_w = p.direct ? route_w : nullptr;
+    ExpertGradW gw{};
+    gw.type = g.type;
+    gw.N = g.N;
+    gw.K = g.K;
+    gw.E = E;
+    gw.dY = dy;
+    gw.ldy = (int32_t)p.ld;
+    gw.X = src1;
+    gw.dy_rows = g.a_rows;
+    gw.x_rows = B == 1 ? p.r.ids_src1 : p.r.ids_dst;
+    gw.slots = p.r.ids_dst;
+    gw.bounds = p.r.bounds;
+    gw.route_w = route_w;
+    gw.dW = d_w;
+    gw.f32 = d_w_type == MOE_F32;
+    const bool rows_wanted = (want & (kWantX | kWantR)) && n > 0;
+    if (rows_wanted && (s = check_grid(expert_gemm_grid(g, 1), "row gradients"))) return s;
+    if (d_w && (s = check_grid(expert_grad_w_grid(gw), "experts' gradient"))) return s;
+    Timer tm(opt, st);
+    tm.begin();
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    tm.end();
+    if (!as_is && n > 0) {
+        const CastRowsArgs ca{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n, w->rows, p.ld, p.dy};
+        tm.begin();
+        if ((s = hip_check(launch_cast_rows(ca, st), "round d_dst"))) return s;
+        tm.end();
+    }
+    if (rows_wanted) {
+        tm.begin();
+        if ((s = hip_check(launch_expert_grad_x(g, st), "row gradients"))) return s;
+        tm.end();
+        tm.begin();
+        if (p.direct) {   // 16-bit rows of K columns are rows of K / 2 words
+            ReduceArgs z{};
+            z.ids = ids;
+            z.T = (int32_t)T;
+            z.k = k;
+            z.E = E;
+            z.N = g.K / 2;
+            z.out = (float*)d_src1;
+            z.mode = 1;
+            if ((s = hip_check(launch_reduce(z, st), "zero invalid slots"))) return s;
+        } else {
+            GradRowsArgs j{};
+            j.type = g.type;
+            j.g = p.g;
+            j.ids = ids;
+            j.route_w = route_w;
+            j.x = src1;
+            j.rows = T * B;
+            j.k = B == 1 ? k : 1;
+            j.E = E;
+            j.K = g.K;
+            j.d_x = d_src1;
+            j.d_route_w = d_route_w;
+            if ((s = hip_check(launch_grad_rows(j, st), "join the slots' gradients"))) return s;
+        }
+        tm.end();
+    }
+    if (d_w) {
+        tm.begin();
+        if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
+        tm.end();
+    }
+    g_stages = tm.stage;
+    return MOE_OK;
+}
+
+moe_status moe_quantize_rows(const void* x, moe_dtype x_type, int64_t rows, int64_t K, int8_t* q,
+                             float* d, void* stream) {
+    g_err.clear();
+    if (x_type != MOE_BF16 && x_type != MOE_F16 && x_type != MOE_F32)
+        return fail(MOE_EINVAL, "x must be BF16, F16 or F32");
+    if (rows < 0 || K <= 0) return fail(MOE_EINVAL, "rows must be >= 0 and K > 0");
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !d) return fail(MOE_EINVAL, "NULL pointer argument");
+    if ((uintptr_t)x % (x_type == MOE_F32 ? 4 : 2) || (uintptr_t)d % 4)
+        return fail(MOE_EINVAL, "x and d must be aligned to their elements");
+    const QuantRowsArgs a{x, elem_of(x_type), rows, K, q, d};
+    return hip_check(launch_quant_rows(a, (hipStream_t)stream), "quantize rows");
 }
 
 moe_status moe_quantize_act(const void* x, moe_dtype x_type, int64_t rows, int64_t K, int8_t* q,

@@ -265,6 +265,76 @@ hipError_t launch_decode_fp4(const DecFp4Args& a, hipStream_t st);
 // Whether a weighted call over n = T * k slots, S shared experts and K columns fuses the sum.
 bool decode_fp4_fuses(int64_t n, int64_t E, int64_t S, int64_t K);
 
+// ---------------------------------------------------------------- 16-bit and int8 experts
+enum ElemType : int32_t { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2, kElemI8 = 3 };
+// Grouped product (depth K, N columns) or row gradient (depth N, K columns) over the routed segments.
+struct ExpertGemm {
+    ElemType type;             // of W and A
+    const void* W;             // [E][N][K]
+    const float* w_scale;      // int8: [E][N]
+    int32_t N, K, E;
+    const void* A;             // rows of lda elements; what passes the depth in a 16-byte chunk is 0
+    int64_t lda;
+    const float* a_scale;      // int8: one per row of A
+    const int32_t* a_rows;     // row of A of position j
+    const int32_t* tile_off;   // [E + 1] M-tile prefix
+    const int32_t* tile_tab;   // per M tile {expert, its first tile, first position, positions}
+    int32_t tile_m;            // expert_gemm_tile_m
+    int32_t m_tiles_max;
+    void* out;                 // [rows][columns], float32, or the element type (out16)
+    int32_t out16;
+    const int32_t* out_rows;   // row of out of position j
+    const float* row_w;        // out16: nullptr, or a factor for each row of out
+};
+int expert_gemm_tile_m(double avg_rows);
+int64_t expert_gemm_grid(const ExpertGemm& a, int grad);   // blocks; at most 512 threads each
+hipError_t launch_expert_gemm(const ExpertGemm& a, hipStream_t st);
+hipError_t launch_expert_grad_x(const ExpertGemm& a, hipStream_t st);
+struct ExpertGradW {
+    ElemType type;             // of dY and X (bf16, f16)
+    int32_t N, K, E;
+    const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
+    int32_t ldy;               // a multiple of 8
+    const void* X;             // rows of K
+    const int32_t *dy_rows, *x_rows, *slots;   // of position j: rows of dY and X, slot
+    const int32_t* bounds;     // [E + 1]
+    const float* route_w;      // nullptr, or a factor for each slot
+    void* dW;                  // [E][N][K], float32 (f32) or the element type
+    int32_t f32;
+};
+int64_t expert_grad_w_grid(const ExpertGradW& a);
+hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st);
+
+struct QuantRowsArgs {
+    const void* src;    // [rows][K]
+    ElemType src_type;  // f32, bf16 or f16
+    int64_t rows, K;
+    int8_t* q;          // [rows][K]
+    float* d;           // [rows]
+};
+hipError_t launch_quant_rows(const QuantRowsArgs& a, hipStream_t st);
+// Rows of float32 (f32) or of the type itself -> rows of the type, ld elements (a multiple of 8), 0 past N.
+struct CastRowsArgs {
+    const void* src;    // [rows][N]
+    int32_t f32;
+    ElemType type;
+    int64_t rows, N, ld;
+    void* dst;
+};
+hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st);
+struct GradRowsArgs {
+    ElemType type;
+    const float* g;          // [rows * k][K]
+    const int32_t* ids;      // [rows * k]
+    const float* route_w;    // nullptr (1) or [rows * k]
+    const void* x;           // [rows][K]
+    int64_t rows;
+    int32_t k, E, K;
+    void* d_x;               // nullptr or [rows][K]
+    float* d_route_w;        // nullptr or [rows * k]
+};
+hipError_t launch_grad_rows(const GradRowsArgs& a, hipStream_t st);
+
 // ---------------------------------------------------------------- fp32 grouped matmul (Tiny)
 struct GemmF32Args {
     const float* W;        // [E][N][K]

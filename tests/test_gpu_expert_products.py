@@ -1,0 +1,180 @@
+"""mul_mat_id with bf16, f16 and int8 experts, its gradients, and the row quantizer against their float64
+forms on a GPU."""
+import pytest
+import torch
+
+import indirect_expert_matmul_amd as moe
+import ref_products as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def _ids(T, E, k, g, segments=None, invalid=0.0, repeat=False):
+    """ids [T][k]; segments: rows of each expert in turn instead of a draw (k = 1)."""
+    if segments is not None:
+        e = torch.repeat_interleave(torch.arange(len(segments)), torch.tensor(segments))
+        return e[torch.randperm(len(e), generator=g)].to(torch.int32)[:, None].contiguous()
+    if repeat:
+        ids = torch.randint(0, E, (T, k), generator=g)
+    else:
+        ids = torch.rand((T, E), generator=g).topk(k, dim=1).indices
+    ids = ids.to(torch.int32)
+    if invalid:
+        ids[torch.rand((T, k), generator=g) < invalid] = -1
+        ids[torch.rand((T, k), generator=g) < invalid / 2] = E
+    return ids.contiguous()
+
+
+def _data(E, N, K, ids, dtype, per_slot, seed):
+    g = torch.Generator().manual_seed(seed)
+    T, k = ids.shape
+    w = (torch.randn((E, N, K), generator=g) * 0.05).to(dtype)
+    x = torch.randn((T * (k if per_slot else 1), K), generator=g).to(dtype)
+    rw = torch.softmax(torch.randn((T, k), generator=g), 1)
+    return w, x, rw
+
+
+# tokens, experts, picks, N, K, rows per token, weighted, invalid ids
+SHAPES = [
+    (1, 4, 2, 64, 64, False, False, 0.0),
+    (1, 8, 1, 1, 8, False, True, 0.0),
+    (3, 5, 2, 33, 72, True, False, 0.3),
+    (17, 3, 3, 130, 136, False, True, 0.2),
+    (40, 2, 2, 257, 200, True, True, 0.0),
+    (9, 16, 16, 95, 1048, False, False, 0.0),
+    (300, 2, 1, 300, 264, False, False, 0.1),
+    (513, 3, 2, 129, 328, True, True, 0.05),
+    (700, 1, 1, 512, 64, False, False, 0.0),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,E,k,N,K,per_slot,weighted,invalid", SHAPES)
+def test_product(T, E, k, N, K, per_slot, weighted, invalid, dtype):
+    ids = _ids(T, E, k, torch.Generator().manual_seed(T + N), invalid=invalid)
+    w, x, rw = _data(E, N, K, ids, dtype, per_slot, 1000 + K)
+    out = moe.moe_mul_mat_id(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), route_w=rw.cuda() if weighted else None,
+                             src1_rows_per_token=k if per_slot else 1)
+    y, tol = ref.product(w.double(), x.double(), ids, E, per_slot)
+    if weighted:
+        y, tol = ref.weighted(y, tol, rw, T, k)
+    else:
+        y, tol = y.view(T, k, N), tol.view(T, k, N)
+    ref.within(out, y, tol, "product")
+
+
+SEGMENTS = [0, 1, 31, 32, 33, 63, 64, 65, 0, 127, 128, 129, 255, 256, 257, 300, 511, 513, 2]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("few", [False, True])
+def test_product_segments(dtype, few):
+    """Segment lengths at the tiles' edges, each expert on its own; many empty experts give the small tiles."""
+    segments = SEGMENTS + ([0] * 300 if few else [])
+    ids = _ids(0, 0, 1, torch.Generator().manual_seed(3), segments=segments)
+    E = len(segments)
+    w, x, _ = _data(E, 72, 136, ids, dtype, False, 5)
+    out = moe.moe_mul_mat_id(moe.Weights(w.cuda()), x.cuda(), ids.cuda())
+    y, tol = ref.product(w.double(), x.double(), ids, E, False)
+    ref.within(out[:, 0], y, tol, "segments")
+
+
+@pytest.mark.parametrize("src", [BF, HF, F32])
+@pytest.mark.parametrize("T,E,k,N,K,per_slot,weighted,invalid",
+                         [(s[0], s[1], s[2], s[3], (s[4] + 15) // 16 * 16) + s[5:] for s in SHAPES])
+def test_int8(T, E, k, N, K, per_slot, weighted, invalid, src):
+    g = torch.Generator().manual_seed(T + N + K)
+    ids = _ids(T, E, k, g, invalid=invalid)
+    x = (torch.randn((T * (k if per_slot else 1), K), generator=g) * 3).to(src)
+    x[0] = 0
+    q = torch.randint(-127, 128, (E, N, K), generator=g, dtype=torch.int8)
+    d = torch.rand((E, N), generator=g) * 1e-2
+    rw = torch.softmax(torch.randn((T, k), generator=g), 1)
+    out = moe.moe_mul_mat_id(moe.Weights(q.cuda(), d.cuda()), x.cuda(), ids.cuda(),
+                             route_w=rw.cuda() if weighted else None, src1_rows_per_token=k if per_slot else 1)
+    xq, xd = ref.quantize_rows(x)
+    y, tol = ref.int8_product(q, d, xq, xd, ids, E, per_slot)
+    if weighted:
+        y, tol = ref.weighted(y, tol, rw, T, k)
+    else:
+        y, tol = y.view(T, k, N), tol.view(T, k, N)
+    ref.within(out, y, tol, "int8")
+
+
+def test_int8_segments_and_extremes():
+    """Segment lengths at the tiles' edges; codes of -128 and 127 over the widest rows' partial stage."""
+    ids = _ids(0, 0, 1, torch.Generator().manual_seed(4), segments=SEGMENTS)
+    E, N, K = len(SEGMENTS), 72, 272
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn((len(ids), K), generator=g)
+    q = torch.randint(-128, 128, (E, N, K), generator=g, dtype=torch.int8)
+    q[3], q[4] = -128, 127
+    x[:100] = 1.0
+    d = torch.rand((E, N), generator=g)
+    out = moe.moe_mul_mat_id(moe.Weights(q.cuda(), d.cuda()), x.cuda(), ids.cuda())
+    xq, xd = ref.quantize_rows(x)
+    y, tol = ref.int8_product(q, d, xq, xd, ids, E, False)
+    ref.within(out[:, 0], y, tol, "int8 segments")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (65, 64), (10, 333), (129, 512), (7, 2056), (5, 9000), (2, 40001)])
+def test_quantize_rows(rows, K, dtype):
+    g = torch.Generator().manual_seed(rows + K)
+    x = (torch.randn((rows, K), generator=g) * torch.exp(3 * torch.randn((rows, 1), generator=g))).to(dtype)
+    q, d = moe.moe_quantize_rows(x.cuda())
+    rq, rd = ref.quantize_rows(x)
+    assert torch.equal(d.cpu(), rd)
+    assert torch.equal(q.cpu().float(), rq)
+
+
+def test_quantize_rows_edges():
+    x = torch.zeros((8, 40))
+    x[1, 5], x[2, 39] = float("inf"), float("nan")
+    x[3, 0], x[4, :3] = -float("inf"), torch.tensor([127.0, 63.5, -62.5])
+    x[5, :2] = torch.tensor([1e-40, -5e-41])           # subnormal scale
+    x[6, 0] = 1e-45                                     # scale rounds to zero
+    x[7, :2] = torch.tensor([3.4e38, -3.4e38])
+    q, d = moe.moe_quantize_rows(x.cuda())
+    rq, rd = ref.quantize_rows(x)
+    assert torch.equal(torch.isnan(d.cpu()), torch.isnan(rd)) and torch.isnan(rd[1:4]).all()
+    fine = ~torch.isnan(rd)
+    assert torch.equal(d.cpu()[fine], rd[fine])
+    assert torch.equal(q.cpu().float(), rq)
+    assert q[4, :3].tolist() == [127, 64, -62]
+    y = moe.moe_mul_mat_id(moe.Weights(torch.ones((1, 16, 48), dtype=torch.int8).cuda(), torch.ones((1, 16)).cuda()),
+                           torch.nn.functional.pad(x, (0, 8)).cuda(), torch.zeros((8, 1), dtype=torch.int32).cuda())
+    assert torch.equal(torch.isnan(y).all(2).flatten().cpu(), torch.isnan(rd))
+    assert torch.equal(torch.isnan(y).any(2).flatten().cpu(), torch.isnan(rd))
+
+
+@pytest.mark.parametrize("dtype,dw", [(BF, BF), (BF, F32), (HF, HF), (HF, F32)])
+@pytest.mark.parametrize("T,E,k,N,K,per_slot,weighted,invalid", SHAPES)
+def test_gradients(T, E, k, N, K, per_slot, weighted, invalid, dtype, dw):
+    ids = _ids(T, E, k, torch.Generator().manual_seed(T + N), invalid=invalid)
+    w, x, rw = _data(E, N, K, ids, dtype, per_slot, 2000 + K)
+    g = torch.Generator().manual_seed(N)
+    dy = torch.randn((T, N) if weighted else (T, k, N), generator=g).to(dtype)
+    got = moe.moe_mul_mat_id_backward(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), dy.cuda(),
+                                      route_w=rw.cuda() if weighted else None,
+                                      src1_rows_per_token=k if per_slot else 1, d_w_dtype=dw)
+    want = ref.grads(w.double(), x.double(), ids, dy.double(), rw if weighted else None, per_slot, dtype, dw)
+    for name, a, b in zip(("d_src1", "d_w", "d_route_w"), got, want):
+        if b is None:
+            assert a is None
+        else:
+            ref.within(a, b[0].view(a.shape), b[1].view(a.shape), name)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_gradient_segments(dtype):
+    ids = _ids(0, 0, 1, torch.Generator().manual_seed(8), segments=SEGMENTS + [1023, 1024, 1025])
+    E = len(SEGMENTS) + 3
+    w, x, rw = _data(E, 72, 40, ids, dtype, False, 9)
+    dy = torch.randn((len(ids), 1, 72), generator=torch.Generator().manual_seed(10)).to(dtype)
+    got = moe.moe_mul_mat_id_backward(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), dy.cuda(), d_w_dtype=F32)
+    want = ref.grads(w.double(), x.double(), ids, dy.double(), None, False, dtype, F32)
+    ref.within(got[0], *want[0], "d_src1")
+    ref.within(got[1], *want[1], "d_w")
