@@ -52,9 +52,9 @@ __device__ __attribute__((aligned(16))) const uint32_t g_zero[4] = {0, 0, 0, 0};
 
 constexpr int kMChunk = 4;   // M tiles sharing each weight slab in turn
 
-// 16-byte chunk c of row r sits at c ^ swz(r). Rows of 128 bytes: 16 rows reading the same chunk
-// cover all 64 banks.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// 16-byte chunk c of row r sits at c ^ swz(r): the rows of a phase of ds_read_b128 cover the banks once.
+template <int RB>
+__device__ __forceinline__ int swz(int r) { return RB == 64 ? (r >> 2) & 3 : (r & 7) ^ ((r >> 3) & 1); }
 // Rows that are read transposed (four rows, 32 or 64 bytes of each, at a time): the four rows'
 // chunks are apart in both 128 and 256 bytes.
 __device__ __forceinline__ int swz_t(int r) { return ((r & 3) << 2) | (r & 2); }
@@ -70,15 +70,18 @@ __device__ __forceinline__ i32x4 read_t(const uint8_t* p) {
     return i32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// Geometry: WM x WN waves, each SM x SN tiles of 32 x 32 at most; NS ring slots.
-template <int WM_, int WN_, int SM_, int SN_, int NS_, int OCC_>
+// Geometry: WM x WN waves, each SM x SN tiles of 32 x 32 at most; a ring of NS slots, RB bytes of every row in
+// each; OCC waves a SIMD.
+template <int WM_, int WN_, int SM_, int SN_, int RB_, int NS_, int OCC_>
 struct Tile {
-    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, NS = NS_, OCC = OCC_;
+    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, RB = RB_, NS = NS_, OCC = OCC_;
     static constexpr int waves = WM * WN, threads = 64 * waves;
     static constexpr int BM = 32 * WM * SM, BN = 32 * WN * SN;
-    static constexpr int stage = (BM + BN) * 128;   // a stage is 128 bytes of every row
+    static constexpr int stage = (BM + BN) * RB;
     static constexpr int lds = NS * stage;
 };
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 // M tile and column tile of this block: tiles ordered by expert, chunk of M tiles, column tile,
 // an eighth of them to each XCD. False: none.
@@ -114,7 +117,8 @@ __device__ __forceinline__ bool find_tile(const ExpertGemm& P, int n_nt, Where& 
 template <class T, int TR, bool OUT16, class G>
 __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     using Elem = typename T::Elem;
-    constexpr int KS = 128 / (int)sizeof(Elem);   // reduction elements per stage
+    constexpr int RB = G::RB, W = G::waves;
+    constexpr int KS = RB / (int)sizeof(Elem);    // reduction elements per stage
     constexpr int EC = 16 / (int)sizeof(Elem);    // elements of a chunk
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int cols = TR ? P.K : P.N, depth = TR ? P.N : P.K;
@@ -129,26 +133,26 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     const int nst = (depth + KS - 1) / KS;
     const void* zero = g_zero;
 
-    // ---- copies of a stage, 1 KB each: activation rows (8 a copy), weights
-    constexpr int CA = G::BM / 8 / G::waves, CB = G::BN / 8 / G::waves;
-    static_assert(CA * 8 * G::waves == G::BM && CB * 8 * G::waves == G::BN, "whole copies per wave");
+    // ---- copies of a stage, 1 KB each: activation rows, 1024 / RB a copy and dealt out to the waves in turn (so
+    // that a shorter tile's rows are the first copies of all of them), then weights
+    constexpr int CR = 1024 / RB, CL = RB / 16;   // rows of a copy, lanes of a row
+    constexpr int CA = (G::BM / CR + W - 1) / W, CB = G::BN / CR / W;
+    static_assert(CB * CR * W == G::BN, "whole copies per wave");
     const uint8_t* ap[CA];
-    int a_k[CA];   // first reduction element of this lane's chunk
+    const int a_k = ((lane % CL) ^ swz<RB>(lane / CL + (CR == 8 ? 8 * (wv & 1) : 0))) * EC;   // of this lane's chunk
+    static_assert(CR == 16 || W % 2 == 0, "a wave's copies differ in multiples of 16 rows");
 #pragma unroll
     for (int i = 0; i < CA; i++) {
-        // copies i of all the waves together are rows 8 waves i .. +8 waves - 1: the first MACT of them hold the
-        // rows of the first MACT sub-tiles
-        const int R = (i * G::waves + wv) * 8 + (lane >> 3), lc = (lane & 7) ^ swz(R);
+        const int R = (i * W + wv) * CR + lane / CL;
         const int j = m0 + min(R, m_len - 1);
         const int64_t row = P.a_rows ? P.a_rows[j] : j;
-        a_k[i] = lc * EC;
-        ap[i] = (const uint8_t*)P.A + (row * P.lda + lc * EC) * (int64_t)sizeof(Elem);
+        ap[i] = (const uint8_t*)P.A + (row * P.lda + a_k) * (int64_t)sizeof(Elem);
     }
-    constexpr int BROW = TR ? G::BN * 2 : 128;        // bytes of a row of the weight tile in LDS
-    constexpr int BLR = BROW / 16;                    // lanes of a row
+    constexpr int BROW = TR ? G::BN * 2 : RB;        // bytes of a row of the weight tile in LDS
+    constexpr int BLR = BROW / 16;                   // lanes of a row
     const uint8_t* bp[CB];
-    int b_k[CB];
-    const int64_t bstep = TR ? (int64_t)KS * P.K * (int)sizeof(Elem) : 128;
+    int b_k[CB];   // reduction element of this lane's chunk
+    const int64_t bstep = TR ? (int64_t)KS * P.K * (int)sizeof(Elem) : RB;
 #pragma unroll
     for (int i = 0; i < CB; i++) {
         const int R = (wv * CB + i) * (64 / BLR) + lane / BLR;
@@ -157,77 +161,108 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
             b_k[i] = R;
             bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + R) * P.K + c) * (int64_t)sizeof(Elem);
         } else {
-            const int lc = (lane & 7) ^ swz(R);
-            b_k[i] = lc * EC;
-            bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + min(col0 + R, cols - 1)) * P.K + lc * EC) * (int64_t)sizeof(Elem);
+            b_k[i] = ((lane % CL) ^ swz<RB>(R)) * EC;
+            bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + min(col0 + R, cols - 1)) * P.K + b_k[i]) * (int64_t)sizeof(Elem);
         }
     }
-    auto issue = [&](int s, int slot, auto n_c) __attribute__((always_inline)) {
+    // copies of stage s; TA: the tile's activation copies
+    auto issue = [&](int s, int slot, auto ta_c) __attribute__((always_inline)) {
+        constexpr int TA = decltype(ta_c)::value;
         const uint32_t st = lds0 + (uint32_t)(slot * G::stage);
         const int k0 = s * KS;
         const bool full = k0 + KS <= depth;   // what passes the end is zero on both sides
+        const bool a_in = full || k0 + a_k < depth;
 #pragma unroll
-        for (int i = 0; i < decltype(n_c)::value; i++) {
-            dma16v(full || k0 + a_k[i] < depth ? (const void*)ap[i] : zero, st + (i * G::waves + wv) * 1024);
-            ap[i] += 128;
+        for (int i = 0; i < (TA + W - 1) / W; i++) {
+            if (i * W + W <= TA || i * W + wv < TA) {
+                dma16v(a_in ? (const void*)ap[i] : zero, st + (i * W + wv) * 1024);
+                ap[i] += RB;
+            }
         }
 #pragma unroll
         for (int i = 0; i < CB; i++) {
-            dma16v(full || k0 + b_k[i] < depth ? (const void*)bp[i] : zero, st + G::BM * 128 + (wv * CB + i) * 1024);
+            dma16v(full || k0 + b_k[i] < depth ? (const void*)bp[i] : zero, st + G::BM * RB + (wv * CB + i) * 1024);
             bp[i] += bstep;
         }
     };
 
     typename T::Acc acc[G::SM][G::SN];
+    const int l16 = lane & 15;
+    const uint32_t a_lane = (wm * 32 + l32) * RB;
+    uint32_t b_lane[G::SN];
+#pragma unroll
+    for (int c = 0; c < G::SN; c++)
+        b_lane[c] = TR ? (8 * h + (l16 >> 2)) * BROW + (l16 & 1) * 8 +
+                             ((((wn * G::SN + c) * 4 + ((lane >> 4) & 1) * 2 + ((l16 >> 1) & 1)) ^ swz_t(l16 >> 2)) << 4)
+                       : ((wn * G::SN + c) * 32 + l32) * RB;
+    struct Frag {
+        i32x4 a[G::SM], b[G::SN];
+    };
+    // operands of 32-byte step q of the stage in a slot
+    auto read = [&](Frag& f, int slot, int q, auto n_c) __attribute__((always_inline)) {
+        const uint8_t* st = smem + slot * G::stage;
+        const uint32_t ch = (uint32_t)((2 * q + h) ^ swz<RB>(l32)) << 4;
+#pragma unroll
+        for (int c = 0; c < G::SN; c++) {
+            if (TR) f.b[c] = read_t<BROW>(st + G::BM * RB + b_lane[c] + q * 16 * BROW);
+            else f.b[c] = *(const i32x4*)(st + G::BM * RB + b_lane[c] + ch);
+        }
+#pragma unroll
+        for (int i = 0; i < decltype(n_c)::value; i++) f.a[i] = *(const i32x4*)(st + a_lane + i * G::WM * 32 * RB + ch);
+    };
+    auto multiply = [&](const Frag& f, auto n_c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < decltype(n_c)::value; i++)
+#pragma unroll
+            for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(f.a[i], f.b[c], acc[i][c]);
+    };
     auto k_loop = [&](auto n_c) __attribute__((always_inline)) {
-        constexpr int MACT = decltype(n_c)::value;
-        constexpr int copies = MACT * CA / G::SM + CB;
-        using NA = std::integral_constant<int, MACT * CA / G::SM>;
-        static_assert(CA % G::SM == 0, "a sub-tile's copies are whole");
+        constexpr int MACT = decltype(n_c)::value, TA = MACT * 32 * G::WM / CR, Q = RB / 32;
+        constexpr int few = (TA / W + CB) * (G::NS - 2), more = ((TA + W - 1) / W + CB) * (G::NS - 2);
+        using NA = Int<TA>;
+        static_assert(MACT * 32 * G::WM % CR == 0, "a sub-tile's copies are whole");
 #pragma unroll
         for (int i = 0; i < MACT; i++)
 #pragma unroll
             for (int c = 0; c < G::SN; c++) acc[i][c] = typename T::Acc{};
-        const int l16 = lane & 15;
-        const uint32_t a_lane = l32 * 128 + wm * 4096;
-        uint32_t b_lane[G::SN];
-#pragma unroll
-        for (int c = 0; c < G::SN; c++)
-            b_lane[c] = TR ? (8 * h + (l16 >> 2)) * BROW + (l16 & 1) * 8 +
-                                 ((((wn * G::SN + c) * 4 + ((lane >> 4) & 1) * 2 + ((l16 >> 1) & 1)) ^ swz_t(l16 >> 2)) << 4)
-                           : ((wn * G::SN + c) * 32 + l32) * 128;
+        // stage s landed; of the copies only those of the NS - 2 stages after it may be in flight
+        auto landed = [&](int s) __attribute__((always_inline)) {
+            if (s + G::NS - 2 >= nst) wait_vm<0>();
+            else if (few == more || wv < TA % W) wait_vm<more>();
+            else wait_vm<few>();
+            wait_stage_and_barrier<63>();
+        };
         for (int s = 0; s < G::NS - 1 && s < nst; s++) issue(s, s, NA{});
+        landed(0);
+        if (G::NS - 1 < nst) issue(G::NS - 1, G::NS - 1, NA{});
+        Frag f0, f1;
+        read(f0, 0, 0, n_c);
         int slot = 0;
+        // at the loop's head: step 0 of stage s in f0, stage s + NS - 1 on its way
         for (int s = 0; s < nst; s++) {
-            // stage s landed (the copies of NS - 2 later stages may be in flight), and every wave is past stage s - 1
-            if (s + G::NS - 2 < nst) wait_stage_and_barrier<(G::NS - 2) * copies>();
-            else wait_stage_and_barrier<0>();
-            if (s + G::NS - 1 < nst) issue(s + G::NS - 1, slot == 0 ? G::NS - 1 : slot - 1, NA{});
-            const uint8_t* st = smem + slot * G::stage;
-            slot = slot == G::NS - 1 ? 0 : slot + 1;
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const uint32_t ch = (uint32_t)((2 * q + h) ^ swz(l32)) << 4;
-                i32x4 a[MACT], b[G::SN];
-#pragma unroll
-                for (int c = 0; c < G::SN; c++) {
-                    if (TR) b[c] = read_t<BROW>(st + G::BM * 128 + b_lane[c] + q * 16 * BROW);
-                    else b[c] = *(const i32x4*)(st + G::BM * 128 + b_lane[c] + ch);
-                }
-#pragma unroll
-                for (int i = 0; i < MACT; i++) a[i] = *(const i32x4*)(st + a_lane + i * G::WM * 4096 + ch);
-#pragma unroll
-                for (int i = 0; i < MACT; i++)
-#pragma unroll
-                    for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(a[i], b[c], acc[i][c]);
+            for (int q = 0; q + 1 < Q; q++) {
+                read(q & 1 ? f0 : f1, slot, q + 1, n_c);
+                multiply(q & 1 ? f1 : f0, n_c);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            // this wave's reads of stage s are done, the other waves' too after the barrier
+            const int next = slot == G::NS - 1 ? 0 : slot + 1;
+            if (s + 1 < nst) {
+                landed(s + 1);
+                if (s + G::NS < nst) issue(s + G::NS, slot, NA{});
+                read(f0, next, 0, n_c);
+            }
+            slot = next;
+            multiply(f1, n_c);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
     const int mact = (m_len + 32 * G::WM - 1) / (32 * G::WM);   // occupied sub-tiles (block-uniform)
-    if (G::SM >= 4 && mact >= 4) k_loop(std::integral_constant<int, G::SM >= 4 ? 4 : 1>{});
-    else if (G::SM >= 3 && mact == 3) k_loop(std::integral_constant<int, G::SM >= 3 ? 3 : 1>{});
-    else if (G::SM >= 2 && mact == 2) k_loop(std::integral_constant<int, G::SM >= 2 ? 2 : 1>{});
-    else k_loop(std::integral_constant<int, 1>{});
+    if (G::SM >= 4 && mact >= 4) k_loop(Int<(G::SM >= 4 ? 4 : 1)>{});
+    else if (G::SM >= 3 && mact == 3) k_loop(Int<(G::SM >= 3 ? 3 : 1)>{});
+    else if (G::SM >= 2 && mact == 2) k_loop(Int<(G::SM >= 2 ? 2 : 1)>{});
+    else k_loop(Int<1>{});
 
     // ---- output rows (and what scales them) into the now idle ring
     int32_t* s_row = (int32_t*)smem;
@@ -267,20 +302,22 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
 }
 
 // ---------------------------------------------------------------- expert gradient
-// dW_e tile of BM rows (n) x BN columns (k); the reduction runs along e's positions, 64 a stage, both operands
+// dW_e tile of BM rows (n) x BN columns (k); the reduction runs along e's positions, KS a stage, both operands
 // read transposed. WEIGHTED: dY row j times route_w of its slot, rounded to the element type.
-constexpr int kMapRows = 1024;   // positions whose rows are in LDS at a time
+constexpr int kMapRows = 512;   // ring of positions whose rows are in LDS, refilled by halves
 
 template <class T, bool WEIGHTED, class G>
 __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     using Elem = typename T::Elem;
-    constexpr int KS = 64;
+    constexpr int W = G::waves, NS = G::NS;
+    constexpr int KS = G::RB / 2, Q = KS / 16, kHalf = kMapRows / 2 / KS;   // positions and MFMA steps of a stage; stages of half a map
+    static_assert(NS < kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
     constexpr int AROW = G::BM * 2, BROW = G::BN * 2, ALR = AROW / 16, BLR = BROW / 16;
     constexpr int stage = KS * (AROW + BROW);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int32_t* s_dy = (int32_t*)(smem + G::NS * stage);   // rows of dY and X of positions j0 ..
+    int32_t* s_dy = (int32_t*)(smem + NS * stage);   // rows of dY and X of the positions
     int32_t* s_x = s_dy + kMapRows;
-    float* s_w = (float*)(s_x + kMapRows);              // WEIGHTED: their routing weights
+    float* s_w = (float*)(s_x + kMapRows);           // WEIGHTED: their routing weights
 
     const int n_nt = (P.N + G::BM - 1) / G::BM, n_kt = (P.K + G::BN - 1) / G::BN;
     const int64_t total = (int64_t)P.E * n_nt * n_kt, part = (total + 7) >> 3;
@@ -297,7 +334,19 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     const int nst = (len + KS - 1) / KS;
     const void* zero = g_zero;
 
-    constexpr int CA = KS * ALR / 64 / G::waves, CB = KS * BLR / 64 / G::waves;
+    // rows of half a map from position `from` of the segment on: 64 a copy
+    auto map = [&](int from) __attribute__((always_inline)) {
+        const uint32_t at = lds0 + NS * stage + (from & (kMapRows - 1)) * 4;
+        for (int i = wv; i < kMapRows / 128; i += W) {
+            const int p = from + 64 * i + lane;
+            const bool in = p < len;
+            dma4v(in ? (const void*)(P.dy_rows + j0 + p) : zero, at + 256 * i);
+            dma4v(in ? (const void*)(P.x_rows + j0 + p) : zero, at + kMapRows * 4 + 256 * i);
+            if (WEIGHTED) dma4v(in ? (const void*)(P.pos_w + j0 + p) : zero, at + kMapRows * 8 + 256 * i);
+        }
+    };
+    constexpr int CA = KS * ALR / 64 / W, CB = KS * BLR / 64 / W;
+    static_assert(CA * 64 * W == KS * ALR && CB * 64 * W == KS * BLR, "whole copies per wave");
     auto issue = [&](int s, int slot) __attribute__((always_inline)) {
         const uint32_t st = lds0 + (uint32_t)(slot * stage);
 #pragma unroll
@@ -315,16 +364,6 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
             dma16v(j < len ? (const void*)p : zero, st + KS * AROW + (wv * CB + i) * 1024);
         }
     };
-    // rows of positions jb .. of the segment (jb a multiple of kMapRows), row 0 past its end
-    auto map = [&](int jb) {
-        for (int i = tid; i < kMapRows; i += G::threads) {
-            const int j = j0 + jb + i;
-            const bool in = jb + i < len;
-            s_dy[i] = in ? P.dy_rows[j] : 0;
-            s_x[i] = in ? P.x_rows[j] : 0;
-            if (WEIGHTED) s_w[i] = in ? P.route_w[P.slots[j]] : 0.f;
-        }
-    };
 
     f32x16 acc[G::SM][G::SN];
 #pragma unroll
@@ -339,62 +378,105 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
 #pragma unroll
     for (int c = 0; c < G::SN; c++)
         b_lane[c] = r4 * BROW + (l16 & 1) * 8 + ((((wn * G::SN + c) * 4 + piece) ^ swz_t(l16 >> 2)) << 4);
-
-    for (int s = 0; s < nst; s++) {
-        if ((s & (kMapRows / KS - 1)) == 0) {   // a ring of two slots: the copies of a stage ahead end at the map's end
-            __syncthreads();
-            map(s * KS);
-            __syncthreads();
-            issue(s, s & 1);
-        }
-        wait_stage_and_barrier<0>();
-        if (s + 1 < nst && ((s + 1) & (kMapRows / KS - 1))) issue(s + 1, (s + 1) & 1);
-        const uint8_t* st = smem + (s & 1) * stage;
+    struct Frag {
+        i32x4 a[G::SM], b[G::SN];
+    };
+    auto read = [&](Frag& f, int s, int slot, int q) __attribute__((always_inline)) {
+        const uint8_t* st = smem + slot * stage;
 #pragma unroll
-        for (int q = 0; q < KS / 16; q++) {
-            i32x4 a[G::SM], b[G::SN];
+        for (int c = 0; c < G::SN; c++) f.b[c] = read_t<BROW>(st + KS * AROW + b_lane[c] + q * 16 * BROW);
 #pragma unroll
-            for (int c = 0; c < G::SN; c++) b[c] = read_t<BROW>(st + KS * AROW + b_lane[c] + q * 16 * BROW);
+        for (int i = 0; i < G::SM; i++) f.a[i] = read_t<AROW>(st + a_lane[i] + q * 16 * AROW);
+        if (WEIGHTED) {
+            typedef Elem Vec __attribute__((ext_vector_type(8)));
+            const float* w = s_w + ((s * KS) & (kMapRows - 1)) + q * 16 + 8 * h;
 #pragma unroll
-            for (int i = 0; i < G::SM; i++) a[i] = read_t<AROW>(st + a_lane[i] + q * 16 * AROW);
-            if (WEIGHTED) {
-                typedef Elem Vec __attribute__((ext_vector_type(8)));
-                const float* w = s_w + ((s * KS) & (kMapRows - 1)) + q * 16 + 8 * h;
+            for (int i = 0; i < G::SM; i++) {
+                Vec v = __builtin_bit_cast(Vec, f.a[i]);
 #pragma unroll
-                for (int i = 0; i < G::SM; i++) {
-                    Vec v = __builtin_bit_cast(Vec, a[i]);
-#pragma unroll
-                    for (int u = 0; u < 8; u++) v[u] = (Elem)((float)v[u] * w[u]);
-                    a[i] = __builtin_bit_cast(i32x4, v);
-                }
+                for (int u = 0; u < 8; u++) v[u] = (Elem)((float)v[u] * w[u]);
+                f.a[i] = __builtin_bit_cast(i32x4, v);
             }
+        }
+    };
+    auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < G::SM; i++)
+        for (int i = 0; i < G::SM; i++)
 #pragma unroll
-                for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(a[i], b[c], acc[i][c]);
+            for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(f.a[i], f.b[c], acc[i][c]);
+    };
+    if (nst > 0) {
+        // stage s landed; of the copies only those of the NS - 2 stages after it may be in flight (a map's copies
+        // among them make it wait for more)
+        auto landed = [&](int s) __attribute__((always_inline)) {
+            if (s + NS - 2 >= nst) wait_stage_and_barrier<0>();
+            else wait_stage_and_barrier<(CA + CB) * (NS - 2)>();
+        };
+        map(0);
+        if (len > kMapRows / 2) map(kMapRows / 2);
+        wait_stage_and_barrier<0>();
+        for (int s = 0; s < NS - 1 && s < nst; s++) issue(s, s);
+        landed(0);
+        if (NS - 1 < nst) issue(NS - 1, NS - 1);
+        Frag f0, f1;
+        read(f0, 0, 0, 0);
+        int slot = 0;
+        for (int s = 0; s < nst; s++) {
+#pragma unroll
+            for (int q = 0; q + 1 < Q; q++) {
+                read(q & 1 ? f0 : f1, s, slot, q + 1);
+                multiply(q & 1 ? f1 : f0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            const int next = slot == NS - 1 ? 0 : slot + 1;
+            if (s + 1 < nst) {
+                landed(s + 1);
+                if (s + NS < nst) {
+                    issue(s + NS, slot);
+                    // The half of the map that holds stage s and the kHalf - 1 before it has served, once s is its
+                    // last stage: the rows two halves on take its place, needed kHalf - NS + 1 stages from now.
+                    if ((s + 1) % kHalf == 0 && (s + 1 + kHalf) * KS < len) map((s + 1 + kHalf) * KS);
+                }
+                read(f0, s + 1, next, 0);
+            }
+            slot = next;
+            multiply(f1);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
+
+    // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the tile, column l % 32
 #pragma unroll
     for (int c = 0; c < G::SN; c++) {
         const int col = col0 + (wn * G::SN + c) * 32 + l32;
-        if (col >= P.K) continue;
+        const bool in = col < P.K;
 #pragma unroll
         for (int i = 0; i < G::SM; i++) {
+            const int row = row0 + (wm * G::SM + i) * 32 + 4 * h;
 #pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int row = row0 + (wm * G::SM + i) * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
-                if (row >= P.N) continue;
-                const int64_t o = ((int64_t)e * P.N + row) * P.K + col;
-                if (P.f32) ((float*)P.dW)[o] = acc[i][c][v];
-                else ((Elem*)P.dW)[o] = (Elem)acc[i][c][v];
+            for (int v = 0; v < 16; v += 2) {
+                const int r = row + 8 * (v >> 2) + (v & 3);
+                const int64_t o = ((int64_t)e * P.N + r) * P.K + col;
+                if (P.f32) {
+                    if (in && r < P.N) ((float*)P.dW)[o] = acc[i][c][v];
+                    if (in && r + 1 < P.N) ((float*)P.dW)[o + P.K] = acc[i][c][v + 1];
+                } else {
+                    // two columns a store: even lanes take row r of both, odd lanes row r + 1
+                    const bool odd = lane & 1;
+                    const float give = odd ? acc[i][c][v] : acc[i][c][v + 1];
+                    const float got = __shfl_xor(give, 1);
+                    typedef Elem Pair __attribute__((ext_vector_type(2)));
+                    const Pair pair = {(Elem)(odd ? got : acc[i][c][v]), (Elem)(odd ? acc[i][c][v + 1] : got)};
+                    if (in && r + odd < P.N) *(Pair*)((Elem*)P.dW + o + (odd ? P.K - 1 : 0)) = pair;
+                }
             }
         }
     }
 }
 
-using Wide = Tile<2, 4, 4, 2, 2, 2>;     // 256 x 256, one block a CU
-using Narrow = Tile<1, 4, 2, 1, 3, 2>;   // 64 x 128, two blocks a CU
-using GradW = Tile<2, 4, 4, 2, 2, 2>;
+using Wide = Tile<2, 4, 4, 2, 64, 5, 2>;      // 256 x 256, one block a CU
+using Narrow = Tile<1, 4, 2, 1, 128, 3, 2>;   // 64 x 128, two blocks a CU
+using GradW = Tile<1, 4, 4, 2, 64, 3, 2>;     // 128 x 256, two blocks a CU
 
 template <class T, int TR, bool OUT16, class G>
 hipError_t launch(const ExpertGemm& a, hipStream_t st) {
@@ -413,7 +495,7 @@ hipError_t launch_tile(const ExpertGemm& a, hipStream_t st) {
 template <class T, bool WEIGHTED>
 hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
     using G = GradW;
-    constexpr int lds = G::NS * 64 * 2 * (G::BM + G::BN) + kMapRows * 12;
+    constexpr int lds = G::lds + kMapRows * (WEIGHTED ? 12 : 8);
     static PerDeviceOnce cap;
     if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, WEIGHTED, G>, lds)) return e;
     k_grad_w<T, WEIGHTED, G><<<(unsigned)expert_grad_w_grid(a), G::threads, lds, st>>>(a);
@@ -448,8 +530,8 @@ hipError_t launch_expert_grad_x(const ExpertGemm& a, hipStream_t st) {
 }
 
 hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st) {
-    if (a.type == kElemBf16) return a.route_w ? launch_w<Bf16, true>(a, st) : launch_w<Bf16, false>(a, st);
-    return a.route_w ? launch_w<F16, true>(a, st) : launch_w<F16, false>(a, st);
+    if (a.type == kElemBf16) return a.pos_w ? launch_w<Bf16, true>(a, st) : launch_w<Bf16, false>(a, st);
+    return a.pos_w ? launch_w<F16, true>(a, st) : launch_w<F16, false>(a, st);
 }
 
 }  // namespace moe

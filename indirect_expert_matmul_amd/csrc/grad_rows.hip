@@ -81,7 +81,20 @@ __global__ __launch_bounds__(kThreads) void k_grad_rows(GradRowsArgs a) {
     }
 }
 
+__global__ __launch_bounds__(kThreads) void k_pos_w(PosWArgs a) {
+    const int64_t n = a.bounds[a.E];
+    for (int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x; j < n; j += (int64_t)gridDim.x * kThreads)
+        a.pos_w[j] = a.route_w[a.slots[j]];
+}
+
 }  // namespace
+
+hipError_t launch_pos_w(const PosWArgs& a, hipStream_t st) {
+    if (a.n <= 0) return hipSuccess;
+    const int64_t blocks = (a.n + kThreads - 1) / kThreads;
+    k_pos_w<<<(unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
 
 hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st) {
     const int64_t n = a.rows * (a.ld / 8);

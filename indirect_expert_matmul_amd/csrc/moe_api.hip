@@ -844,6 +844,7 @@ struct GradPlan {
     int64_t ld;     // row length of dY
     void* dy;       // d_dst in the experts' type, rows of ld (nullptr: d_dst itself)
     float* g;       // per-slot rows of g
+    float* pos_w;   // weighted d_w: route_w by position
 };
 // dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
 GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int want,
@@ -855,6 +856,7 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     p.ld = (w->rows + 7) / 8 * 8;
     if (!dy_as_is) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
+    if (weighted && (want & kWantW)) p.pos_w = (float*)c.take((size_t)n * 4);
     if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
     return p;
 }
@@ -1618,9 +1620,8 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.X = src1;
     gw.dy_rows = g.a_rows;
     gw.x_rows = B == 1 ? p.r.ids_src1 : p.r.ids_dst;
-    gw.slots = p.r.ids_dst;
     gw.bounds = p.r.bounds;
-    gw.route_w = route_w;
+    gw.pos_w = p.pos_w;
     gw.dW = d_w;
     gw.f32 = d_w_type == MOE_F32;
     const bool rows_wanted = (want & (kWantX | kWantR)) && n > 0;
@@ -1669,6 +1670,12 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         tm.end();
     }
     if (d_w) {
+        if (p.pos_w && n > 0) {
+            const PosWArgs pw{route_w, p.r.ids_dst, p.r.bounds, n, E, p.pos_w};
+            tm.begin();
+            if ((s = hip_check(launch_pos_w(pw, st), "route_w by position"))) return s;
+            tm.end();
+        }
         tm.begin();
         if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
         tm.end();

@@ -296,9 +296,9 @@ struct ExpertGradW {
     const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
     int32_t ldy;               // a multiple of 8
     const void* X;             // rows of K
-    const int32_t *dy_rows, *x_rows, *slots;   // of position j: rows of dY and X, slot
+    const int32_t *dy_rows, *x_rows;   // of position j: rows of dY and X
     const int32_t* bounds;     // [E + 1]
-    const float* route_w;      // nullptr, or a factor for each slot
+    const float* pos_w;        // nullptr, or a factor for each position's row of dY
     void* dW;                  // [E][N][K], float32 (f32) or the element type
     int32_t f32;
 };
@@ -322,6 +322,15 @@ struct CastRowsArgs {
     void* dst;
 };
 hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st);
+// pos_w[j] = route_w[slots[j]] of the positions below bounds[E]
+struct PosWArgs {
+    const float* route_w;
+    const int32_t *slots, *bounds;
+    int64_t n;
+    int32_t E;
+    float* pos_w;
+};
+hipError_t launch_pos_w(const PosWArgs& a, hipStream_t st);
 struct GradRowsArgs {
     ElemType type;
     const float* g;          // [rows * k][K]
