@@ -22,6 +22,7 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // An element type: its 32x32 MFMA takes 16 bytes a lane of each operand, lane half h the bytes
@@ -70,25 +71,41 @@ __device__ __forceinline__ i32x4 read_t(const uint8_t* p) {
     return i32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
-// Geometry: WM x WN waves, each SM x SN tiles of 32 x 32 at most; a ring of NS slots, RB bytes of every row in
-// each; OCC waves a SIMD.
-template <int WM_, int WN_, int SM_, int SN_, int RB_, int NS_, int OCC_>
+// Geometry: WM x WN waves, each SM x SN tiles of 32 x 32; RB bytes of every row a stage, rings of NSA slots for the
+// first operand (activations) and NSB >= NSA for the second (weights); OCC waves a SIMD. TX: rows that a segment's
+// tiles may have beyond BM (the last ring slot of the weights makes room for them).
+template <int WM_, int WN_, int SM_, int SN_, int RB_, int NSA_, int NSB_, int OCC_, int TX_ = 0>
 struct Tile {
-    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, RB = RB_, NS = NS_, OCC = OCC_;
+    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, RB = RB_, NSA = NSA_, NSB = NSB_, OCC = OCC_, TX = TX_;
     static constexpr int waves = WM * WN, threads = 64 * waves;
-    static constexpr int BM = 32 * WM * SM, BN = 32 * WN * SN;
-    static constexpr int stage = (BM + BN) * RB;
-    static constexpr int lds = NS * stage;
+    static constexpr int BM = 32 * WM * SM, BN = 32 * WN * SN, MX = SM + TX / (32 * WM);
+    static constexpr int a_slot = BM * RB, b_slot = BN * RB;
+    static constexpr int lds = NSA * a_slot + NSB * b_slot;
+    static_assert(NSA * TX * RB <= (NSB - NSA) * b_slot, "room for the taller tiles");
 };
 template <int N>
 using Int = std::integral_constant<int, N>;
+
+// The neighbour's value (lane ^ 1).
+__device__ __forceinline__ float swap1(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xb1, 0xf, 0xf, true));
+}
+// Two columns a store: of the values of rows r and r + 1 in columns c (even lanes) and c + 1 (odd lanes), even lanes
+// get row r of both columns, odd lanes row r + 1.
+template <class Elem>
+__device__ __forceinline__ uint32_t pair_up(float a, float b, bool odd) {
+    const float got = swap1(odd ? a : b);
+    typedef Elem Pair __attribute__((ext_vector_type(2)));
+    const Pair p = {(Elem)(odd ? got : a), (Elem)(odd ? b : got)};
+    return __builtin_bit_cast(uint32_t, p);
+}
 
 // M tile and column tile of this block: tiles ordered by expert, chunk of M tiles, column tile,
 // an eighth of them to each XCD. False: none.
 struct Where {
     int e, m0, m_len, nt;
 };
-template <int BM>
+template <int BM, int TX>
 __device__ __forceinline__ bool find_tile(const ExpertGemm& P, int n_nt, Where& w) {
     const int b = (int)blockIdx.x;
     const int total = P.tile_off[P.E] * n_nt;
@@ -99,7 +116,7 @@ __device__ __forceinline__ bool find_tile(const ExpertGemm& P, int n_nt, Where& 
     const int first = __builtin_amdgcn_readfirstlane(ti.y);
     const int row0 = __builtin_amdgcn_readfirstlane(ti.z);
     const int rows = __builtin_amdgcn_readfirstlane(ti.w);
-    const int tiles = (rows + BM - 1) / BM;
+    const int tiles = tiles_of(rows, BM, TX);
     const int r = t - n_nt * first;
     const int c = r / (kMChunk * n_nt);
     const int g = min(kMChunk, tiles - c * kMChunk);
@@ -123,20 +140,22 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int cols = TR ? P.K : P.N, depth = TR ? P.N : P.K;
     Where at;
-    if (!find_tile<G::BM>(P, (cols + G::BN - 1) / G::BN, at)) return;
+    if (!find_tile<G::BM, G::TX>(P, (cols + G::BN - 1) / G::BN, at)) return;
     const int e = at.e, m0 = at.m0, m_len = at.m_len, col0 = at.nt * G::BN;
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wv % G::WM, wn = wv / G::WM;
+    const int wm = wv / G::WN, wn = wv % G::WN;   // waves of a SIMD (wv, wv + 4) share the columns: uneven rows meet there
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
     const int nst = (depth + KS - 1) / KS;
+    const int subs = (m_len + 31) >> 5;           // 32-row sub-tiles: of wave row wm, wm, wm + WM, ...
     const void* zero = g_zero;
 
     // ---- copies of a stage, 1 KB each: activation rows, 1024 / RB a copy and dealt out to the waves in turn (so
     // that a shorter tile's rows are the first copies of all of them), then weights
     constexpr int CR = 1024 / RB, CL = RB / 16;   // rows of a copy, lanes of a row
-    constexpr int CA = (G::BM / CR + W - 1) / W, CB = G::BN / CR / W;
+    constexpr int CA = ((G::BM + G::TX) / CR + W - 1) / W, CB = G::BN / CR / W;
+    const int n_copies = subs * (32 / CR);
     static_assert(CB * CR * W == G::BN, "whole copies per wave");
     const uint8_t* ap[CA];
     const int a_k = ((lane % CL) ^ swz<RB>(lane / CL + (CR == 8 ? 8 * (wv & 1) : 0))) * EC;   // of this lane's chunk
@@ -165,28 +184,21 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
             bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + min(col0 + R, cols - 1)) * P.K + b_k[i]) * (int64_t)sizeof(Elem);
         }
     }
-    // copies of stage s; TA: the tile's activation copies
-    auto issue = [&](int s, int slot, auto ta_c) __attribute__((always_inline)) {
-        constexpr int TA = decltype(ta_c)::value;
-        const uint32_t st = lds0 + (uint32_t)(slot * G::stage);
-        const int k0 = s * KS;
-        const bool full = k0 + KS <= depth;   // what passes the end is zero on both sides
-        const bool a_in = full || k0 + a_k < depth;
-#pragma unroll
-        for (int i = 0; i < (TA + W - 1) / W; i++) {
-            if (i * W + W <= TA || i * W + wv < TA) {
-                dma16v(a_in ? (const void*)ap[i] : zero, st + (i * W + wv) * 1024);
-                ap[i] += RB;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CB; i++) {
-            dma16v(full || k0 + b_k[i] < depth ? (const void*)bp[i] : zero, st + G::BM * RB + (wv * CB + i) * 1024);
-            bp[i] += bstep;
+    // copy i of a wave's: of a stage's activations, of its weights; to: the ring slot
+    auto copy_a = [&](int i, int s, uint32_t to) __attribute__((always_inline)) {
+        if (i * W + wv < n_copies) {
+            const bool in = s * KS + a_k < depth;   // what passes the end is zero on both sides
+            dma16v(in ? (const void*)ap[i] : zero, lds0 + to + (i * W + wv) * 1024);
+            ap[i] += RB;
         }
     };
+    auto copy_b = [&](int i, int s, uint32_t to) __attribute__((always_inline)) {
+        const bool in = s * KS + b_k[i] < depth;
+        dma16v(in ? (const void*)bp[i] : zero, lds0 + to + (wv * CB + i) * 1024);
+        bp[i] += bstep;
+    };
 
-    typename T::Acc acc[G::SM][G::SN];
+    typename T::Acc acc[G::MX][G::SN];
     const int l16 = lane & 15;
     const uint32_t a_lane = (wm * 32 + l32) * RB;
     uint32_t b_lane[G::SN];
@@ -196,79 +208,115 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
                              ((((wn * G::SN + c) * 4 + ((lane >> 4) & 1) * 2 + ((l16 >> 1) & 1)) ^ swz_t(l16 >> 2)) << 4)
                        : ((wn * G::SN + c) * 32 + l32) * RB;
     struct Frag {
-        i32x4 a[G::SM], b[G::SN];
+        i32x4 a[G::MX], b[G::SN];
     };
-    // operands of 32-byte step q of the stage in a slot
-    auto read = [&](Frag& f, int slot, int q, auto n_c) __attribute__((always_inline)) {
-        const uint8_t* st = smem + slot * G::stage;
+    // operands of 32-byte step q of the stage in these slots
+    auto read = [&](Frag& f, uint32_t sa, uint32_t sb, int q, auto n_c) __attribute__((always_inline)) {
+        const uint8_t *pa = smem + sa + a_lane, *pb = smem + sb;
         const uint32_t ch = (uint32_t)((2 * q + h) ^ swz<RB>(l32)) << 4;
 #pragma unroll
         for (int c = 0; c < G::SN; c++) {
-            if (TR) f.b[c] = read_t<BROW>(st + G::BM * RB + b_lane[c] + q * 16 * BROW);
-            else f.b[c] = *(const i32x4*)(st + G::BM * RB + b_lane[c] + ch);
+            if (TR) f.b[c] = read_t<BROW>(pb + b_lane[c] + q * 16 * BROW);
+            else f.b[c] = *(const i32x4*)(pb + b_lane[c] + ch);
         }
 #pragma unroll
-        for (int i = 0; i < decltype(n_c)::value; i++) f.a[i] = *(const i32x4*)(st + a_lane + i * G::WM * 32 * RB + ch);
+        for (int i = 0; i < decltype(n_c)::value; i++) f.a[i] = *(const i32x4*)(pa + i * G::WM * 32 * RB + ch);
     };
-    auto multiply = [&](const Frag& f, auto n_c) __attribute__((always_inline)) {
+    auto multiply = [&](const Frag& f, int from, int to) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < decltype(n_c)::value; i++)
+        for (int i = from; i < to; i++)
 #pragma unroll
             for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(f.a[i], f.b[c], acc[i][c]);
     };
-    auto k_loop = [&](auto n_c) __attribute__((always_inline)) {
-        constexpr int MACT = decltype(n_c)::value, TA = MACT * 32 * G::WM / CR, Q = RB / 32;
-        constexpr int few = (TA / W + CB) * (G::NS - 2), more = ((TA + W - 1) / W + CB) * (G::NS - 2);
-        using NA = Int<TA>;
-        static_assert(MACT * 32 * G::WM % CR == 0, "a sub-tile's copies are whole");
+    // n_c: sub-tiles of this wave; tall_c: of a tile of more than BM rows
+    auto k_loop = [&](auto n_c, auto tall_c) __attribute__((always_inline)) {
+        constexpr int MACT = decltype(n_c)::value, Q = RB / 32, NSA = G::NSA;
+        constexpr bool tall = decltype(tall_c)::value;
+        constexpr int NSB = tall ? NSA : G::NSB, a_slot = tall ? (G::BM + G::TX) * RB : G::a_slot;
+        constexpr int NCA = tall ? CA : (G::BM / CR + W - 1) / W;   // activation copies of a wave at most
+        static_assert(NSA == 2 && NSA * a_slot + NSB * G::b_slot <= G::lds, "");
+        auto slot_a = [&](int i) { return (uint32_t)(i * a_slot); };
+        auto slot_b = [&](int i) { return (uint32_t)(NSA * a_slot + i * G::b_slot); };
 #pragma unroll
         for (int i = 0; i < MACT; i++)
 #pragma unroll
             for (int c = 0; c < G::SN; c++) acc[i][c] = typename T::Acc{};
-        // stage s landed; of the copies only those of the NS - 2 stages after it may be in flight
+        // stage s landed; the weights of NSB - 2 stages after it may be in flight (its activations are the newest
+        // but for those)
         auto landed = [&](int s) __attribute__((always_inline)) {
-            if (s + G::NS - 2 >= nst) wait_vm<0>();
-            else if (few == more || wv < TA % W) wait_vm<more>();
-            else wait_vm<few>();
-            wait_stage_and_barrier<63>();
+            if (NSB == 2 || s + NSB - 2 >= nst) wait_stage_and_barrier<0>();
+            else wait_stage_and_barrier<(NSB - 2) * CB>();
         };
-        for (int s = 0; s < G::NS - 1 && s < nst; s++) issue(s, s, NA{});
-        landed(0);
-        if (G::NS - 1 < nst) issue(G::NS - 1, G::NS - 1, NA{});
-        Frag f0, f1;
-        read(f0, 0, 0, n_c);
-        int slot = 0;
-        // at the loop's head: step 0 of stage s in f0, stage s + NS - 1 on its way
-        for (int s = 0; s < nst; s++) {
+        // copies into the slots of stage s: stage s + NSA's activations, then stage s + NSB's weights
+        auto copies = [&](int s, int sa, int sb) __attribute__((always_inline)) {
+            if (s + NSA < nst) {
 #pragma unroll
-            for (int q = 0; q + 1 < Q; q++) {
-                read(q & 1 ? f0 : f1, slot, q + 1, n_c);
-                multiply(q & 1 ? f1 : f0, n_c);
+                for (int i = 0; i < NCA; i++) copy_a(i, s + NSA, slot_a(sa));
+            }
+            if (s + NSB < nst) {
+#pragma unroll
+                for (int i = 0; i < CB; i++) copy_b(i, s + NSB, slot_b(sb));
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < NSB - 1; s++) {   // weights of stages 0 .. NSB - 2, the last ones after stage 0's activations
+            if (s == NSB - NSA) {
+#pragma unroll
+                for (int i = 0; i < NCA; i++) copy_a(i, 0, slot_a(0));
+            }
+#pragma unroll
+            for (int i = 0; i < CB; i++)
+                if (s < nst) copy_b(i, s, slot_b(s));
+        }
+        landed(0);
+        Frag f0, f1;
+        read(f0, slot_a(0), slot_b(0), 0, n_c);
+        copies(-1, NSA - 1, NSB - 1);
+        int sa = 0, sb = 0;
+        auto step = [&](auto q_c, Frag& now, Frag& next) __attribute__((always_inline)) {
+            read(next, slot_a(sa), slot_b(sb), decltype(q_c)::value + 1, n_c);
+            __builtin_amdgcn_sched_barrier(0);   // or they sink behind the products and are waited for at once
+            multiply(now, 0, MACT);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // at the loop's head: step 0 of stage s in f0, the copies into the slots of stage s - 1 on their way
+        for (int s = 0; s < nst; s++) {
+            static_assert(Q == 4, "");
+            step(Int<0>{}, f0, f1);
+            step(Int<1>{}, f1, f0);
+            step(Int<2>{}, f0, f1);
+            const int pa = sa, pb = sb;
+            sa ^= 1;
+            sb = sb == NSB - 1 ? 0 : sb + 1;
+            if (s + 1 < nst) {
+                landed(s + 1);   // and every wave's reads of stage s are done
+                read(f0, slot_a(sa), slot_b(sb), 0, n_c);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            // this wave's reads of stage s are done, the other waves' too after the barrier
-            const int next = slot == G::NS - 1 ? 0 : slot + 1;
-            if (s + 1 < nst) {
-                landed(s + 1);
-                if (s + G::NS < nst) issue(s + G::NS, slot, NA{});
-                read(f0, next, 0, n_c);
-            }
-            slot = next;
-            multiply(f1, n_c);
+            // products before the copies: a wave issues in order, and the copies take a while
+            multiply(f1, 0, (MACT + 1) / 2);
+            __builtin_amdgcn_sched_barrier(0);
+            copies(s, pa, pb);
+            multiply(f1, (MACT + 1) / 2, MACT);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const int mact = (m_len + 32 * G::WM - 1) / (32 * G::WM);   // occupied sub-tiles (block-uniform)
-    if (G::SM >= 4 && mact >= 4) k_loop(Int<(G::SM >= 4 ? 4 : 1)>{});
-    else if (G::SM >= 3 && mact == 3) k_loop(Int<(G::SM >= 3 ? 3 : 1)>{});
-    else if (G::SM >= 2 && mact == 2) k_loop(Int<(G::SM >= 2 ? 2 : 1)>{});
-    else k_loop(Int<1>{});
+    const int mine = (subs + G::WM - 1 - wm) / G::WM;   // this wave's
+    using No = std::false_type;
+    if (G::TX && m_len > G::BM) {
+        if (mine > G::SM) k_loop(Int<G::MX>{}, std::integral_constant<bool, (G::TX > 0)>{});
+        else k_loop(Int<G::SM>{}, std::integral_constant<bool, (G::TX > 0)>{});
+    } else if (G::SM >= 4 && mine >= 4) k_loop(Int<(G::SM >= 4 ? 4 : 1)>{}, No{});
+    else if (G::SM >= 3 && mine == 3) k_loop(Int<(G::SM >= 3 ? 3 : 1)>{}, No{});
+    else if (G::SM >= 2 && mine == 2) k_loop(Int<(G::SM >= 2 ? 2 : 1)>{}, No{});
+    else if (G::WM == 1 || mine == 1) k_loop(Int<1>{}, No{});
+    else k_loop(Int<0>{}, No{});
 
     // ---- output rows (and what scales them) into the now idle ring
     int32_t* s_row = (int32_t*)smem;
-    float* s_scale = (float*)(smem + G::BM * 4);
+    float* s_scale = (float*)(smem + (G::BM + G::TX) * 4);
     __syncthreads();
-    for (int r = tid; r < G::BM; r += G::threads) {
+    for (int r = tid; r < G::BM + G::TX; r += G::threads) {
         const int j = m0 + min(r, m_len - 1);
         const int o = P.out_rows ? P.out_rows[j] : j;
         s_row[r] = o;
@@ -277,27 +325,57 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     }
     __syncthreads();
 
-    // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the sub-tile, column l % 32
+    // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the sub-tile, column l % 32. A tile's edges are told
+    // apart once: 128 stores a lane with their own conditions took as long as the products of 20 stages.
+    const int col = col0 + wn * G::SN * 32 + l32, col_left = cols - col;
+    const bool odd = lane & 1;
+    float ws[G::SN];
+    if constexpr (std::is_same<T, I8>::value) {
 #pragma unroll
-    for (int c = 0; c < G::SN; c++) {
-        const int col = col0 + (wn * G::SN + c) * 32 + l32;
-        if (col >= cols) continue;
-        float ws = 1.f;
-        if constexpr (std::is_same<T, I8>::value) ws = P.w_scale[(int64_t)e * P.N + col];
+        for (int c = 0; c < G::SN; c++) ws[c] = P.w_scale[(int64_t)e * P.N + min(col + 32 * c, cols - 1)];
+    }
+    auto put = [&](int i, auto rows_c, auto cols_c) __attribute__((always_inline)) {
+        constexpr bool all_rows = decltype(rows_c)::value, all_cols = decltype(cols_c)::value;
+        const int base = (i * G::WM + wm) * 32 + 4 * h;
 #pragma unroll
-        for (int i = 0; i < G::SM; i++) {
-            const int base = (i * G::WM + wm) * 32 + 4 * h;
-            if (base >= m_len) continue;
+        for (int g = 0; g < 4; g++) {
+            const i32x4 row = *(const i32x4*)(s_row + base + 8 * g);
+            f32x4 sc;
+            if (std::is_same<T, I8>::value || OUT16) sc = *(const f32x4*)(s_scale + base + 8 * g);
+            if constexpr (OUT16) {
 #pragma unroll
-            for (int v = 0; v < 16; v++) {
-                const int m = base + 8 * (v >> 2) + (v & 3);
-                if (m >= m_len) continue;
-                const int64_t o = (int64_t)s_row[m] * cols + col;
-                if constexpr (std::is_same<T, I8>::value) ((float*)P.out)[o] = (float)acc[i][c][v] * (s_scale[m] * ws);
-                else if (OUT16) ((Elem*)P.out)[o] = (Elem)(acc[i][c][v] * s_scale[m]);
-                else ((float*)P.out)[o] = acc[i][c][v];
+                for (int u = 0; u < 4; u += 2) {
+                    const bool in = all_rows || base + 8 * g + u + odd < m_len;
+                    Elem* o = (Elem*)P.out + (uint64_t)(uint32_t)(odd ? row[u + 1] : row[u]) * (uint32_t)cols + (col - odd);
+#pragma unroll
+                    for (int c = 0; c < G::SN; c++) {
+                        const uint32_t v = pair_up<Elem>(acc[i][c][4 * g + u] * sc[u], acc[i][c][4 * g + u + 1] * sc[u + 1], odd);
+                        if (in && (all_cols || 32 * c < col_left)) *(uint32_t*)(o + 32 * c) = v;   // columns are even
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; u++) {
+                    if (!all_rows && base + 8 * g + u >= m_len) continue;
+                    float* o = (float*)P.out + (uint64_t)(uint32_t)row[u] * (uint32_t)cols + col;
+#pragma unroll
+                    for (int c = 0; c < G::SN; c++) {
+                        float v;
+                        if constexpr (std::is_same<T, I8>::value) v = (float)acc[i][c][4 * g + u] * (sc[u] * ws[c]);
+                        else v = acc[i][c][4 * g + u];
+                        if (all_cols || 32 * c < col_left) o[32 * c] = v;
+                    }
+                }
             }
         }
+    };
+    const bool wide = col0 + G::BN <= cols;
+#pragma unroll
+    for (int i = 0; i < G::MX; i++) {
+        const int left = m_len - (i * G::WM + wm) * 32;
+        if (left <= 0) break;
+        if (left >= 32 && wide) put(i, std::true_type{}, std::true_type{});
+        else put(i, std::false_type{}, std::false_type{});
     }
 }
 
@@ -309,9 +387,10 @@ constexpr int kMapRows = 512;   // ring of positions whose rows are in LDS, refi
 template <class T, bool WEIGHTED, class G>
 __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     using Elem = typename T::Elem;
-    constexpr int W = G::waves, NS = G::NS;
+    constexpr int W = G::waves, NS = G::NSA;
+    static_assert(G::NSA == G::NSB, "one ring");
     constexpr int KS = G::RB / 2, Q = KS / 16, kHalf = kMapRows / 2 / KS;   // positions and MFMA steps of a stage; stages of half a map
-    static_assert(NS < kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
+    static_assert(NS + 1 < kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
     constexpr int AROW = G::BM * 2, BROW = G::BN * 2, ALR = AROW / 16, BLR = BROW / 16;
     constexpr int stage = KS * (AROW + BROW);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -347,22 +426,41 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     };
     constexpr int CA = KS * ALR / 64 / W, CB = KS * BLR / 64 / W;
     static_assert(CA * 64 * W == KS * ALR && CB * 64 * W == KS * BLR, "whole copies per wave");
-    auto issue = [&](int s, int slot) __attribute__((always_inline)) {
-        const uint32_t st = lds0 + (uint32_t)(slot * stage);
+    // Where a stage's copies read. Found a stage ahead of them: the rows come from the map in LDS, and a copy that
+    // waits for its address keeps the wave's products waiting.
+    const uint8_t *from_a[CA], *from_b[CB];
+    auto locate = [&](int s) __attribute__((always_inline)) {
+        int ra[CA], rb[CB];
+#pragma unroll
+        for (int i = 0; i < CA; i++) ra[i] = s_dy[(s * KS + (wv * CA + i) * (64 / ALR) + lane / ALR) & (kMapRows - 1)];
+#pragma unroll
+        for (int i = 0; i < CB; i++) rb[i] = s_x[(s * KS + (wv * CB + i) * (64 / BLR) + lane / BLR) & (kMapRows - 1)];
+        // all of them at once, and not behind the conditions below one by one
+#pragma unroll
+        for (int i = 0; i < CA; i++) asm volatile("" : "+v"(ra[i]));
+#pragma unroll
+        for (int i = 0; i < CB; i++) asm volatile("" : "+v"(rb[i]));
 #pragma unroll
         for (int i = 0; i < CA; i++) {
-            const int R = (wv * CA + i) * (64 / ALR) + lane / ALR, j = s * KS + R;
+            const int R = (wv * CA + i) * (64 / ALR) + lane / ALR;
             const int c = min(row0 + ((lane % ALR) ^ swz_t(R)) * 8, P.ldy - 8);
-            const uint8_t* p = (const uint8_t*)P.dY + ((int64_t)s_dy[j & (kMapRows - 1)] * P.ldy + c) * 2;
-            dma16v(j < len ? (const void*)p : zero, st + (wv * CA + i) * 1024);
+            const uint8_t* p = (const uint8_t*)P.dY + ((int64_t)ra[i] * P.ldy + c) * 2;
+            from_a[i] = s * KS + R < len ? p : (const uint8_t*)zero;
         }
 #pragma unroll
         for (int i = 0; i < CB; i++) {
-            const int R = (wv * CB + i) * (64 / BLR) + lane / BLR, j = s * KS + R;
+            const int R = (wv * CB + i) * (64 / BLR) + lane / BLR;
             const int c = min(col0 + ((lane % BLR) ^ swz_t(R)) * 8, P.K - 8);
-            const uint8_t* p = (const uint8_t*)P.X + ((int64_t)s_x[j & (kMapRows - 1)] * P.K + c) * 2;
-            dma16v(j < len ? (const void*)p : zero, st + KS * AROW + (wv * CB + i) * 1024);
+            const uint8_t* p = (const uint8_t*)P.X + ((int64_t)rb[i] * P.K + c) * 2;
+            from_b[i] = s * KS + R < len ? p : (const uint8_t*)zero;
         }
+    };
+    auto issue = [&](int slot) __attribute__((always_inline)) {
+        const uint32_t st = lds0 + (uint32_t)(slot * stage);
+#pragma unroll
+        for (int i = 0; i < CA; i++) dma16v(from_a[i], st + (wv * CA + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < CB; i++) dma16v(from_b[i], st + KS * AROW + (wv * CB + i) * 1024);
     };
 
     f32x16 acc[G::SM][G::SN];
@@ -399,9 +497,9 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
             }
         }
     };
-    auto multiply = [&](const Frag& f) __attribute__((always_inline)) {
+    auto multiply = [&](const Frag& f, int from = 0, int to = G::SM) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < G::SM; i++)
+        for (int i = from; i < to; i++)
 #pragma unroll
             for (int c = 0; c < G::SN; c++) acc[i][c] = T::mfma(f.a[i], f.b[c], acc[i][c]);
     };
@@ -415,68 +513,85 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
         map(0);
         if (len > kMapRows / 2) map(kMapRows / 2);
         wait_stage_and_barrier<0>();
-        for (int s = 0; s < NS - 1 && s < nst; s++) issue(s, s);
+        for (int s = 0; s < NS - 1 && s < nst; s++) {
+            locate(s);
+            issue(s);
+        }
+        locate(NS - 1);
         landed(0);
-        if (NS - 1 < nst) issue(NS - 1, NS - 1);
+        if (NS - 1 < nst) issue(NS - 1);
         Frag f0, f1;
         read(f0, 0, 0, 0);
         int slot = 0;
         for (int s = 0; s < nst; s++) {
-#pragma unroll
-            for (int q = 0; q + 1 < Q; q++) {
-                read(q & 1 ? f0 : f1, s, slot, q + 1);
-                multiply(q & 1 ? f1 : f0);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            const int next = slot == NS - 1 ? 0 : slot + 1;
+            static_assert(Q == 2, "");
+            read(f1, s, slot, 1);
+            locate(s + NS);   // past the end: of rows that are not copied
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(f0);
+            __builtin_amdgcn_sched_barrier(0);
+            const int was = slot;
+            slot = slot == NS - 1 ? 0 : slot + 1;
             if (s + 1 < nst) {
                 landed(s + 1);
-                if (s + NS < nst) {
-                    issue(s + NS, slot);
-                    // The half of the map that holds stage s and the kHalf - 1 before it has served, once s is its
-                    // last stage: the rows two halves on take its place, needed kHalf - NS + 1 stages from now.
-                    if ((s + 1) % kHalf == 0 && (s + 1 + kHalf) * KS < len) map((s + 1 + kHalf) * KS);
-                }
-                read(f0, s + 1, next, 0);
+                read(f0, s + 1, slot, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
-            slot = next;
-            multiply(f1);
+            multiply(f1, 0, G::SM / 2);
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + NS < nst) {
+                issue(was);
+                // The half of the map that holds stage s and the kHalf - 1 before it has served, once s is its
+                // last stage: the rows two halves on take its place, needed kHalf - NS stages from now.
+                if ((s + 1) % kHalf == 0 && (s + 1 + kHalf) * KS < len) map((s + 1 + kHalf) * KS);
+            }
+            multiply(f1, G::SM / 2, G::SM);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 
     // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the tile, column l % 32
+    const int row = row0 + wm * G::SM * 32 + 4 * h, col = col0 + wn * G::SN * 32 + l32;
+    const bool odd = lane & 1;
+    auto put = [&](auto all_c) __attribute__((always_inline)) {
+        constexpr bool all = decltype(all_c)::value;
+        const int row_left = P.N - row, col_left = P.K - col;
+        const int64_t first = ((int64_t)e * P.N + row) * P.K + col;
+        if (P.f32) {
+            float* o = (float*)P.dW + first;
 #pragma unroll
-    for (int c = 0; c < G::SN; c++) {
-        const int col = col0 + (wn * G::SN + c) * 32 + l32;
-        const bool in = col < P.K;
+            for (int i = 0; i < G::SM; i++)
 #pragma unroll
-        for (int i = 0; i < G::SM; i++) {
-            const int row = row0 + (wm * G::SM + i) * 32 + 4 * h;
+                for (int v = 0; v < 16; v++) {
+                    const int r = i * 32 + 8 * (v >> 2) + (v & 3);
+                    if (all || r < row_left) {
 #pragma unroll
-            for (int v = 0; v < 16; v += 2) {
-                const int r = row + 8 * (v >> 2) + (v & 3);
-                const int64_t o = ((int64_t)e * P.N + r) * P.K + col;
-                if (P.f32) {
-                    if (in && r < P.N) ((float*)P.dW)[o] = acc[i][c][v];
-                    if (in && r + 1 < P.N) ((float*)P.dW)[o + P.K] = acc[i][c][v + 1];
-                } else {
-                    // two columns a store: even lanes take row r of both, odd lanes row r + 1
-                    const bool odd = lane & 1;
-                    const float give = odd ? acc[i][c][v] : acc[i][c][v + 1];
-                    const float got = __shfl_xor(give, 1);
-                    typedef Elem Pair __attribute__((ext_vector_type(2)));
-                    const Pair pair = {(Elem)(odd ? got : acc[i][c][v]), (Elem)(odd ? acc[i][c][v + 1] : got)};
-                    if (in && r + odd < P.N) *(Pair*)((Elem*)P.dW + o + (odd ? P.K - 1 : 0)) = pair;
+                        for (int c = 0; c < G::SN; c++)
+                            if (all || 32 * c < col_left) o[(int64_t)r * P.K + 32 * c] = acc[i][c][v];
+                    }
                 }
-            }
+        } else {
+            Elem* o = (Elem*)P.dW + first + (odd ? P.K - 1 : 0);
+#pragma unroll
+            for (int i = 0; i < G::SM; i++)
+#pragma unroll
+                for (int v = 0; v < 16; v += 2) {
+                    const int r = i * 32 + 8 * (v >> 2) + (v & 3);
+#pragma unroll
+                    for (int c = 0; c < G::SN; c++) {
+                        const uint32_t w = pair_up<Elem>(acc[i][c][v], acc[i][c][v + 1], odd);
+                        if (all || (r + odd < row_left && 32 * c < col_left)) *(uint32_t*)(o + (int64_t)r * P.K + 32 * c) = w;
+                    }
+                }
         }
-    }
+    };
+    if (row0 + G::BM <= P.N && col0 + G::BN <= P.K) put(std::true_type{});
+    else put(std::false_type{});
 }
 
-using Wide = Tile<2, 4, 4, 2, 64, 5, 2>;      // 256 x 256, one block a CU
-using Narrow = Tile<1, 4, 2, 1, 128, 3, 2>;   // 64 x 128, two blocks a CU
-using GradW = Tile<1, 4, 4, 2, 64, 3, 2>;     // 128 x 256, two blocks a CU
+using Wide = Tile<2, 4, 4, 2, 128, 2, 3, 2, 64>;   // up to 320 x 256, one block a CU
+using Narrow = Tile<1, 4, 2, 1, 128, 2, 3, 2>;    // 64 x 128, two blocks a CU
+using GradW = Tile<1, 4, 4, 2, 64, 3, 3, 2>;      // 128 x 256, two blocks a CU
 
 template <class T, int TR, bool OUT16, class G>
 hipError_t launch(const ExpertGemm& a, hipStream_t st) {
@@ -503,6 +618,8 @@ hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
 }
 
 }  // namespace
+
+int expert_gemm_tile_x(int tile_m) { return tile_m == Wide::BM ? Wide::TX : Narrow::TX; }
 
 int expert_gemm_tile_m(double avg_rows) { return avg_rows > 64 ? Wide::BM : Narrow::BM; }
 

@@ -764,6 +764,7 @@ ExpertGemm elem_gemm(const moe_weights* w, const RowIdsPlan& r, int tile_m, int6
 void elem_tiles(RowIdsArgs& ra, const RowIdsPlan& r, int tile_m) {
     ra.tile_off[0] = r.tile_a;
     ra.tile_m[0] = tile_m;
+    ra.tile_x[0] = expert_gemm_tile_x(tile_m);
     ra.tile_tab[0] = r.tile_tab;
     ra.tile_cap[0] = r.tile_cap;
 }

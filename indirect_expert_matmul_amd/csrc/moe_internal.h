@@ -287,6 +287,7 @@ struct ExpertGemm {
     const float* row_w;        // out16: nullptr, or a factor for each row of out
 };
 int expert_gemm_tile_m(double avg_rows);
+int expert_gemm_tile_x(int tile_m);   // RowIdsArgs::tile_x
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad);   // blocks; at most 512 threads each
 hipError_t launch_expert_gemm(const ExpertGemm& a, hipStream_t st);
 hipError_t launch_expert_grad_x(const ExpertGemm& a, hipStream_t st);
