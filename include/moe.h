@@ -124,7 +124,9 @@ typedef struct {
  * reduce, where small batches (the distinct experts plus the shared ones fit two per
  * wave) do the reduce inside the down GEMV and time two kernels only.
  * moe_mul_mat_id GEMM path: row ids, grouped GEMM, fix-up/reduce; GEMV path: GEMV,
- * fix-up/reduce (weighted calls of small batches: the GEMV alone).
+ * fix-up/reduce (weighted calls of small batches: the GEMV alone; BF16 and F16 experts: always; I8
+ * experts: a quantize kernel before the GEMV for more than one token, and after the row ids of the GEMM
+ * path; the reduce only for single tokens with more than 64 KB of activations as int8).
  * moe_last_stage_count() tells how many kernels the last call timed. */
 typedef struct {
     int32_t path; /* 0 auto, 1 force grouped GEMM, 2 force GEMV (decode)        */
@@ -201,7 +203,10 @@ moe_status moe_gather_rows(const void *src1, moe_dtype src1_type, int64_t src1_r
  *              row[n] = d_row * d_w[n] * sum over the columns of q_row * q_w[n]
  *            with the sum exact in int32 (rows of src1 with an infinity or a NaN give NaN).
  *            BF16, F16 and I8: src1, w's data and the workspace 16-byte aligned
- *            (MOE_EINVAL), rows and cols < 2^30, opt->act_quant 0.
+ *            (MOE_EINVAL), rows and cols < 2^30, opt->act_quant 0. Their GEMV path: n_tokens *
+ *            n_used <= 64, I8 also cols <= 16384 (else forcing it is MOE_EINVAL); path 0 takes it
+ *            there while n_tokens * n_used <= 4 * n_experts; tau is not read. The two paths
+ *            add the same products in different orders.
  *   src1     device [n_tokens][B][K], B = src1_rows_per_token in {1, n_used}
  *   ids      device int32 [n_tokens][n_used]
  *   route_w  NULL: dst = float32 [n_tokens][n_used][N], dst[t][s] = W_{ids[t][s]} src1_row;
@@ -464,7 +469,7 @@ int32_t moe_select_path(int64_t n_tokens, int32_t n_used, int32_t n_experts, int
                         const moe_options *opt);
 
 /* The path moe_mul_mat_id / moe_ffn_fused take for experts of weight_type (MOE_Q8_0,
- * MOE_MXFP4, MOE_IQ4_NL or MOE_IQ4_XS) under opt: 1 grouped GEMM, 2 GEMV, 3 the grouped
+ * MOE_MXFP4, MOE_IQ4_NL or MOE_IQ4_XS; moe_mul_mat_id also MOE_BF16, MOE_F16, MOE_I8) under opt: 1 grouped GEMM, 2 GEMV, 3 the grouped
  * GEMM over quantized activations (opt->act_quant = 1, Q8_0 only), 4 the grouped GEMM or 5
  * the GEMV over MXFP4 activations (opt->act_quant = 2, MXFP4 only; act_width: the narrowest
  * row, shared experts apart), or a negative moe_status (MOE_EINVAL for other weight types,

@@ -390,7 +390,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     constexpr int W = G::waves, NS = G::NSA;
     static_assert(G::NSA == G::NSB, "one ring");
     constexpr int KS = G::RB / 2, Q = KS / 16, kHalf = kMapRows / 2 / KS;   // positions and MFMA steps of a stage; stages of half a map
-    static_assert(NS + 1 < kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
+    static_assert(NS + 1 <= kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
     constexpr int AROW = G::BM * 2, BROW = G::BN * 2, ALR = AROW / 16, BLR = BROW / 16;
     constexpr int stage = KS * (AROW + BROW);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -524,12 +524,20 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
         read(f0, 0, 0, 0);
         int slot = 0;
         for (int s = 0; s < nst; s++) {
-            static_assert(Q == 2, "");
-            read(f1, s, slot, 1);
-            locate(s + NS);   // past the end: of rows that are not copied
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(f0);
-            __builtin_amdgcn_sched_barrier(0);
+            auto step = [&](auto q_c, Frag& now, Frag& next) __attribute__((always_inline)) {
+                constexpr int q = decltype(q_c)::value;
+                read(next, s, slot, q + 1);
+                if (q == 0) locate(s + NS);   // past the end: of rows that are not copied
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(now);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            static_assert(Q == 2 || Q == 4, "");
+            step(Int<0>{}, f0, f1);
+            if constexpr (Q == 4) {
+                step(Int<1>{}, f1, f0);
+                step(Int<2>{}, f0, f1);
+            }
             const int was = slot;
             slot = slot == NS - 1 ? 0 : slot + 1;
             if (s + 1 < nst) {

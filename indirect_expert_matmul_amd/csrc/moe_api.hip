@@ -723,21 +723,41 @@ moe_status check_elem_options(const moe_options* o, int max_path, const char* wh
 }
 
 // 1 grouped GEMM, 2 GEMV, or a negative status.
-int elem_path(int64_t, int32_t, int32_t, int64_t, moe_dtype, const moe_options* o) {
-    const moe_status s = check_elem_options(o, 1, "mul_mat_id");
-    return s ? (int)s : 1;
+int elem_path(int64_t T, int32_t k, int32_t E, int64_t K, moe_dtype type, const moe_options* o) {
+    const moe_status s = check_elem_options(o, 2, "mul_mat_id");
+    if (s) return s;
+    const bool dec_ok = T * (int64_t)k <= kDecXSlots && (type != MOE_I8 || K <= kDecXMaxK);
+    const int32_t force = o ? o->path : 0;
+    if (force == 1) return 1;
+    if (force == 2) {
+        if (!dec_ok)
+            return fail(MOE_EINVAL, "GEMV path with BF16, F16 or I8 experts needs n_tokens*n_used <= %d, and I8 cols <= %d",
+                        kDecXSlots, kDecXMaxK);
+        return 2;
+    }
+    return dec_ok && T * (int64_t)k <= 4 * (int64_t)E ? 2 : 1;
 }
 
 struct ElemPlan {
+    bool fuse;    // the GEMV writes the weighted sum itself
     RowIdsPlan r;
     int tile_m;
     int8_t* q;    // I8: src1 codes and row scales
     float* d;
     float* y;     // weighted: per-slot rows
 };
-ElemPlan carve_elem(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted) {
+ElemPlan carve_elem(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int path) {
     ElemPlan p{};
     const int64_t n = T * k;
+    if (path == 2) {
+        p.fuse = weighted && decode_x_fuses(elem_of(w->type), T, B, w->cols);
+        if (w->type == MOE_I8 && !decode_x_makes(T)) {
+            p.q = (int8_t*)c.take((size_t)(T * B) * w->cols);
+            p.d = (float*)c.take((size_t)(T * B) * 4);
+        }
+        if (weighted && !p.fuse) p.y = (float*)c.take((size_t)n * w->rows * 4);
+        return p;
+    }
     p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     if (w->type == MOE_I8) {
@@ -812,14 +832,47 @@ moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src
     const bool weighted = route_w != nullptr;
     if ((s = check_aligned(src1, "src1"))) return s;
     Carve sz(nullptr);
-    carve_elem(sz, w, T, k, B, weighted);
+    carve_elem(sz, w, T, k, B, weighted, path);
     if (sz.off > ws_bytes || (sz.off && !ws)) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
     if ((s = check_aligned(ws, "the workspace"))) return s;
     Carve c(ws);
-    const ElemPlan p = carve_elem(c, w, T, k, B, weighted);
+    const ElemPlan p = carve_elem(c, w, T, k, B, weighted, path);
     Timer tm(opt, st);
     float* slot_out = weighted ? p.y : dst;
-    if ((s = mmid_elem(p, w, src1, src1_type, B, ids, T, k, slot_out, tm, st))) return s;
+    if (path == 2) {
+        DecXArgs a{};
+        a.type = elem_of(w->type);
+        a.W = w->data;
+        a.w_scale = (const float*)w->scales;
+        a.N = (int32_t)w->rows;
+        a.K = (int32_t)w->cols;
+        a.E = (int32_t)w->n_mat;
+        a.T = (int32_t)T;
+        a.k = k;
+        a.act_B = B;
+        a.ids = ids;
+        a.src = p.q ? (const void*)p.q : src1;
+        a.src_type = elem_of(src1_type);
+        a.src_scale = p.d;
+        a.out = slot_out;
+        a.route_w = route_w;
+        a.out_tok = p.fuse ? dst : nullptr;
+        if (p.q) {
+            const QuantRowsArgs q{src1, elem_of(src1_type), T * B, w->cols, p.q, p.d};
+            tm.begin();
+            if ((s = hip_check(launch_quant_rows(q, st), "quantize src1"))) return s;
+            tm.end();
+        }
+        tm.begin();
+        if ((s = hip_check(launch_decode_x(a, st), "GEMV"))) return s;
+        tm.end();
+        if (p.fuse || !weighted) {   // written in full, rows of invalid slots too
+            g_stages = tm.stage;
+            return MOE_OK;
+        }
+    } else if ((s = mmid_elem(p, w, src1, src1_type, B, ids, T, k, slot_out, tm, st))) {
+        return s;
+    }
     ReduceArgs rd{};
     rd.ids = ids;
     rd.route_w = route_w;
@@ -1349,9 +1402,10 @@ size_t moe_mul_mat_id_workspace_size(const moe_weights* w, moe_dtype src1_type,
                                      int32_t n_used, const moe_options* opt) {
     if (validate_mmid(w, src1_type, src1_rows_per_token, n_tokens, n_used)) return 0;
     if (is_elem(w->type)) {   // the weighted call's, which is the larger
-        if (elem_path(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt) < 0) return 0;
+        const int path = elem_path(n_tokens, n_used, (int32_t)w->n_mat, w->cols, w->type, opt);
+        if (path < 0) return 0;
         Carve c(nullptr);
-        carve_elem(c, w, n_tokens, n_used, src1_rows_per_token, true);
+        carve_elem(c, w, n_tokens, n_used, src1_rows_per_token, true, path);
         return c.off;
     }
     const bool q8 = w->type != MOE_F32;   // quantized experts

@@ -306,6 +306,30 @@ struct ExpertGradW {
 int64_t expert_grad_w_grid(const ExpertGradW& a);
 hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st);
 
+// GEMV (decode) path of those experts: T * k slots of at most kDecXSlots.
+constexpr int kDecXSlots = 64;
+constexpr int kDecXMaxK = 16384;           // int8: a single token's codes of a pass are in LDS
+constexpr int kDecXLds = 72 * 1024;
+struct DecXArgs {
+    ElemType type;            // of W
+    const void* W;            // [E][N][K]
+    const float* w_scale;     // int8: [E][N]
+    int32_t N, K, E, T, k, act_B;
+    const int32_t* ids;       // [T][k]
+    const void* src;          // [T][act_B][K] of W's type; int8 without src_scale: of src_type
+    ElemType src_type;
+    const float* src_scale;   // int8: nullptr, or a scale for each row of src
+    float* out;               // [T * k][N], or
+    const float* route_w;
+    float* out_tok;           // [T][N], the weighted sum
+    int32_t xs;               // set by the launcher
+};
+hipError_t launch_decode_x(const DecXArgs& a, hipStream_t st);
+// Whether a weighted call takes the sum itself.
+bool decode_x_fuses(ElemType type, int64_t T, int64_t B, int64_t K);
+// Whether int8 experts take activations as they are (else codes and scales).
+bool decode_x_makes(int64_t T);
+
 struct QuantRowsArgs {
     const void* src;    // [rows][K]
     ElemType src_type;  // f32, bf16 or f16

@@ -5,20 +5,17 @@
 // A pass of memory: one wave a row, 16 bytes a lane and load, the row held in registers between
 // its maximum and its codes (up to 16 loads; longer rows are read again, from the caches). Rows may
 // start anywhere and have any length: the loads need no alignment, and the last of a row ends with
-// it, so that some elements are done twice, with the same result. The quotient is x times the
-// reciprocal of d, at most 3 * 2^-24 of it off, that is 2.3e-5: where that could move it past a
-// half, which is one element in ten thousand, it is divided.
+// it, so that some elements are done twice, with the same result.
 // Measured (one MI355X): TODO
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "quant_rows.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256, kRows = kThreads / 64;
 constexpr int64_t kMaxGrid = 1 << 22;   // blocks take several rows past it
-constexpr float kMinFast = 1e-30f;      // scales whose reciprocal is a normal number
 
 template <int SRC>
 struct Src {
@@ -36,16 +33,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
     return v;
 }
-// The scale of a row whose largest magnitude has these bits.
-__device__ __forceinline__ float scale_of(uint32_t top) {
-    return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
-}
-__device__ __forceinline__ int code(float x, float d, float r, bool fast) {
-    float t = x * r;
-    float q = rintf(t);
-    if (!fast || fabsf(fabsf(t - q) - 0.5f) < 1e-4f) q = rintf(x / d);
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
-}
 template <int SRC>
 __device__ __forceinline__ void store(int8_t* o, const typename Src<SRC>::Vec& v, float d, float r, bool fast, bool some) {
     constexpr int EC = Src<SRC>::EC;
@@ -54,7 +41,7 @@ __device__ __forceinline__ void store(int8_t* o, const typename Src<SRC>::Vec& v
     for (int i = 0; i < EC / 4; i++) {
         w[i] = 0;
 #pragma unroll
-        for (int u = 0; u < 4; u++) w[i] |= ((uint32_t)code((float)v[4 * i + u], d, r, fast) & 255u) << (8 * u);
+        for (int u = 0; u < 4; u++) w[i] |= ((uint32_t)quant_code((float)v[4 * i + u], d, r, fast) & 255u) << (8 * u);
         if (!some) w[i] = 0;
     }
     __builtin_memcpy(o, w, EC);
@@ -85,8 +72,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a) {
 #pragma unroll
             for (int c = 0; c < CH; c++) grow(v[c]);
             top = wave_max(top);
-            const float d = scale_of(top), r = 1.0f / d;
-            const bool some = d > 0.f, fast = d > kMinFast;
+            const float d = quant_scale(top), r = 1.0f / d;
+            const bool some = d > 0.f, fast = d > kQuantMinFast;
 #pragma unroll
             for (int c = 0; c < CH; c++) {
                 const int at = (c * 64 + lane) * EC;
@@ -96,8 +83,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a) {
         } else {
             for (int64_t at = lane * EC; at < a.K; at += 64 * EC) grow(S::load(x + (at < last ? at : last)));
             top = wave_max(top);
-            const float d = scale_of(top), r = 1.0f / d;
-            const bool some = d > 0.f, fast = d > kMinFast;
+            const float d = quant_scale(top), r = 1.0f / d;
+            const bool some = d > 0.f, fast = d > kQuantMinFast;
             for (int64_t at = lane * EC; at < a.K; at += 64 * EC) {
                 const int64_t p = at < last ? at : last;
                 store<SRC>(q + p, S::load(x + p), d, r, fast, some);
@@ -115,8 +102,8 @@ __global__ __launch_bounds__(kThreads) void k_quant_short(QuantRowsArgs a) {
         const Elem* x = (const Elem*)a.src + row * a.K;
         uint32_t top = 0;
         for (int c = 0; c < a.K; c++) top = max(top, __float_as_uint((float)x[c]) & 0x7fffffffu);
-        const float d = scale_of(top);
-        for (int c = 0; c < a.K; c++) a.q[row * a.K + c] = d > 0.f ? (int8_t)code((float)x[c], d, 0.f, false) : 0;
+        const float d = quant_scale(top);
+        for (int c = 0; c < a.K; c++) a.q[row * a.K + c] = d > 0.f ? (int8_t)quant_code((float)x[c], d, 0.f, false) : 0;
         a.d[row] = d;
     }
 }

@@ -99,10 +99,24 @@ def test_product_validation():
     assert _mm(aq=1) == moe.MOE_EINVAL and "act_quant" in moe.last_error()
     assert _mm(_w(moe.MOE_I8), aq=2) == moe.MOE_EINVAL
     assert _mm(path=3) == moe.MOE_EINVAL
+    assert _mm(path=2) == moe.MOE_EINVAL and "GEMV" in moe.last_error()      # 128 slots
+    assert _mm(path=2, T=33) == moe.MOE_EINVAL
+    assert _mm(_w(moe.MOE_I8, cols=16400), path=2, T=1) == moe.MOE_EINVAL
     assert _mm(path=-1) == moe.MOE_EINVAL
     assert _mm(T=0) == moe.MOE_OK
     w = moe.c_moe_weights(moe.MOE_I8, FAKE, None, 8, 64, 128)
     assert _mm(w) == moe.MOE_EINVAL and "scales" in moe.last_error()
+
+
+def test_path_choice():
+    for typ in (moe.MOE_BF16, moe.MOE_F16, moe.MOE_I8):
+        assert moe.moe_select_path_typed(1, 4, 32, 2880, typ) == 2
+        assert moe.moe_select_path_typed(16, 4, 16, 2880, typ) == 2      # 64 slots, four an expert
+        assert moe.moe_select_path_typed(16, 4, 15, 2880, typ) == 1
+        assert moe.moe_select_path_typed(17, 4, 32, 2880, typ) == 1
+        assert moe.moe_select_path_typed(1, 4, 32, 2880, typ, path=1) == 1
+    assert moe.moe_select_path_typed(1, 4, 32, 16400, moe.MOE_I8) == 1
+    assert moe.moe_select_path_typed(1, 4, 32, 16400, moe.MOE_F16) == 2
 
 
 def test_fused_ffn_refuses_these_experts():

@@ -65,6 +65,47 @@ def test_product(T, E, k, N, K, per_slot, weighted, invalid, dtype):
     ref.within(out, y, tol, "product")
 
 
+# tokens, experts, picks, N, K, rows per token, weighted, invalid ids, ids repeat
+DECODE = [
+    (1, 4, 2, 1, 16, False, False, 0.0, False),
+    (1, 32, 4, 131, 2880, False, False, 0.0, False),
+    (1, 32, 4, 131, 2880, True, True, 0.0, False),
+    (8, 64, 6, 67, 1408, True, True, 0.1, False),
+    (8, 64, 6, 67, 1408, False, False, 0.3, False),
+    (16, 1, 4, 18, 528, False, True, 0.0, True),
+    (64, 3, 1, 18, 4112, False, False, 0.1, True),
+    (32, 2, 2, 5, 7184, True, True, 0.2, True),
+    (5, 1024, 12, 33, 512, False, True, 0.0, False),
+    (3, 7, 5, 21, 16384, False, True, 0.0, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, torch.int8])
+@pytest.mark.parametrize("T,E,k,N,K,per_slot,weighted,invalid,repeat", DECODE)
+def test_decode(T, E, k, N, K, per_slot, weighted, invalid, repeat, dtype):
+    """The GEMV path and the grouped GEMM on batches of few slots."""
+    g = torch.Generator().manual_seed(T + N)
+    ids = _ids(T, E, k, g, invalid=invalid, repeat=repeat)
+    w, x, rw = _data(E, N, K, ids, BF if dtype == torch.int8 else dtype, per_slot, 3000 + K)
+    if dtype == torch.int8:
+        q, d = ref.quantize_rows(w.view(E * N, K))
+        q, d = q.view(E, N, K), d.view(E, N)
+        W = moe.Weights(q.to(torch.int8).cuda(), d.cuda())
+        y, tol = ref.int8_product(q, d, *ref.quantize_rows(x), ids, E, per_slot)
+    else:
+        W = moe.Weights(w.cuda())
+        y, tol = ref.product(w.double(), x.double(), ids, E, per_slot)
+    if weighted:
+        y, tol = ref.weighted(y, tol, rw, T, k)
+    else:
+        y, tol = y.view(T, k, N), tol.view(T, k, N)
+    for path in (moe.PATH_GEMV, moe.PATH_GEMM):
+        out = torch.full(tuple(y.shape), float("nan"), device="cuda")
+        moe.moe_mul_mat_id(W, x.cuda(), ids.cuda(), route_w=rw.cuda() if weighted else None,
+                           src1_rows_per_token=k if per_slot else 1, path=path, out=out)
+        ref.within(out, y, tol, "path %d" % path)
+
+
 SEGMENTS = [0, 1, 31, 32, 33, 63, 64, 65, 0, 127, 128, 129, 255, 256, 257, 300, 511, 513, 2]
 
 
