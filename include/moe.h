@@ -125,8 +125,9 @@ typedef struct {
  * wave) do the reduce inside the down GEMV and time two kernels only.
  * moe_mul_mat_id GEMM path: row ids, grouped GEMM, fix-up/reduce; GEMV path: GEMV,
  * fix-up/reduce (weighted calls of small batches: the GEMV alone; BF16 and F16 experts: always; I8
- * experts: a quantize kernel before the GEMV for more than one token, and after the row ids of the GEMM
- * path; the reduce only for single tokens with more than 64 KB of activations as int8).
+ * experts: a quantize kernel before the GEMV for more than one token; the reduce only for single tokens
+ * with more than 64 KB of activations as int8. Their GEMM path has no fix-up kernel; I8: a quantize kernel
+ * after the row ids from 2^22 activations on).
  * moe_last_stage_count() tells how many kernels the last call timed. */
 typedef struct {
     int32_t path; /* 0 auto, 1 force grouped GEMM, 2 force GEMV (decode)        */
@@ -205,7 +206,7 @@ moe_status moe_gather_rows(const void *src1, moe_dtype src1_type, int64_t src1_r
  *            BF16, F16 and I8: src1, w's data and the workspace 16-byte aligned
  *            (MOE_EINVAL), rows and cols < 2^30, opt->act_quant 0. Their GEMV path: n_tokens *
  *            n_used <= 64, I8 also cols <= 16384 (else forcing it is MOE_EINVAL); path 0 takes it
- *            there while n_tokens * n_used <= 4 * n_experts; tau is not read. The two paths
+ *            there while n_tokens * n_used <= 4 * n_experts, or 12; tau is not read. The two paths
  *            add the same products in different orders.
  *   src1     device [n_tokens][B][K], B = src1_rows_per_token in {1, n_used}
  *   ids      device int32 [n_tokens][n_used]
@@ -240,7 +241,7 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
  * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
  * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids[, round d_dst][, rows of g]
- * [, join or zero rows][, route_w by position][, experts' gradient].
+ * [, join][, route_w by position][, experts' gradient].
  */
 moe_status moe_mul_mat_id_backward(const moe_weights *w, const void *src1, moe_dtype src1_type,
                                    int32_t src1_rows_per_token, const int32_t *ids,

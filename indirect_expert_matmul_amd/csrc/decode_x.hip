@@ -3,8 +3,10 @@
 // the activations of their slots.
 //
 //   * A wave takes kR rows of one distinct expert (found from ids by wave ballots), 16 bytes a lane
-//     and load: 1 KB in a row for each of kR rows, kAhead loads of each under way. Its lanes' sums meet
-//     in a tree of fixed order.
+//     and load: 1 KB in a row for each of kR rows, the next one asked for when one has been used. That
+//     keeps few registers, and so many waves, busy: two loads of a row under way took 160 registers instead
+//     of 130 (8 tokens, 6 of 64 experts of 2048 x 1408, weighted 46 us instead of 36), three 200. Its lanes'
+//     sums meet in a tree of fixed order.
 //   * Up to kP of the expert's slots are done at a time; more read the rows again, from the caches.
 //   * 16-bit elements are widened and summed by float32 FMAs (the instructions for pairs of them
 //     need not keep subnormals). int8: v_dot4_i32_i8 on the codes. A single token's are made by every
@@ -24,7 +26,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kR = 4;         // rows of a wave
 constexpr int kP = 4;         // slots of a pass at most
-constexpr int kAhead = 3;     // loads of a row under way
 constexpr int kRowWaves = 4;  // waves of a block that does not sum
 constexpr int kSumWaves = 8;  // of one that does, at most
 
@@ -141,17 +142,15 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_decode_x(DecXArgs a) {
     };
 
     const uint8_t* w[kR];
-    i32x4 wq[kAhead][kR];
+    i32x4 wq[kR];
     // what a lane would read past the row's end is a piece of its beginning, and counts as zero
     auto load = [&](int r, int c0) __attribute__((always_inline)) -> i32x4 {
         const int64_t at = c0 + lane * EC < K ? (int64_t)c0 * (I8 ? 1 : 2) : -(int64_t)lane * 16;
         return __builtin_nontemporal_load((const i32x4*)(w[r] + at));
     };
-    auto first_loads = [&]() __attribute__((always_inline)) {
+    auto loads = [&](int c0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int b = 0; b < kAhead; b++)
-#pragma unroll
-            for (int r = 0; r < kR; r++) wq[b][r] = load(r, b * STEP);
+        for (int r = 0; r < kR; r++) wq[r] = load(r, c0);
     };
     auto expert_of = [&](int u) -> int {
         uint64_t m = firsts;
@@ -166,7 +165,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_decode_x(DecXArgs a) {
     const int u0 = FUSE ? wv : unit;
     if (u0 < nd) {   // the first weights, before anything that takes time
         rows_of(expert_of(u0));
-        first_loads();
+        loads(0);
     }
     if (FUSE && MAKE) make(a.xs, [](int i) { return (int64_t)i; });   // all rows of activations
 
@@ -176,10 +175,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_decode_x(DecXArgs a) {
         const int64_t w0 = (int64_t)e * N;
         if (u != u0) {
             rows_of(e);
-            first_loads();
+            loads(0);
         }
         for (bool again = false; left; again = true) {
-            if (again) first_loads();
+            if (again) loads(0);
             int cnt = min(__popcll(left), kP);
             if (MAKE && !FUSE) cnt = min(cnt, a.xs);
             int slot[kP];
@@ -209,50 +208,41 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_decode_x(DecXArgs a) {
                 for (int p = 0; p < P; p++)
                     x[p] = MAKE ? (const uint8_t*)s_q + (size_t)(FUSE ? src_row(slot[p]) : min(p, cnt - 1)) * K
                                 : (const uint8_t*)a.src + src_row(slot[p]) * K * (I8 ? 1 : 2);
-                for (int c0 = 0; c0 < K; c0 += kAhead * STEP) {
+                for (int c = 0; c < K; c += STEP) {
+                    const bool in = c + lane * EC < K;
+                    i32x4 xv[P];
 #pragma unroll
-                    for (int b = 0; b < kAhead; b++) {
-                        const int c = c0 + b * STEP;
-                        if (c >= K) break;
-                        const bool in = c + lane * EC < K;
-                        i32x4 now[kR], xv[P];
+                    for (int p = 0; p < P; p++) xv[p] = *(const i32x4*)(x[p] + (int64_t)(in ? c + lane * EC : 0) * (I8 ? 1 : 2));
+                    if (c + STEP > K) {   // the row's end
 #pragma unroll
-                        for (int p = 0; p < P; p++) xv[p] = *(const i32x4*)(x[p] + (int64_t)(in ? c + lane * EC : 0) * (I8 ? 1 : 2));
+                        for (int r = 0; r < kR; r++)
+                            if (!in) wq[r] = i32x4{0, 0, 0, 0};
 #pragma unroll
-                        for (int r = 0; r < kR; r++) {
-                            now[r] = wq[b][r];
-                            if (c + kAhead * STEP < K) wq[b][r] = load(r, c + kAhead * STEP);
-                        }
-                        if (c + STEP > K) {   // the row's end
+                        for (int p = 0; p < P; p++)
+                            if (!in) xv[p] = i32x4{0, 0, 0, 0};
+                    }
+                    if constexpr (I8) {
+#pragma unroll
+                        for (int p = 0; p < P; p++)
 #pragma unroll
                             for (int r = 0; r < kR; r++)
-                                if (!in) now[r] = i32x4{0, 0, 0, 0};
 #pragma unroll
-                            for (int p = 0; p < P; p++)
-                                if (!in) xv[p] = i32x4{0, 0, 0, 0};
-                        }
-                        if constexpr (I8) {
+                                for (int i = 0; i < 4; i++) acc[p][r] = __builtin_amdgcn_sdot4(wq[r][i], xv[p][i], acc[p][r], false);
+                    } else {
+                        float wf[kR][8];
 #pragma unroll
-                            for (int p = 0; p < P; p++)
+                        for (int r = 0; r < kR; r++) widen<TYPE>(wq[r], wf[r]);
 #pragma unroll
-                                for (int r = 0; r < kR; r++)
+                        for (int p = 0; p < P; p++) {
+                            float xf[8];
+                            widen<TYPE>(xv[p], xf);
 #pragma unroll
-                                    for (int i = 0; i < 4; i++) acc[p][r] = __builtin_amdgcn_sdot4(now[r][i], xv[p][i], acc[p][r], false);
-                        } else {
-                            float wf[kR][8];
+                            for (int r = 0; r < kR; r++)
 #pragma unroll
-                            for (int r = 0; r < kR; r++) widen<TYPE>(now[r], wf[r]);
-#pragma unroll
-                            for (int p = 0; p < P; p++) {
-                                float xf[8];
-                                widen<TYPE>(xv[p], xf);
-#pragma unroll
-                                for (int r = 0; r < kR; r++)
-#pragma unroll
-                                    for (int i = 0; i < 8; i++) acc[p][r] = fmaf(wf[r][i], xf[i], acc[p][r]);
-                            }
+                                for (int i = 0; i < 8; i++) acc[p][r] = fmaf(wf[r][i], xf[i], acc[p][r]);
                         }
                     }
+                    if (c + STEP < K) loads(c + STEP);
                 }
             };
             if (cnt > 2) run(std::integral_constant<int, kP>{});

@@ -735,7 +735,12 @@ int elem_path(int64_t T, int32_t k, int32_t E, int64_t K, moe_dtype type, const 
                         kDecXSlots, kDecXMaxK);
         return 2;
     }
-    return dec_ok && T * (int64_t)k <= 4 * (int64_t)E ? 2 : 1;
+    // The GEMV up to four slots an expert on average, which is one of its passes, and always for a dozen slots
+    // (mul_mat_id, GEMV against GEMM in us per call on one MI355X, weight copies in turn, bf16: E32 k4 2880 x 2880
+    // T = 1 12.2 / 26.5, T = 16 82 / 104; E128 k8 2048 x 7168 T = 8 213 / 257; four slots an expert, E16 k1 2048 x 2048
+    // T = 64, 37.5 / 38.1, int8 27.3 / 25.6; eight, E8 k8 2880 x 2880 T = 8, 51.6 / 34.5; E1 4096 x 4096 T = 12
+    // 30.7 / 37.9, T = 16 39.9 / 38.1)
+    return dec_ok && (T * (int64_t)k <= 4 * (int64_t)E || T * (int64_t)k <= 12) ? 2 : 1;
 }
 
 struct ElemPlan {
@@ -793,9 +798,13 @@ moe_status check_grid(int64_t blocks, const char* what) {
     return MOE_OK;
 }
 
-// moe_mul_mat_id up to the per-slot rows (slot_out, those of invalid slots not written).
+// Activations (elements) that are quantized beside the row ids, where they save a launch; more go through the
+// quantizer's own kernel, which reads them once.
+constexpr int64_t kRowsBesideMax = 4 << 20;
+
+// moe_mul_mat_id up to the per-slot rows (slot_out; weighted: those of invalid slots are not written).
 moe_status mmid_elem(const ElemPlan& p, const moe_weights* w, const void* src1, moe_dtype src1_type, int32_t B,
-                     const int32_t* ids, int64_t T, int32_t k, float* slot_out, Timer& tm, hipStream_t st) {
+                     const int32_t* ids, int64_t T, int32_t k, float* slot_out, bool weighted, Timer& tm, hipStream_t st) {
     moe_status s;
     const int64_t n = T * k;
     RowIdsArgs ra = row_ids_args(ids, n, k, (int32_t)w->n_mat, B, p.r);
@@ -808,11 +817,15 @@ moe_status mmid_elem(const ElemPlan& p, const moe_weights* w, const void* src1, 
     g.out = slot_out;
     g.out_rows = p.r.ids_dst;
     if ((s = check_grid(expert_gemm_grid(g, 0), "mul_mat_id"))) return s;
+    const QuantRowsArgs q{src1, elem_of(src1_type), T * B, w->cols, p.q, p.d};
+    const bool apart = w->type == MOE_I8 && T * B * w->cols > kRowsBesideMax;
+    BesideRowIds beside{};
+    if (w->type == MOE_I8 && !apart) beside.rows = q;
+    if (!weighted) beside.zero = ZeroSlots{ids, slot_out, n, (int32_t)w->n_mat, (int32_t)w->rows};
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();
-    if (w->type == MOE_I8) {
-        const QuantRowsArgs q{src1, elem_of(src1_type), T * B, w->cols, p.q, p.d};
+    if (apart) {
         tm.begin();
         if ((s = hip_check(launch_quant_rows(q, st), "quantize src1"))) return s;
         tm.end();
@@ -870,8 +883,12 @@ moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src
             g_stages = tm.stage;
             return MOE_OK;
         }
-    } else if ((s = mmid_elem(p, w, src1, src1_type, B, ids, T, k, slot_out, tm, st))) {
-        return s;
+    } else {
+        if ((s = mmid_elem(p, w, src1, src1_type, B, ids, T, k, slot_out, weighted, tm, st))) return s;
+        if (!weighted) {
+            g_stages = tm.stage;
+            return MOE_OK;
+        }
     }
     ReduceArgs rd{};
     rd.ids = ids;
@@ -882,9 +899,8 @@ moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src
     rd.N = (int32_t)w->rows;
     rd.y = slot_out;
     rd.out = dst;
-    rd.mode = weighted ? 0 : 1;
     tm.begin();
-    if ((s = hip_check(launch_reduce(rd, st), weighted ? "reduce" : "zero invalid slots"))) return s;
+    if ((s = hip_check(launch_reduce(rd, st), "reduce"))) return s;
     tm.end();
     g_stages = tm.stage;
     return MOE_OK;
@@ -1683,8 +1699,10 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     if (rows_wanted && (s = check_grid(expert_gemm_grid(g, 1), "row gradients"))) return s;
     if (d_w && (s = check_grid(expert_grad_w_grid(gw), "experts' gradient"))) return s;
     Timer tm(opt, st);
+    BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
+    if (rows_wanted && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
     tm.begin();
-    if ((s = hip_check(launch_row_ids(ra, st, nullptr), "row ids"))) return s;
+    if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();
     if (!as_is && n > 0) {
         const CastRowsArgs ca{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n, w->rows, p.ld, p.dy};
@@ -1696,18 +1714,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         tm.begin();
         if ((s = hip_check(launch_expert_grad_x(g, st), "row gradients"))) return s;
         tm.end();
-        tm.begin();
-        if (p.direct) {   // 16-bit rows of K columns are rows of K / 2 words
-            ReduceArgs z{};
-            z.ids = ids;
-            z.T = (int32_t)T;
-            z.k = k;
-            z.E = E;
-            z.N = g.K / 2;
-            z.out = (float*)d_src1;
-            z.mode = 1;
-            if ((s = hip_check(launch_reduce(z, st), "zero invalid slots"))) return s;
-        } else {
+        if (!p.direct) {
             GradRowsArgs j{};
             j.type = g.type;
             j.g = p.g;
@@ -1720,9 +1727,10 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
             j.K = g.K;
             j.d_x = d_src1;
             j.d_route_w = d_route_w;
+            tm.begin();
             if ((s = hip_check(launch_grad_rows(j, st), "join the slots' gradients"))) return s;
+            tm.end();
         }
-        tm.end();
     }
     if (d_w) {
         if (p.pos_w && n > 0) {

@@ -218,11 +218,21 @@ struct ZeroSlots {
     int64_t n;   // 0: none
     int32_t E, N;
 };
+// Element types of the 16-bit and int8 experts' kernels.
+enum ElemType : int32_t { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2, kElemI8 = 3 };
+struct QuantRowsArgs {
+    const void* src;    // [rows][K]
+    ElemType src_type;  // f32, bf16 or f16
+    int64_t rows, K;
+    int8_t* q;          // [rows][K]
+    float* d;           // [rows]
+};
 // Work that the row-id pass's first launch does in thread blocks of its own behind its own ones.
 struct BesideRowIds {
-    QuantFp4Args quant;   // bf16
+    QuantFp4Args quant;   // bf16; rows 0: none
+    QuantRowsArgs rows;   // rows 0: none; K a multiple of 16
     ZeroSlots zero;
-    int32_t quant_blocks;   // set by the launcher
+    int32_t quant_blocks, rows_blocks;   // set by the launcher
 };
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
@@ -266,7 +276,6 @@ hipError_t launch_decode_fp4(const DecFp4Args& a, hipStream_t st);
 bool decode_fp4_fuses(int64_t n, int64_t E, int64_t S, int64_t K);
 
 // ---------------------------------------------------------------- 16-bit and int8 experts
-enum ElemType : int32_t { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2, kElemI8 = 3 };
 // Grouped product (depth K, N columns) or row gradient (depth N, K columns) over the routed segments.
 struct ExpertGemm {
     ElemType type;             // of W and A
@@ -330,13 +339,6 @@ bool decode_x_fuses(ElemType type, int64_t T, int64_t B, int64_t K);
 // Whether int8 experts take activations as they are (else codes and scales).
 bool decode_x_makes(int64_t T);
 
-struct QuantRowsArgs {
-    const void* src;    // [rows][K]
-    ElemType src_type;  // f32, bf16 or f16
-    int64_t rows, K;
-    int8_t* q;          // [rows][K]
-    float* d;           // [rows]
-};
 hipError_t launch_quant_rows(const QuantRowsArgs& a, hipStream_t st);
 // Rows of float32 (f32) or of the type itself -> rows of the type, ld elements (a multiple of 8), 0 past N.
 struct CastRowsArgs {

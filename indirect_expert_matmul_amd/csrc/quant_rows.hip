@@ -7,8 +7,6 @@
 // start anywhere and have any length: the loads need no alignment, and the last of a row ends with
 // it, so that some elements are done twice, with the same result.
 // Measured (one MI355X): TODO
-#include <type_traits>
-
 #include "quant_rows.h"
 
 namespace moe {
@@ -17,40 +15,10 @@ namespace {
 constexpr int kThreads = 256, kRows = kThreads / 64;
 constexpr int64_t kMaxGrid = 1 << 22;   // blocks take several rows past it
 
-template <int SRC>
-struct Src {
-    using Elem = std::conditional_t<SRC == kElemF32, float, std::conditional_t<SRC == kElemBf16, __bf16, _Float16>>;
-    static constexpr int EC = 16 / (int)sizeof(Elem);   // elements of a load
-    typedef Elem Vec __attribute__((ext_vector_type(EC)));
-    static __device__ __forceinline__ Vec load(const Elem* p) {
-        Vec v;
-        __builtin_memcpy(&v, p, 16);
-        return v;
-    }
-};
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-    for (int m = 32; m; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
-    return v;
-}
-template <int SRC>
-__device__ __forceinline__ void store(int8_t* o, const typename Src<SRC>::Vec& v, float d, float r, bool fast, bool some) {
-    constexpr int EC = Src<SRC>::EC;
-    uint32_t w[EC / 4];
-#pragma unroll
-    for (int i = 0; i < EC / 4; i++) {
-        w[i] = 0;
-#pragma unroll
-        for (int u = 0; u < 4; u++) w[i] |= ((uint32_t)quant_code((float)v[4 * i + u], d, r, fast) & 255u) << (8 * u);
-        if (!some) w[i] = 0;
-    }
-    __builtin_memcpy(o, w, EC);
-}
-
 // CH: loads a lane holds; 0: the row is read twice.
 template <int SRC, int CH>
 __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a) {
-    using S = Src<SRC>;
+    using S = QuantSrc<SRC>;
     constexpr int EC = S::EC;
     const int lane = threadIdx.x & 63;
     for (int64_t row = (int64_t)blockIdx.x * kRows + (threadIdx.x >> 6); row < a.rows; row += (int64_t)gridDim.x * kRows) {
@@ -71,25 +39,17 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a) {
             }
 #pragma unroll
             for (int c = 0; c < CH; c++) grow(v[c]);
-            top = wave_max(top);
+            top = quant_wave_max(top);
             const float d = quant_scale(top), r = 1.0f / d;
             const bool some = d > 0.f, fast = d > kQuantMinFast;
 #pragma unroll
             for (int c = 0; c < CH; c++) {
                 const int at = (c * 64 + lane) * EC;
-                if (at < a.K) store<SRC>(q + (at < last ? at : last), v[c], d, r, fast, some);
+                if (at < a.K) quant_store<SRC>(q + (at < last ? at : last), v[c], d, r, fast, some);
             }
             if (lane == 0) a.d[row] = d;
         } else {
-            for (int64_t at = lane * EC; at < a.K; at += 64 * EC) grow(S::load(x + (at < last ? at : last)));
-            top = wave_max(top);
-            const float d = quant_scale(top), r = 1.0f / d;
-            const bool some = d > 0.f, fast = d > kQuantMinFast;
-            for (int64_t at = lane * EC; at < a.K; at += 64 * EC) {
-                const int64_t p = at < last ? at : last;
-                store<SRC>(q + p, S::load(x + p), d, r, fast, some);
-            }
-            if (lane == 0) a.d[row] = d;
+            quant_row_twice<SRC>(a, row, lane);
         }
     }
 }
@@ -97,7 +57,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a) {
 // Rows shorter than a load.
 template <int SRC>
 __global__ __launch_bounds__(kThreads) void k_quant_short(QuantRowsArgs a) {
-    using Elem = typename Src<SRC>::Elem;
+    using Elem = typename QuantSrc<SRC>::Elem;
     for (int64_t row = (int64_t)blockIdx.x * kThreads + threadIdx.x; row < a.rows; row += (int64_t)gridDim.x * kThreads) {
         const Elem* x = (const Elem*)a.src + row * a.K;
         uint32_t top = 0;
@@ -112,8 +72,8 @@ template <int SRC>
 void launch(const QuantRowsArgs& a, hipStream_t st) {
     const auto grid = [](int64_t blocks) { return (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid); };
     const unsigned g = grid((a.rows + kRows - 1) / kRows);
-    const int64_t ch = (a.K + 64 * Src<SRC>::EC - 1) / (64 * Src<SRC>::EC);
-    if (a.K < Src<SRC>::EC) k_quant_short<SRC><<<grid((a.rows + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+    const int64_t ch = (a.K + 64 * QuantSrc<SRC>::EC - 1) / (64 * QuantSrc<SRC>::EC);
+    if (a.K < QuantSrc<SRC>::EC) k_quant_short<SRC><<<grid((a.rows + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
     else if (ch <= 1) k_quant_rows<SRC, 1><<<g, kThreads, 0, st>>>(a);
     else if (ch <= 2) k_quant_rows<SRC, 2><<<g, kThreads, 0, st>>>(a);
     else if (ch <= 4) k_quant_rows<SRC, 4><<<g, kThreads, 0, st>>>(a);

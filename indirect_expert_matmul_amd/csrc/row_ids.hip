@@ -31,6 +31,7 @@
 //     ballots: position = bucket start + chunk offset + wave offset + rank.
 #include "moe_internal.h"
 #include "quant_mxfp4.h"
+#include "quant_rows.h"
 #include "zero_slots.h"
 
 namespace moe {
@@ -290,9 +291,21 @@ constexpr int kSingleMaskBuckets = 512;
 // Thread block `block` behind the `own` row-id ones.
 template <int THREADS>
 __device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int own) {
-    const int block = (int)blockIdx.x - own;
-    if (block < b.quant_blocks) quantize_mxfp4_blocks<true, THREADS>(b.quant, block);
-    else zero_invalid_slots<THREADS>(b.zero, block - b.quant_blocks, gridDim.x - own - b.quant_blocks);
+    const int block = (int)blockIdx.x - own, rows_block = block - b.quant_blocks;
+    if (rows_block < 0) {
+        quantize_mxfp4_blocks<true, THREADS>(b.quant, block);
+    } else if (rows_block < b.rows_blocks) {
+        constexpr int kWavesBeside = THREADS / 64;
+        const int lane = threadIdx.x & 63;
+        for (int64_t r = (int64_t)rows_block * kWavesBeside + (threadIdx.x >> 6); r < b.rows.rows;
+             r += (int64_t)b.rows_blocks * kWavesBeside) {
+            if (b.rows.src_type == kElemF32) quant_row_twice<kElemF32>(b.rows, r, lane);
+            else if (b.rows.src_type == kElemBf16) quant_row_twice<kElemBf16>(b.rows, r, lane);
+            else quant_row_twice<kElemF16>(b.rows, r, lane);
+        }
+    } else {
+        zero_invalid_slots<THREADS>(b.zero, rows_block - b.rows_blocks, gridDim.x - own - b.quant_blocks - b.rows_blocks);
+    }
 }
 
 template <bool MASK, bool BESIDE>
@@ -657,10 +670,13 @@ void row_ids_carve_scratch(RowIdsArgs& a, void* scratch) {
 namespace {
 
 // Thread blocks of THREADS threads for the work beside the row ids.
+constexpr int64_t kRowsBlocks = 1 << 14;   // they take several rows past it
 template <int THREADS>
 unsigned beside_grid(BesideRowIds& b) {
     b.quant_blocks = (int32_t)quant_fp4_grid(b.quant, THREADS);
-    return (unsigned)(b.quant_blocks + zero_slots_grid(b.zero, THREADS));
+    const int64_t rows_blocks = (b.rows.rows * 64 + THREADS - 1) / THREADS;
+    b.rows_blocks = (int32_t)(rows_blocks < kRowsBlocks ? rows_blocks : kRowsBlocks);
+    return (unsigned)(b.quant_blocks + b.rows_blocks + zero_slots_grid(b.zero, THREADS));
 }
 
 template <bool MASK, bool BESIDE>

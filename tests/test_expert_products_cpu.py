@@ -114,6 +114,7 @@ def test_path_choice():
         assert moe.moe_select_path_typed(16, 4, 16, 2880, typ) == 2      # 64 slots, four an expert
         assert moe.moe_select_path_typed(16, 4, 15, 2880, typ) == 1
         assert moe.moe_select_path_typed(17, 4, 32, 2880, typ) == 1
+        assert moe.moe_select_path_typed(12, 1, 1, 2880, typ) == 2 and moe.moe_select_path_typed(13, 1, 1, 2880, typ) == 1
         assert moe.moe_select_path_typed(1, 4, 32, 2880, typ, path=1) == 1
     assert moe.moe_select_path_typed(1, 4, 32, 16400, moe.MOE_I8) == 1
     assert moe.moe_select_path_typed(1, 4, 32, 16400, moe.MOE_F16) == 2
