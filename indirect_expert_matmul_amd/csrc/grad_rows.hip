@@ -81,18 +81,43 @@ __global__ __launch_bounds__(kThreads) void k_grad_rows(GradRowsArgs a) {
     }
 }
 
-__global__ __launch_bounds__(kThreads) void k_pos_w(PosWArgs a) {
+// A wave a row at a time.
+template <class Elem>
+__global__ __launch_bounds__(kThreads) void k_scale_rows(ScaleRowsArgs a) {
+    typedef Elem Vec __attribute__((ext_vector_type(8)));
+    const int lane = threadIdx.x & 63;
     const int64_t n = a.bounds[a.E];
-    for (int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x; j < n; j += (int64_t)gridDim.x * kThreads)
-        a.pos_w[j] = a.route_w[a.slots[j]];
+    const bool whole = a.N % 8 == 0 && ((uintptr_t)a.src & 15) == 0;
+    for (int64_t j = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); j < n; j += (int64_t)gridDim.x * kWaves) {
+        const float w = a.route_w[a.slots[j]];
+        const int64_t from = (int64_t)a.tokens[j] * a.N;
+        Elem* o = (Elem*)a.dst + j * a.ld;
+        for (int64_t c = 8 * lane; c < a.ld; c += 512) {
+            Vec v;
+            if (whole && !a.f32) {
+                v = *(const Vec*)((const Elem*)a.src + from + c);
+#pragma unroll
+                for (int u = 0; u < 8; u++) v[u] = (Elem)(w * (float)v[u]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; u++) {
+                    const float x = c + u >= a.N ? 0.f : a.f32 ? ((const float*)a.src)[from + c + u] : (float)((const Elem*)a.src)[from + c + u];
+                    v[u] = c + u >= a.N ? (Elem)0.f : (Elem)(w * x);
+                }
+            }
+            *(Vec*)(o + c) = v;
+        }
+    }
 }
 
 }  // namespace
 
-hipError_t launch_pos_w(const PosWArgs& a, hipStream_t st) {
+hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st) {
     if (a.n <= 0) return hipSuccess;
-    const int64_t blocks = (a.n + kThreads - 1) / kThreads;
-    k_pos_w<<<(unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), kThreads, 0, st>>>(a);
+    const int64_t blocks = (a.n + kWaves - 1) / kWaves;
+    const unsigned grid = (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid);
+    if (a.type == kElemBf16) k_scale_rows<__bf16><<<grid, kThreads, 0, st>>>(a);
+    else k_scale_rows<_Float16><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -914,7 +914,7 @@ struct GradPlan {
     int64_t ld;     // row length of dY
     void* dy;       // d_dst in the experts' type, rows of ld (nullptr: d_dst itself)
     float* g;       // per-slot rows of g
-    float* pos_w;   // weighted d_w: route_w by position
+    void* scaled;   // weighted d_w: rows route_w * dY by position
 };
 // dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
 GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int want,
@@ -925,8 +925,8 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
     p.direct = B == k && !(want & kWantR);
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     p.ld = (w->rows + 7) / 8 * 8;
-    if (!dy_as_is) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
-    if (weighted && (want & kWantW)) p.pos_w = (float*)c.take((size_t)n * 4);
+    if (!dy_as_is && (!weighted || (want & (kWantX | kWantR)))) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
+    if (weighted && (want & kWantW)) p.scaled = c.take((size_t)n * p.ld * 2);
     if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
     return p;
 }
@@ -1686,13 +1686,12 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.N = g.N;
     gw.K = g.K;
     gw.E = E;
-    gw.dY = dy;
+    gw.dY = weighted ? p.scaled : dy;
     gw.ldy = (int32_t)p.ld;
     gw.X = src1;
-    gw.dy_rows = g.a_rows;
+    gw.dy_rows = weighted ? nullptr : g.a_rows;
     gw.x_rows = B == 1 ? p.r.ids_src1 : p.r.ids_dst;
     gw.bounds = p.r.bounds;
-    gw.pos_w = p.pos_w;
     gw.dW = d_w;
     gw.f32 = d_w_type == MOE_F32;
     const bool rows_wanted = (want & (kWantX | kWantR)) && n > 0;
@@ -1704,7 +1703,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();
-    if (!as_is && n > 0) {
+    if (!as_is && n > 0 && (rows_wanted || !weighted)) {
         const CastRowsArgs ca{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n, w->rows, p.ld, p.dy};
         tm.begin();
         if ((s = hip_check(launch_cast_rows(ca, st), "round d_dst"))) return s;
@@ -1733,10 +1732,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         }
     }
     if (d_w) {
-        if (p.pos_w && n > 0) {
-            const PosWArgs pw{route_w, p.r.ids_dst, p.r.bounds, n, E, p.pos_w};
+        if (weighted && n > 0) {
+            const ScaleRowsArgs sa{d_dst, d_dst_type == MOE_F32, g.type, n, w->rows, p.ld, route_w,
+                                   p.r.ids_dst, p.r.ids_src1, p.r.bounds, E, p.scaled};
             tm.begin();
-            if ((s = hip_check(launch_pos_w(pw, st), "route_w by position"))) return s;
+            if ((s = hip_check(launch_scale_rows(sa, st), "scale d_dst's rows"))) return s;
             tm.end();
         }
         tm.begin();

@@ -306,9 +306,8 @@ struct ExpertGradW {
     const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
     int32_t ldy;               // a multiple of 8
     const void* X;             // rows of K
-    const int32_t *dy_rows, *x_rows;   // of position j: rows of dY and X
+    const int32_t *dy_rows, *x_rows;   // of position j: rows of dY (nullptr: j) and X
     const int32_t* bounds;     // [E + 1]
-    const float* pos_w;        // nullptr, or a factor for each position's row of dY
     void* dW;                  // [E][N][K], float32 (f32) or the element type
     int32_t f32;
 };
@@ -349,15 +348,19 @@ struct CastRowsArgs {
     void* dst;
 };
 hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st);
-// pos_w[j] = route_w[slots[j]] of the positions below bounds[E]
-struct PosWArgs {
+// Rows in position order, scaled: dst[j] = route_w[slots[j]] * src[tokens[j]] for positions below bounds[E], from
+// float32 (f32) or the type, rounded to the type; ld elements a row (a multiple of 8), 0 past N.
+struct ScaleRowsArgs {
+    const void* src;    // [tokens][N]
+    int32_t f32;
+    ElemType type;
+    int64_t n, N, ld;
     const float* route_w;
-    const int32_t *slots, *bounds;
-    int64_t n;
+    const int32_t *slots, *tokens, *bounds;
     int32_t E;
-    float* pos_w;
+    void* dst;
 };
-hipError_t launch_pos_w(const PosWArgs& a, hipStream_t st);
+hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st);
 struct GradRowsArgs {
     ElemType type;
     const float* g;          // [rows * k][K]
