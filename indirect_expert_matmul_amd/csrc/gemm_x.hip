@@ -92,12 +92,17 @@ __device__ __forceinline__ float swap1(float v) {
 }
 // Two columns a store: of the values of rows r and r + 1 in columns c (even lanes) and c + 1 (odd lanes), even lanes
 // get row r of both columns, odd lanes row r + 1.
-template <class Elem>
-__device__ __forceinline__ uint32_t pair_up(float a, float b, bool odd) {
+struct Pair {
+    float lo, hi;
+};
+__device__ __forceinline__ Pair pair_up(float a, float b, bool odd) {
     const float got = swap1(odd ? a : b);
-    typedef Elem Pair __attribute__((ext_vector_type(2)));
-    const Pair p = {(Elem)(odd ? got : a), (Elem)(odd ? b : got)};
-    return __builtin_bit_cast(uint32_t, p);
+    return Pair{odd ? got : a, odd ? b : got};
+}
+template <class Elem>
+__device__ __forceinline__ uint32_t packed(Pair p) {
+    typedef Elem Two __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, Two{(Elem)p.lo, (Elem)p.hi});
 }
 
 // M tile and column tile of this block: tiles ordered by expert, chunk of M tiles, column tile,
@@ -337,6 +342,17 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     auto put = [&](int i, auto rows_c, auto cols_c) __attribute__((always_inline)) {
         constexpr bool all_rows = decltype(rows_c)::value, all_cols = decltype(cols_c)::value;
         const int base = (i * G::WM + wm) * 32 + 4 * h;
+        float dot[8];   // OUT16: of this lane's 8 rows with those of x, over its columns
+        uint32_t x[8][G::SN];
+        if (OUT16 && P.dots) {   // all loads before the first use
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int m = base + 4 * j - 2 * (j & 1) + odd;   // 8 (j / 2) + 2 (j % 2)
+                const Elem* from = (const Elem*)P.x + (uint64_t)(uint32_t)s_row[min(m, m_len - 1)] * (uint32_t)cols + (col - odd);
+#pragma unroll
+                for (int c = 0; c < G::SN; c++) x[j][c] = all_cols || 32 * c < col_left ? *(const uint32_t*)(from + 32 * c) : 0u;
+            }
+        }
 #pragma unroll
         for (int g = 0; g < 4; g++) {
             const i32x4 row = *(const i32x4*)(s_row + base + 8 * g);
@@ -346,12 +362,21 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
 #pragma unroll
                 for (int u = 0; u < 4; u += 2) {
                     const bool in = all_rows || base + 8 * g + u + odd < m_len;
-                    Elem* o = (Elem*)P.out + (uint64_t)(uint32_t)(odd ? row[u + 1] : row[u]) * (uint32_t)cols + (col - odd);
+                    const uint64_t from = (uint64_t)(uint32_t)(odd ? row[u + 1] : row[u]) * (uint32_t)cols + (col - odd);
+                    const float scale = odd ? sc[u + 1] : sc[u];
+                    float d = 0.f;
 #pragma unroll
                     for (int c = 0; c < G::SN; c++) {
-                        const uint32_t v = pair_up<Elem>(acc[i][c][4 * g + u] * sc[u], acc[i][c][4 * g + u + 1] * sc[u + 1], odd);
-                        if (in && (all_cols || 32 * c < col_left)) *(uint32_t*)(o + 32 * c) = v;   // columns are even
+                        const Pair v = pair_up(acc[i][c][4 * g + u], acc[i][c][4 * g + u + 1], odd);
+                        if (!(in && (all_cols || 32 * c < col_left))) continue;   // columns are even
+                        if (P.dots) {
+                            typedef Elem Two __attribute__((ext_vector_type(2)));
+                            const Two w = __builtin_bit_cast(Two, x[2 * g + u / 2][c]);
+                            d = fmaf(v.lo, (float)w[0], fmaf(v.hi, (float)w[1], d));
+                        }
+                        if (P.out) *(uint32_t*)((Elem*)P.out + from + 32 * c) = packed<Elem>(Pair{v.lo * scale, v.hi * scale});
                     }
+                    dot[2 * g + u / 2] = d;
                 }
             } else {
 #pragma unroll
@@ -367,6 +392,17 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
                     }
                 }
             }
+        }
+        if (OUT16 && P.dots) {   // the 16 lanes of one parity: halve the rows a lane holds, then add the last two lanes
+            const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+#pragma unroll
+            for (int j = 0; j < 4; j++) dot[j] = (b4 ? dot[j + 4] : dot[j]) + __shfl_xor(b4 ? dot[j] : dot[j + 4], 16);
+#pragma unroll
+            for (int j = 0; j < 2; j++) dot[j] = (b3 ? dot[j + 2] : dot[j]) + __shfl_xor(b3 ? dot[j] : dot[j + 2], 8);
+            dot[0] = (b2 ? dot[1] : dot[0]) + __shfl_xor(b2 ? dot[0] : dot[1], 4);
+            dot[0] += __shfl_xor(dot[0], 2);
+            const int m = base + 8 * (2 * b4 + b3) + 2 * b2 + odd;
+            if (!(lane & 2) && m < m_len) P.dots[(int64_t)s_row[m] * P.dot_parts + at.nt * G::WN + wn] = dot[0];
         }
     };
     const bool wide = col0 + G::BN <= cols;
@@ -592,7 +628,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
                     const int r = i * 32 + 8 * (v >> 2) + (v & 3);
 #pragma unroll
                     for (int c = 0; c < G::SN; c++) {
-                        const uint32_t w = pair_up<Elem>(acc[i][c][v], acc[i][c][v + 1], odd);
+                        const uint32_t w = packed<Elem>(pair_up(acc[i][c][v], acc[i][c][v + 1], odd));
                         if (all || (r + odd < row_left && 32 * c < col_left)) __builtin_nontemporal_store(w, (uint32_t*)(o + (int64_t)r * P.K + 32 * c));
                     }
                 }
@@ -639,6 +675,11 @@ int expert_gemm_tile_m(double avg_rows) { return avg_rows > 64 ? Wide::BM : Narr
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad) {
     const int64_t cols = grad ? a.K : a.N, bn = a.tile_m == Wide::BM ? Wide::BN : Narrow::BN;
     return ((int64_t)a.m_tiles_max * ((cols + bn - 1) / bn) + 7) / 8 * 8;
+}
+
+int expert_dot_parts(const ExpertGemm& a) {
+    const int bn = a.tile_m == Wide::BM ? Wide::BN : Narrow::BN, wn = a.tile_m == Wide::BM ? Wide::WN : Narrow::WN;
+    return (a.K + bn - 1) / bn * wn;
 }
 
 int64_t expert_grad_w_grid(const ExpertGradW& a) {

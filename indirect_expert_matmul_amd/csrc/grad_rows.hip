@@ -110,7 +110,30 @@ __global__ __launch_bounds__(kThreads) void k_scale_rows(ScaleRowsArgs a) {
     }
 }
 
+// 16 lanes a slot.
+__global__ __launch_bounds__(kThreads) void k_join_dots(JoinDotsArgs a) {
+    constexpr int kLanes = 16;
+    const int l = threadIdx.x % kLanes;
+    for (int64_t i = (int64_t)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes; i < a.n;
+         i += (int64_t)gridDim.x * (kThreads / kLanes)) {
+        const int32_t e = a.ids[i];
+        float d = 0.f;
+        if (e >= 0 && e < a.E)
+            for (int p = l; p < a.parts; p += kLanes) d += a.dots[i * a.parts + p];
+#pragma unroll
+        for (int m = kLanes / 2; m; m >>= 1) d += __shfl_xor(d, m);
+        if (l == 0) a.out[i] = d;
+    }
+}
+
 }  // namespace
+
+hipError_t launch_join_dots(const JoinDotsArgs& a, hipStream_t st) {
+    if (a.n <= 0) return hipSuccess;
+    const int64_t blocks = (a.n + kThreads / 16 - 1) / (kThreads / 16);
+    k_join_dots<<<(unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
 
 hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st) {
     if (a.n <= 0) return hipSuccess;

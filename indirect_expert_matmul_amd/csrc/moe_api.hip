@@ -913,7 +913,9 @@ struct GradPlan {
     bool direct;    // the row gradients go to d_src1 as they are
     int64_t ld;     // row length of dY
     void* dy;       // d_dst in the experts' type, rows of ld (nullptr: d_dst itself)
-    float* g;       // per-slot rows of g
+    float* g;       // per-slot rows of g (not direct)
+    float* dots;    // direct: parts of d_route_w
+    int dot_parts;
     void* scaled;   // weighted d_w: rows route_w * dY by position
 };
 // dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
@@ -922,12 +924,16 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
     GradPlan p{};
     const int64_t n = T * k;
     p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
-    p.direct = B == k && !(want & kWantR);
+    p.direct = B == k;   // a slot a row of d_src1
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     p.ld = (w->rows + 7) / 8 * 8;
     if (!dy_as_is && (!weighted || (want & (kWantX | kWantR)))) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
     if (weighted && (want & kWantW)) p.scaled = c.take((size_t)n * p.ld * 2);
     if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
+    if ((want & kWantR) && p.direct) {
+        p.dot_parts = expert_dot_parts(elem_gemm(w, p.r, p.tile_m, n));
+        p.dots = (float*)c.take((size_t)n * p.dot_parts * 4);
+    }
     return p;
 }
 moe_status validate_grad(const moe_weights* w, moe_dtype src1_type, moe_dtype d_dst_type, int32_t B, int64_t T,
@@ -1681,6 +1687,9 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     g.out = p.direct ? d_src1 : (void*)p.g;
     g.out_rows = p.r.ids_dst;
     g.row_w = p.direct ? route_w : nullptr;
+    g.dots = p.dots;
+    g.dot_parts = p.dot_parts;
+    g.x = src1;
     ExpertGradW gw{};
     gw.type = g.type;
     gw.N = g.N;
@@ -1699,7 +1708,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     if (d_w && (s = check_grid(expert_grad_w_grid(gw), "experts' gradient"))) return s;
     Timer tm(opt, st);
     BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
-    if (rows_wanted && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
+    if (d_src1 && n > 0 && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();
@@ -1713,6 +1722,12 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         tm.begin();
         if ((s = hip_check(launch_expert_grad_x(g, st), "row gradients"))) return s;
         tm.end();
+        if (p.dots) {
+            const JoinDotsArgs jd{p.dots, ids, n, p.dot_parts, E, d_route_w};
+            tm.begin();
+            if ((s = hip_check(launch_join_dots(jd, st), "join d_route_w"))) return s;
+            tm.end();
+        }
         if (!p.direct) {
             GradRowsArgs j{};
             j.type = g.type;
@@ -1720,8 +1735,8 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
             j.ids = ids;
             j.route_w = route_w;
             j.x = src1;
-            j.rows = T * B;
-            j.k = B == 1 ? k : 1;
+            j.rows = T;   // B = 1
+            j.k = k;
             j.E = E;
             j.K = g.K;
             j.d_x = d_src1;

@@ -294,7 +294,13 @@ struct ExpertGemm {
     int32_t out16;
     const int32_t* out_rows;   // row of out of position j
     const float* row_w;        // out16: nullptr, or a factor for each row of out
+    // out16: nullptr, or parts of the inner products of each unscaled row with that of x, [rows][dot_parts];
+    // out may be nullptr then
+    float* dots;
+    int32_t dot_parts;         // expert_dot_parts
+    const void* x;             // rows as those of out
 };
+int expert_dot_parts(const ExpertGemm& a);   // of N, K, tile_m
 int expert_gemm_tile_m(double avg_rows);
 int expert_gemm_tile_x(int tile_m);   // RowIdsArgs::tile_x
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad);   // blocks; at most 512 threads each
@@ -361,6 +367,15 @@ struct ScaleRowsArgs {
     void* dst;
 };
 hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st);
+// out[i] = the sum of dots[i][0 .. parts - 1] in a fixed order, 0 for ids outside [0, E)
+struct JoinDotsArgs {
+    const float* dots;
+    const int32_t* ids;
+    int64_t n;
+    int32_t parts, E;
+    float* out;
+};
+hipError_t launch_join_dots(const JoinDotsArgs& a, hipStream_t st);
 struct GradRowsArgs {
     ElemType type;
     const float* g;          // [rows * k][K]
