@@ -127,7 +127,7 @@ typedef struct {
  * fix-up/reduce (weighted calls of small batches: the GEMV alone; BF16 and F16 experts: always; I8
  * experts: a quantize kernel before the GEMV for more than one token; the reduce only for single tokens
  * with more than 64 KB of activations as int8. Their GEMM path has no fix-up kernel; I8: a quantize kernel
- * after the row ids from 2^22 activations on).
+ * after the row ids from 6 * 2^20 activations on).
  * moe_last_stage_count() tells how many kernels the last call timed. */
 typedef struct {
     int32_t path; /* 0 auto, 1 force grouped GEMM, 2 force GEMV (decode)        */

@@ -165,13 +165,15 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     const uint8_t* ap[CA];
     const int a_k = ((lane % CL) ^ swz<RB>(lane / CL + (CR == 8 ? 8 * (wv & 1) : 0))) * EC;   // of this lane's chunk
     static_assert(CR == 16 || W % 2 == 0, "a wave's copies differ in multiples of 16 rows");
+    auto find_rows = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < CA; i++) {
-        const int R = (i * W + wv) * CR + lane / CL;
-        const int j = m0 + min(R, m_len - 1);
-        const int64_t row = P.a_rows ? P.a_rows[j] : j;
-        ap[i] = (const uint8_t*)P.A + (row * P.lda + a_k) * (int64_t)sizeof(Elem);
-    }
+        for (int i = 0; i < CA; i++) {
+            const int R = (i * W + wv) * CR + lane / CL;
+            const int j = m0 + min(R, m_len - 1);
+            const int64_t row = P.a_rows ? P.a_rows[j] : j;
+            ap[i] = (const uint8_t*)P.A + (row * P.lda + a_k) * (int64_t)sizeof(Elem);
+        }
+    };
     constexpr int BROW = TR ? G::BN * 2 : RB;        // bytes of a row of the weight tile in LDS
     constexpr int BLR = BROW / 16;                   // lanes of a row
     const uint8_t* bp[CB];
@@ -264,16 +266,15 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
             }
         };
 #pragma unroll
-        for (int s = 0; s < NSB - 1; s++) {   // weights of stages 0 .. NSB - 2, the last ones after stage 0's activations
-            if (s == NSB - NSA) {
-#pragma unroll
-                for (int i = 0; i < NCA; i++) copy_a(i, 0, slot_a(0));
-            }
+        for (int s = 0; s < NSB - 1; s++) {   // weights before the row map has arrived
 #pragma unroll
             for (int i = 0; i < CB; i++)
                 if (s < nst) copy_b(i, s, slot_b(s));
         }
-        landed(0);
+        find_rows();
+#pragma unroll
+        for (int i = 0; i < NCA; i++) copy_a(i, 0, slot_a(0));
+        wait_stage_and_barrier<0>();
         Frag f0, f1;
         read(f0, slot_a(0), slot_b(0), 0, n_c);
         copies(-1, NSA - 1, NSB - 1);
