@@ -671,7 +671,14 @@ hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
 
 int expert_gemm_tile_x(int tile_m) { return tile_m == Wide::BM ? Wide::TX : Narrow::TX; }
 
-int expert_gemm_tile_m(double avg_rows) { return avg_rows > 64 ? Wide::BM : Narrow::BM; }
+// The wide tile from 48 rows an expert on, where there are blocks enough for it (mul_mat_id, wide against narrow in us
+// per call on one MI355X: E128 k8 2048 x 7168 T = 384 645 / 647, T = 768 665 / 724, T = 1536 713 / 914; E64 k4
+// 1408 x 2048 T = 512 98 / 100, T = 2048 117 / 135; E16 k4 2880 x 2880 T = 256, 192 blocks, 53 / 81; E8 k2 4096 x 4096
+// T = 512, 128 blocks, 78 / 73; E8 k2 1024 x 4096 T = 2048, 64 blocks, 110 / 59; E1 4096 x 4096 T = 256, 16, 105 / 41).
+int expert_gemm_tile_m(int64_t slots, int64_t E, int64_t cols) {
+    const int64_t rows = slots / E, blocks = E * ((rows + Wide::BM - 1) / Wide::BM) * ((cols + Wide::BN - 1) / Wide::BN);
+    return rows >= 48 && blocks >= 160 ? Wide::BM : Narrow::BM;
+}
 
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad) {
     const int64_t cols = grad ? a.K : a.N, bn = a.tile_m == Wide::BM ? Wide::BN : Narrow::BN;

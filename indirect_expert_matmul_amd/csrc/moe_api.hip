@@ -763,7 +763,7 @@ ElemPlan carve_elem(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
         if (weighted && !p.fuse) p.y = (float*)c.take((size_t)n * w->rows * 4);
         return p;
     }
-    p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
+    p.tile_m = expert_gemm_tile_m(n, w->n_mat, w->rows);
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     if (w->type == MOE_I8) {
         p.q = (int8_t*)c.take((size_t)(T * B) * w->cols);
@@ -923,7 +923,7 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
                     bool dy_as_is) {
     GradPlan p{};
     const int64_t n = T * k;
-    p.tile_m = expert_gemm_tile_m((double)n / (double)w->n_mat);
+    p.tile_m = expert_gemm_tile_m(n, w->n_mat, w->cols);
     p.direct = B == k;   // a slot a row of d_src1
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     p.ld = (w->rows + 7) / 8 * 8;

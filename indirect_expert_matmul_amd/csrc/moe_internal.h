@@ -301,7 +301,7 @@ struct ExpertGemm {
     const void* x;             // rows as those of out
 };
 int expert_dot_parts(const ExpertGemm& a);   // of N, K, tile_m
-int expert_gemm_tile_m(double avg_rows);
+int expert_gemm_tile_m(int64_t slots, int64_t E, int64_t cols);
 int expert_gemm_tile_x(int tile_m);   // RowIdsArgs::tile_x
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad);   // blocks; at most 512 threads each
 hipError_t launch_expert_gemm(const ExpertGemm& a, hipStream_t st);

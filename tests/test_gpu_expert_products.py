@@ -110,13 +110,13 @@ SEGMENTS = [0, 1, 31, 32, 33, 63, 64, 65, 0, 127, 128, 129, 255, 256, 257, 300, 
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-@pytest.mark.parametrize("few", [False, True])
-def test_product_segments(dtype, few):
-    """Segment lengths at the tiles' edges, each expert on its own; many empty experts give the small tiles."""
-    segments = SEGMENTS + ([0] * 300 if few else [])
-    ids = _ids(0, 0, 1, torch.Generator().manual_seed(3), segments=segments)
-    E = len(segments)
-    w, x, _ = _data(E, 72, 136, ids, dtype, False, 5)
+@pytest.mark.parametrize("N,K", [(72, 136), (2100, 136), (2050, 8), (2304, 72)])
+def test_product_segments(N, K, dtype):
+    """Segment lengths at the tiles' edges, each expert on its own, on the narrow tiles and (wide rows of output) the
+    wide ones, with one stage or a part of one too."""
+    ids = _ids(0, 0, 1, torch.Generator().manual_seed(3), segments=SEGMENTS)
+    E = len(SEGMENTS)
+    w, x, _ = _data(E, N, K, ids, dtype, False, 5)
     out = moe.moe_mul_mat_id(moe.Weights(w.cuda()), x.cuda(), ids.cuda())
     y, tol = ref.product(w.double(), x.double(), ids, E, False)
     ref.within(out[:, 0], y, tol, "segments")
@@ -144,10 +144,11 @@ def test_int8(T, E, k, N, K, per_slot, weighted, invalid, src):
     ref.within(out, y, tol, "int8")
 
 
-def test_int8_segments_and_extremes():
+@pytest.mark.parametrize("N", [72, 2100])
+def test_int8_segments_and_extremes(N):
     """Segment lengths at the tiles' edges; codes of -128 and 127 over the widest rows' partial stage."""
     ids = _ids(0, 0, 1, torch.Generator().manual_seed(4), segments=SEGMENTS)
-    E, N, K = len(SEGMENTS), 72, 272
+    E, K = len(SEGMENTS), 272
     g = torch.Generator().manual_seed(6)
     x = torch.randn((len(ids), K), generator=g)
     q = torch.randint(-128, 128, (E, N, K), generator=g, dtype=torch.int8)
@@ -210,12 +211,29 @@ def test_gradients(T, E, k, N, K, per_slot, weighted, invalid, dtype, dw):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
-def test_gradient_segments(dtype):
+@pytest.mark.parametrize("N,K", [(72, 40), (40, 2104), (9, 2056)])
+def test_gradient_segments(N, K, dtype):
+    """The row gradient on narrow and wide tiles (wide rows of src1); the experts' over more positions than its map holds."""
     ids = _ids(0, 0, 1, torch.Generator().manual_seed(8), segments=SEGMENTS + [1023, 1024, 1025])
     E = len(SEGMENTS) + 3
-    w, x, rw = _data(E, 72, 40, ids, dtype, False, 9)
-    dy = torch.randn((len(ids), 1, 72), generator=torch.Generator().manual_seed(10)).to(dtype)
+    w, x, rw = _data(E, N, K, ids, dtype, False, 9)
+    dy = torch.randn((len(ids), 1, N), generator=torch.Generator().manual_seed(10)).to(dtype)
     got = moe.moe_mul_mat_id_backward(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), dy.cuda(), d_w_dtype=F32)
     want = ref.grads(w.double(), x.double(), ids, dy.double(), None, False, dtype, F32)
     ref.within(got[0], *want[0], "d_src1")
     ref.within(got[1], *want[1], "d_w")
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gradients_of_wide_tiles(per_slot, weighted):
+    T, E, k, N, K = 900, 8, 2, 72, 5128
+    ids = _ids(T, E, k, torch.Generator().manual_seed(11), invalid=0.05)
+    w, x, rw = _data(E, N, K, ids, BF, per_slot, 12)
+    dy = torch.randn((T, N) if weighted else (T, k, N), generator=torch.Generator().manual_seed(13)).to(BF)
+    got = moe.moe_mul_mat_id_backward(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), dy.cuda(),
+                                      route_w=rw.cuda() if weighted else None, src1_rows_per_token=k if per_slot else 1)
+    want = ref.grads(w.double(), x.double(), ids, dy.double(), rw if weighted else None, per_slot, BF, BF)
+    for name, a, b in zip(("d_src1", "d_w", "d_route_w"), got, want):
+        if b is not None:
+            ref.within(a, b[0].view(a.shape), b[1].view(a.shape), name)

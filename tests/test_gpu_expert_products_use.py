@@ -21,7 +21,8 @@ def _free():
 def _same(a, b):
     assert a.shape == b.shape and a.dtype == b.dtype
     kind = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[a.element_size()]
-    assert torch.equal(a.contiguous().view(kind), b.contiguous().view(kind))
+    differ = (a.contiguous().view(kind) != b.contiguous().view(kind)).sum().item()
+    assert differ == 0, "%d of %d values differ" % (differ, a.numel())
 
 
 def _ids(T, E, k, invalid=0.0):
@@ -218,7 +219,7 @@ def _guarded(nbytes):
 
 
 @pytest.mark.parametrize("T,E,k,N,K,per_slot", [(3, 4, 2, 37, 48, False), (9, 5, 3, 40, 64, True), (400, 6, 2, 333, 272, False),
-                                                (700, 3, 2, 260, 528, True)])
+                                                (700, 3, 2, 260, 528, True), (600, 8, 2, 5000, 5136, True), (600, 8, 2, 5001, 5136, False)])
 def test_workspace_of_the_size_asked_for(T, E, k, N, K, per_slot):
     """Used workspaces of exactly the reported size, outputs in guarded buffers; ten identical runs."""
     torch.manual_seed(T)
@@ -418,9 +419,14 @@ def test_rows_past_32_bits(dtype):
             s = slice(at, at + n)
             part = moe.moe_mul_mat_id_backward(w, x[s], ids[s], d[s].contiguous(), route_w=rw[s].contiguous() if weighted else None,
                                                want=("src1", "route_w") if weighted else ("src1",))
-            for a, b in zip(got, part):
-                if a is not None:
-                    _same(a[s], b)
+            _same(got[0][s], part[0])
+            if weighted:
+                # d_route_w's sum of K products is split by the tiles of the call, which its size decides: two results
+                # are apart by at most twice K roundings of 2^-24 of the sum of their magnitudes (the rows of g from
+                # d_src1, whose rounding is 2^-8 of them)
+                g = part[0].double().abs() / rw[s].double()
+                tol = 2 * K * ref.U32 * (1 + 2.0 ** -7) * (g * x[s].double().abs()).sum(1, keepdim=True)
+                assert ((got[2][s].double() - part[2].double()).abs() <= tol).all()
     # the experts' gradients from rows past 32 bits: only the last tokens have an expert
     few = torch.full_like(ids, -1)
     few[T - n:] = ids[T - n:]
