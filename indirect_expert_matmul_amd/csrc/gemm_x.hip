@@ -442,7 +442,13 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     const int tt = (int)(blockIdx.x & 7) * per + (q - e * per);
     if (e >= P.E || tt >= n_nt * n_kt) return;
     const int row0 = tt / n_kt * G::BM, col0 = tt % n_kt * G::BN;
-    const int j0 = P.bounds[e], len = P.bounds[e + 1] - j0;
+    int j0 = P.bounds[e], len = P.bounds[e + 1] - j0;
+    if (P.splits > 1) {   // a part of the segment's stages, summed up by the pass that joins the parts
+        const int per = expert_split_len(len, P.splits), from = (int)blockIdx.y * per;
+        if (from >= len) return;
+        j0 += from;
+        len = min(len - from, per);
+    }
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, l16 = lane & 15, h = lane >> 5;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -607,8 +613,8 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
         constexpr bool all = decltype(all_c)::value;
         const int row_left = P.N - row, col_left = P.K - col;
         const int64_t first = ((int64_t)e * P.N + row) * P.K + col;
-        if (P.f32) {
-            float* o = (float*)P.dW + first;
+        if (P.f32 || P.splits > 1) {
+            float* o = (P.splits > 1 ? P.parts + (int64_t)blockIdx.y * P.E * P.N * P.K : (float*)P.dW) + first;
 #pragma unroll
             for (int i = 0; i < G::SM; i++)
 #pragma unroll
@@ -663,7 +669,8 @@ hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
     constexpr int lds = G::lds + kMapRows * 8;
     static PerDeviceOnce cap;
     if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G>, lds)) return e;
-    k_grad_w<T, G><<<(unsigned)expert_grad_w_grid(a), G::threads, lds, st>>>(a);
+    const dim3 grid((unsigned)expert_grad_w_grid(a), (unsigned)a.splits);
+    k_grad_w<T, G><<<grid, G::threads, lds, st>>>(a);
     return hipGetLastError();
 }
 
@@ -688,6 +695,18 @@ int64_t expert_gemm_grid(const ExpertGemm& a, int grad) {
 int expert_dot_parts(const ExpertGemm& a) {
     const int bn = a.tile_m == Wide::BM ? Wide::BN : Narrow::BN, wn = a.tile_m == Wide::BM ? Wide::WN : Narrow::WN;
     return (a.K + bn - 1) / bn * wn;
+}
+
+// Two blocks a CU, where that takes 32 stages of an expert's 32 positions or more off its longest row of products: the
+// parts and their join cost some 15 us (us per call, in parts against whole: E1 1024 x 1024, 32768 slots 135 / 586;
+// E8 278 x 128, 14905 slots with Zipf(1.1) ids 61 / 82; in two parts E8 1024 x 1024, 8192 slots 57 / 41, which is left
+// whole).
+int expert_grad_w_splits(int64_t slots, int64_t E, int64_t N, int64_t K) {
+    const int64_t blocks = E * ((N + GradW::BM - 1) / GradW::BM) * ((K + GradW::BN - 1) / GradW::BN);
+    const int64_t stages = slots / E / 32;
+    int64_t s = 512 / blocks;
+    s = s > 16 ? 16 : s;
+    return s > 1 && stages - stages / s >= 32 ? (int)s : 1;
 }
 
 int64_t expert_grad_w_grid(const ExpertGradW& a) {

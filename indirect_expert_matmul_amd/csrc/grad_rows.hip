@@ -126,7 +126,48 @@ __global__ __launch_bounds__(kThreads) void k_join_dots(JoinDotsArgs a) {
     }
 }
 
+// dW from the parts of its sums, ascending; eight neighbours a thread (an expert's elements are a multiple of 8).
+template <class Elem>
+__global__ __launch_bounds__(kThreads) void k_join_w(ExpertGradW a) {
+    const int64_t per = (int64_t)a.N * a.K, all = per * a.E;
+    for (int64_t i = 8 * ((int64_t)blockIdx.x * kThreads + threadIdx.x); i < all; i += 8 * (int64_t)gridDim.x * kThreads) {
+        const int e = (int)(i / per);
+        const int len = a.bounds[e + 1] - a.bounds[e];
+        f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+        if (len > 0) {
+            const int parts = (len - 1) / expert_split_len(len, a.splits) + 1;
+            for (int p = 0; p < parts; p++) {
+                const f32x4* v = (const f32x4*)(a.parts + p * all + i);
+                lo += v[0];
+                hi += v[1];
+            }
+        }
+        if (a.f32) {
+            f32x4* o = (f32x4*)((float*)a.dW + i);
+            o[0] = lo;
+            o[1] = hi;
+        } else {
+            typedef Elem Vec __attribute__((ext_vector_type(8)));
+            Vec v;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                v[u] = (Elem)lo[u];
+                v[4 + u] = (Elem)hi[u];
+            }
+            *(Vec*)((Elem*)a.dW + i) = v;
+        }
+    }
+}
+
 }  // namespace
+
+hipError_t launch_join_w(const ExpertGradW& a, hipStream_t st) {
+    const int64_t blocks = ((int64_t)a.E * a.N * a.K / 8 + kThreads - 1) / kThreads;
+    const unsigned grid = (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid);
+    if (a.type == kElemBf16) k_join_w<__bf16><<<grid, kThreads, 0, st>>>(a);
+    else k_join_w<_Float16><<<grid, kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
 
 hipError_t launch_join_dots(const JoinDotsArgs& a, hipStream_t st) {
     if (a.n <= 0) return hipSuccess;

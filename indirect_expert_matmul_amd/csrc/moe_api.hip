@@ -844,6 +844,7 @@ moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src
     if (path < 0) return (moe_status)path;
     const bool weighted = route_w != nullptr;
     if ((s = check_aligned(src1, "src1"))) return s;
+    if (weighted && (s = check_grid((w->rows + 1023) / 1024 * T, "the weighted sum"))) return s;
     Carve sz(nullptr);
     carve_elem(sz, w, T, k, B, weighted, path);
     if (sz.off > ws_bytes || (sz.off && !ws)) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
@@ -917,6 +918,8 @@ struct GradPlan {
     float* dots;    // direct: parts of d_route_w
     int dot_parts;
     void* scaled;   // weighted d_w: rows route_w * dY by position
+    int splits;     // of the positions of each expert, for d_w
+    float* parts;
 };
 // dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
 GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int want,
@@ -929,6 +932,8 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
     p.ld = (w->rows + 7) / 8 * 8;
     if (!dy_as_is && (!weighted || (want & (kWantX | kWantR)))) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
     if (weighted && (want & kWantW)) p.scaled = c.take((size_t)n * p.ld * 2);
+    p.splits = want & kWantW ? expert_grad_w_splits(n, w->n_mat, w->rows, w->cols) : 1;
+    if (p.splits > 1) p.parts = (float*)c.take((size_t)p.splits * w->n_mat * w->rows * w->cols * 4);
     if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
     if ((want & kWantR) && p.direct) {
         p.dot_parts = expert_dot_parts(elem_gemm(w, p.r, p.tile_m, n));
@@ -1666,6 +1671,9 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     if (T > 0 && (!src1 || !ids || !d_dst)) return fail(MOE_EINVAL, "NULL pointer argument");
     if ((s = check_aligned(src1, "src1")) || (s = check_aligned(d_src1, "d_src1")) || (s = check_aligned(d_w, "d_w")))
         return s;
+    if (T > 0 && ((d_src1 && (d_src1 == src1 || d_src1 == d_dst || d_src1 == d_w)) ||
+                  (d_w && (d_w == w->data || d_w == src1 || d_w == d_dst))))   // they are read again after the first writes
+        return fail(MOE_EINVAL, "d_src1 and d_w must not be one of the inputs or each other");
     const int32_t E = (int32_t)w->n_mat;
     const bool as_is = d_dst_type == w->type && w->rows % 8 == 0 && (uintptr_t)d_dst % 16 == 0;
     Carve sz(nullptr);
@@ -1703,9 +1711,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.bounds = p.r.bounds;
     gw.dW = d_w;
     gw.f32 = d_w_type == MOE_F32;
+    gw.splits = p.splits;
+    gw.parts = p.parts;
     const bool rows_wanted = (want & (kWantX | kWantR)) && n > 0;
     if (rows_wanted && (s = check_grid(expert_gemm_grid(g, 1), "row gradients"))) return s;
-    if (d_w && (s = check_grid(expert_grad_w_grid(gw), "experts' gradient"))) return s;
+    if (d_w && (s = check_grid(expert_grad_w_grid(gw) * p.splits, "experts' gradient"))) return s;
     Timer tm(opt, st);
     BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
     if (d_src1 && n > 0 && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
@@ -1757,6 +1767,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         tm.begin();
         if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
         tm.end();
+        if (p.splits > 1) {
+            tm.begin();
+            if ((s = hip_check(launch_join_w(gw, st), "join the experts' gradient"))) return s;
+            tm.end();
+        }
     }
     g_stages = tm.stage;
     return MOE_OK;

@@ -316,9 +316,15 @@ struct ExpertGradW {
     const int32_t* bounds;     // [E + 1]
     void* dW;                  // [E][N][K], float32 (f32) or the element type
     int32_t f32;
+    int32_t splits;            // expert_grad_w_splits: above 1, parts of the sums go to parts [splits][E][N][K] and
+    float* parts;              // launch_join_w makes dW of them
 };
-int64_t expert_grad_w_grid(const ExpertGradW& a);
+// Parts that the positions of each expert are cut into, and the length of a part (whole stages).
+int expert_grad_w_splits(int64_t slots, int64_t E, int64_t N, int64_t K);
+inline __host__ __device__ int expert_split_len(int len, int splits) { return ((len + splits - 1) / splits + 31) & ~31; }
+int64_t expert_grad_w_grid(const ExpertGradW& a);   // blocks, for each of the parts
 hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st);
+hipError_t launch_join_w(const ExpertGradW& a, hipStream_t st);
 
 // GEMV (decode) path of those experts: T * k slots of at most kDecXSlots.
 constexpr int kDecXSlots = 64;

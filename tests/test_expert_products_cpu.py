@@ -72,9 +72,9 @@ def _w(typ=moe.MOE_BF16, n_mat=8, rows=64, cols=128, data=FAKE, scales=FAKE):
     return moe.c_moe_weights(typ, data, scales if typ == moe.MOE_I8 else None, n_mat, rows, cols)
 
 
-def _mm(w=None, st=moe.MOE_BF16, path=0, aq=0, ws=1 << 40, x=FAKE, T=64, k=2, B=1, wsp=FAKE):
+def _mm(w=None, st=moe.MOE_BF16, path=0, aq=0, ws=1 << 40, x=FAKE, T=64, k=2, B=1, wsp=FAKE, rw=None):
     opt = moe._options(path, act_quant=aq)
-    return moe.lib.moe_mul_mat_id(ctypes.byref(w or _w()), x, st, B, FAKE, T, k, None, FAKE, ctypes.byref(opt), wsp,
+    return moe.lib.moe_mul_mat_id(ctypes.byref(w or _w()), x, st, B, FAKE, T, k, rw, FAKE, ctypes.byref(opt), wsp,
                                   ws, None)
 
 
@@ -104,6 +104,7 @@ def test_product_validation():
     assert _mm(_w(moe.MOE_I8, cols=16400), path=2, T=1) == moe.MOE_EINVAL
     assert _mm(path=-1) == moe.MOE_EINVAL
     assert _mm(T=0) == moe.MOE_OK
+    assert _mm(_w(rows=1 << 25), T=1000, rw=FAKE, ws=16) == moe.MOE_ELIMIT and "weighted sum" in moe.last_error()  # more blocks than a dispatch holds
     w = moe.c_moe_weights(moe.MOE_I8, FAKE, None, 8, 64, 128)
     assert _mm(w) == moe.MOE_EINVAL and "scales" in moe.last_error()
 
@@ -129,7 +130,7 @@ def test_fused_ffn_refuses_these_experts():
 
 
 def _bw(w=None, st=moe.MOE_BF16, dt=moe.MOE_BF16, path=0, aq=0, ws=1 << 40, x=FAKE, T=64, k=2, B=1, rw=None,
-        dx=FAKE, dw=FAKE, dwt=moe.MOE_BF16, dr=None, dy=FAKE, wsp=FAKE):
+        dx=2 * FAKE, dw=3 * FAKE, dwt=moe.MOE_BF16, dr=None, dy=4 * FAKE, wsp=FAKE):
     opt = moe._options(path, act_quant=aq)
     return moe.lib.moe_mul_mat_id_backward(ctypes.byref(w or _w()), x, st, B, FAKE, T, k, rw, dy, dt, dx, dw, dwt, dr,
                                            ctypes.byref(opt), wsp, ws, None)
@@ -149,8 +150,10 @@ def test_gradient_validation():
     assert _bw(path=2) == moe.MOE_EINVAL
     assert _bw(aq=1) == moe.MOE_EINVAL
     assert _bw(x=FAKE + 8) == moe.MOE_EINVAL
-    assert _bw(dx=FAKE + 8) == moe.MOE_EINVAL
-    assert _bw(dw=FAKE + 8) == moe.MOE_EINVAL
+    assert _bw(dx=2 * FAKE + 8) == moe.MOE_EINVAL
+    assert _bw(dw=3 * FAKE + 8) == moe.MOE_EINVAL
+    for same in (dict(dx=FAKE), dict(dx=4 * FAKE), dict(dw=FAKE), dict(dw=2 * FAKE), dict(dw=4 * FAKE)):
+        assert _bw(**same) == moe.MOE_EINVAL and "inputs" in moe.last_error()
     assert _bw(wsp=FAKE + 8) == moe.MOE_EINVAL
     assert _bw(dy=None) == moe.MOE_EINVAL
     assert _bw(_w(cols=100)) == moe.MOE_ELIMIT

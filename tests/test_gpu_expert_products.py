@@ -161,8 +161,29 @@ def test_int8_segments_and_extremes(N):
     ref.within(out[:, 0], y, tol, "int8 segments")
 
 
+@pytest.mark.parametrize("src", [BF, HF, F32])
+@pytest.mark.parametrize("T,k,N,K,per_slot,weighted", [(3000, 2, 40, 64, False, False), (2500, 2, 33, 80, True, True),
+                                                       (1500, 3, 24, 4256, False, True)])
+def test_int8_of_many_slots(T, k, N, K, per_slot, weighted, src):
+    """Codes made beside the row ids of several chunks, or (the last) by the quantizer's own launch."""
+    g = torch.Generator().manual_seed(T)
+    ids, E = _ids(T, 5, k, g, invalid=0.1), 5
+    x = torch.randn((T * (k if per_slot else 1), K), generator=g).to(src)
+    q = torch.randint(-127, 128, (E, N, K), generator=g, dtype=torch.int8)
+    d, rw = torch.rand((E, N), generator=g) * 1e-2, torch.rand((T, k), generator=g)
+    out = moe.moe_mul_mat_id(moe.Weights(q.cuda(), d.cuda()), x.cuda(), ids.cuda(), route_w=rw.cuda() if weighted else None,
+                             src1_rows_per_token=k if per_slot else 1)
+    y, tol = ref.int8_product(q, d, *ref.quantize_rows(x), ids, E, per_slot)
+    if weighted:
+        y, tol = ref.weighted(y, tol, rw, T, k)
+    else:
+        y, tol = y.view(T, k, N), tol.view(T, k, N)
+    ref.within(out, y, tol, "int8")
+
+
 @pytest.mark.parametrize("dtype", [F32, BF, HF])
-@pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (65, 64), (10, 333), (129, 512), (7, 2056), (5, 9000), (2, 40001)])
+@pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (300, 8), (70, 15), (65, 64), (33, 90), (1001, 120), (9, 121), (10, 333), (129, 512),
+                                    (7, 2056), (6, 5003), (4, 7001), (5, 9000), (3, 16380), (2, 40001)])
 def test_quantize_rows(rows, K, dtype):
     g = torch.Generator().manual_seed(rows + K)
     x = (torch.randn((rows, K), generator=g) * torch.exp(3 * torch.randn((rows, 1), generator=g))).to(dtype)
@@ -170,6 +191,20 @@ def test_quantize_rows(rows, K, dtype):
     rq, rd = ref.quantize_rows(x)
     assert torch.equal(d.cpu(), rd)
     assert torch.equal(q.cpu().float(), rq)
+
+
+@pytest.mark.parametrize("rows,K", [((1 << 30) + 300, 1), ((1 << 28) + 130, 9), ((1 << 24) + 9, 264), ((1 << 22) + 5, 2056)])
+def test_quantize_more_rows_than_a_grid(rows, K):
+    """Blocks that take several rows, each kernel's: zeros but for some rows, the first, the last and those between."""
+    at = torch.tensor([0, 1, 255, 256, (1 << 22) - 1, 1 << 22, rows - 260, rows - 2, rows - 1])
+    some = torch.randn((len(at), K), generator=torch.Generator().manual_seed(K)).to(BF)
+    x = torch.zeros((rows, K), dtype=BF, device="cuda")
+    x[at.cuda()] = some.cuda()
+    q, d = moe.moe_quantize_rows(x)
+    rq, rd = ref.quantize_rows(some)
+    assert torch.equal(q[at.cuda()].cpu(), rq.to(torch.int8)) and torch.equal(d[at.cuda()].cpu(), rd)
+    assert int((d != 0).sum()) == len(at)
+    assert int(q.view(-1)[:rows * K // 8 * 8].view(torch.int64).count_nonzero()) <= 2 * len(at) * (K // 8 + 1)
 
 
 def test_quantize_rows_edges():
@@ -237,3 +272,19 @@ def test_gradients_of_wide_tiles(per_slot, weighted):
     for name, a, b in zip(("d_src1", "d_w", "d_route_w"), got, want):
         if b is not None:
             ref.within(a, b[0].view(a.shape), b[1].view(a.shape), name)
+
+
+@pytest.mark.parametrize("dtype,dw", [(BF, BF), (HF, F32)])
+@pytest.mark.parametrize("segments", [[3001], [2500, 0, 1, 33, 4000, 64, 1025, 900]])
+def test_gradient_of_long_segments(segments, dtype, dw):
+    """Few experts of many positions: their sums in parts, some experts with fewer parts than others, or none."""
+    ids = _ids(0, 0, 1, torch.Generator().manual_seed(14), segments=segments)
+    E, N, K = len(segments), 75, 72
+    w, x, rw = _data(E, N, K, ids, dtype, False, 15)
+    dy = torch.randn((len(ids), N), generator=torch.Generator().manual_seed(16)).to(dtype)
+    for weighted in (False, True):
+        d = dy if weighted else dy[:, None].contiguous()
+        got = moe.moe_mul_mat_id_backward(moe.Weights(w.cuda()), x.cuda(), ids.cuda(), d.cuda(),
+                                          route_w=rw.cuda() if weighted else None, want=("w",), d_w_dtype=dw)[1]
+        ref.within(got, *ref.grads(w.double(), x.double(), ids, d.double(), rw if weighted else None, False, dtype, dw)[1],
+                   "d_w")
