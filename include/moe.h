@@ -240,8 +240,8 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  *   d_route_w    NULL, or device float32 [n_tokens][n_used] (written); needs route_w
  * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
  * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
- * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids[, round d_dst][, rows of g]
- * [, join][, scale d_dst's rows][, experts' gradient[, join]].
+ * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids (which also round and scale
+ * d_dst's rows)[, rows of g][, join][, experts' gradient[, join]].
  */
 moe_status moe_mul_mat_id_backward(const moe_weights *w, const void *src1, moe_dtype src1_type,
                                    int32_t src1_rows_per_token, const int32_t *ids,

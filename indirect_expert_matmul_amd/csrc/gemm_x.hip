@@ -463,7 +463,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
         for (int i = wv; i < kMapRows / 128; i += W) {
             const int p = from + 64 * i + lane;
             const bool in = p < len;
-            if (P.dy_rows) dma4v(in ? (const void*)(P.dy_rows + j0 + p) : zero, at + 256 * i);
+            dma4v(in ? (const void*)(P.dy_rows + j0 + p) : zero, at + 256 * i);
             dma4v(in ? (const void*)(P.x_rows + j0 + p) : zero, at + kMapRows * 4 + 256 * i);
         }
     };
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
 #pragma unroll
         for (int i = 0; i < CA; i++) {
             const int R = (wv * CA + i) * (64 / ALR) + lane / ALR;
-            row_a[i] = P.dy_rows ? s_dy[at + R] : j0 + s * KS + R;
+            row_a[i] = s_dy[at + R];
         }
 #pragma unroll
         for (int i = 0; i < CB; i++) row_b[i] = s_x[at + (wv * CB + i) * (64 / BLR) + lane / BLR];

@@ -1,5 +1,4 @@
-// What the gradients of mul_mat_id do besides the grouped products: the gradient rows of dst in the
-// element type, and the joining of the slots' gradient rows g:
+// What the gradients of mul_mat_id do after the grouped products, joining the slots' gradient rows g:
 //   d_src1[r] = sum over r's slots, ascending, of route_w * g   (float32, rounded once)
 //   d_route_w[i] = sum over the columns of g[i] * src1[r]
 #include "moe_internal.h"
@@ -10,23 +9,6 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int64_t kMaxGrid = 1 << 22;   // blocks take several rows past it
-
-template <class Elem>
-__global__ __launch_bounds__(kThreads) void k_cast_rows(CastRowsArgs a) {
-    typedef Elem Vec __attribute__((ext_vector_type(8)));
-    const int64_t chunks = a.ld / 8;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.rows * chunks; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = i / chunks, c = (i - row * chunks) * 8;
-        Vec v;
-#pragma unroll
-        for (int u = 0; u < 8; u++) {
-            if (c + u >= a.N) v[u] = (Elem)0.f;
-            else if (a.f32) v[u] = (Elem)((const float*)a.src)[row * a.N + c + u];
-            else v[u] = ((const Elem*)a.src)[row * a.N + c + u];
-        }
-        *(Vec*)((Elem*)a.dst + row * a.ld + c) = v;
-    }
-}
 
 // One block a row of d_src1 and its k slots; the dot products' parts of a wave are in LDS.
 template <class Elem>
@@ -78,35 +60,6 @@ __global__ __launch_bounds__(kThreads) void k_grad_rows(GradRowsArgs a) {
             }
         }
         __syncthreads();
-    }
-}
-
-// A wave a row at a time.
-template <class Elem>
-__global__ __launch_bounds__(kThreads) void k_scale_rows(ScaleRowsArgs a) {
-    typedef Elem Vec __attribute__((ext_vector_type(8)));
-    const int lane = threadIdx.x & 63;
-    const int64_t n = a.bounds[a.E];
-    const bool whole = a.N % 8 == 0 && ((uintptr_t)a.src & 15) == 0;
-    for (int64_t j = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6); j < n; j += (int64_t)gridDim.x * kWaves) {
-        const float w = a.route_w[a.slots[j]];
-        const int64_t from = (int64_t)a.tokens[j] * a.N;
-        Elem* o = (Elem*)a.dst + j * a.ld;
-        for (int64_t c = 8 * lane; c < a.ld; c += 512) {
-            Vec v;
-            if (whole && !a.f32) {
-                v = *(const Vec*)((const Elem*)a.src + from + c);
-#pragma unroll
-                for (int u = 0; u < 8; u++) v[u] = (Elem)(w * (float)v[u]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < 8; u++) {
-                    const float x = c + u >= a.N ? 0.f : a.f32 ? ((const float*)a.src)[from + c + u] : (float)((const Elem*)a.src)[from + c + u];
-                    v[u] = c + u >= a.N ? (Elem)0.f : (Elem)(w * x);
-                }
-            }
-            *(Vec*)(o + c) = v;
-        }
     }
 }
 
@@ -173,25 +126,6 @@ hipError_t launch_join_dots(const JoinDotsArgs& a, hipStream_t st) {
     if (a.n <= 0) return hipSuccess;
     const int64_t blocks = (a.n + kThreads / 16 - 1) / (kThreads / 16);
     k_join_dots<<<(unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid), kThreads, 0, st>>>(a);
-    return hipGetLastError();
-}
-
-hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st) {
-    if (a.n <= 0) return hipSuccess;
-    const int64_t blocks = (a.n + kWaves - 1) / kWaves;
-    const unsigned grid = (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid);
-    if (a.type == kElemBf16) k_scale_rows<__bf16><<<grid, kThreads, 0, st>>>(a);
-    else k_scale_rows<_Float16><<<grid, kThreads, 0, st>>>(a);
-    return hipGetLastError();
-}
-
-hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st) {
-    const int64_t n = a.rows * (a.ld / 8);
-    if (n <= 0) return hipSuccess;
-    const int64_t blocks = (n + kThreads - 1) / kThreads;
-    const unsigned grid = (unsigned)(blocks < kMaxGrid ? blocks : kMaxGrid);
-    if (a.type == kElemBf16) k_cast_rows<__bf16><<<grid, kThreads, 0, st>>>(a);
-    else k_cast_rows<_Float16><<<grid, kThreads, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -917,7 +917,7 @@ struct GradPlan {
     float* g;       // per-slot rows of g (not direct)
     float* dots;    // direct: parts of d_route_w
     int dot_parts;
-    void* scaled;   // weighted d_w: rows route_w * dY by position
+    void* scaled;   // weighted d_w: rows route_w * dY by slot
     int splits;     // of the positions of each expert, for d_w
     float* parts;
 };
@@ -1706,7 +1706,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.dY = weighted ? p.scaled : dy;
     gw.ldy = (int32_t)p.ld;
     gw.X = src1;
-    gw.dy_rows = weighted ? nullptr : g.a_rows;
+    gw.dy_rows = p.r.ids_dst;
     gw.x_rows = B == 1 ? p.r.ids_src1 : p.r.ids_dst;
     gw.bounds = p.r.bounds;
     gw.dW = d_w;
@@ -1719,15 +1719,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     Timer tm(opt, st);
     BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
     if (d_src1 && n > 0 && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
+    if ((p.dy || p.scaled) && n > 0) beside.grad = GradInArgs{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n,
+                                                              w->rows, p.ld, p.dy, route_w, k, p.scaled};
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();
-    if (!as_is && n > 0 && (rows_wanted || !weighted)) {
-        const CastRowsArgs ca{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n, w->rows, p.ld, p.dy};
-        tm.begin();
-        if ((s = hip_check(launch_cast_rows(ca, st), "round d_dst"))) return s;
-        tm.end();
-    }
     if (rows_wanted) {
         tm.begin();
         if ((s = hip_check(launch_expert_grad_x(g, st), "row gradients"))) return s;
@@ -1757,13 +1753,6 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         }
     }
     if (d_w) {
-        if (weighted && n > 0) {
-            const ScaleRowsArgs sa{d_dst, d_dst_type == MOE_F32, g.type, n, w->rows, p.ld, route_w,
-                                   p.r.ids_dst, p.r.ids_src1, p.r.bounds, E, p.scaled};
-            tm.begin();
-            if ((s = hip_check(launch_scale_rows(sa, st), "scale d_dst's rows"))) return s;
-            tm.end();
-        }
         tm.begin();
         if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
         tm.end();

@@ -227,12 +227,26 @@ struct QuantRowsArgs {
     int8_t* q;          // [rows][K]
     float* d;           // [rows]
 };
+// Rows of d_dst, float32 (f32) or of the type, as the gradients' products read them: rows of the type, ld elements (a
+// multiple of 8), 0 past N; and rounded once from the product, each slot's row times its factor:
+// scaled[row * k + s] = route_w[row * k + s] * src[row].
+struct GradInArgs {
+    const void* src;    // [rows][N]; rows 0: nothing
+    int32_t f32;
+    ElemType type;
+    int64_t rows, N, ld;
+    void* dst;          // or nullptr
+    const float* route_w;
+    int32_t k;
+    void* scaled;       // or nullptr
+};
 // Work that the row-id pass's first launch does in thread blocks of its own behind its own ones.
 struct BesideRowIds {
     QuantFp4Args quant;   // bf16; rows 0: none
     QuantRowsArgs rows;   // rows 0: none; K a multiple of 16
+    GradInArgs grad;      // rows 0: none
     ZeroSlots zero;
-    int32_t quant_blocks, rows_blocks;   // set by the launcher
+    int32_t quant_blocks, rows_blocks, grad_blocks;   // set by the launcher
 };
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4
@@ -312,7 +326,7 @@ struct ExpertGradW {
     const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
     int32_t ldy;               // a multiple of 8
     const void* X;             // rows of K
-    const int32_t *dy_rows, *x_rows;   // of position j: rows of dY (nullptr: j) and X
+    const int32_t *dy_rows, *x_rows;   // of position j: rows of dY and X
     const int32_t* bounds;     // [E + 1]
     void* dW;                  // [E][N][K], float32 (f32) or the element type
     int32_t f32;
@@ -351,28 +365,6 @@ bool decode_x_fuses(ElemType type, int64_t T, int64_t B, int64_t K);
 bool decode_x_makes(int64_t T);
 
 hipError_t launch_quant_rows(const QuantRowsArgs& a, hipStream_t st);
-// Rows of float32 (f32) or of the type itself -> rows of the type, ld elements (a multiple of 8), 0 past N.
-struct CastRowsArgs {
-    const void* src;    // [rows][N]
-    int32_t f32;
-    ElemType type;
-    int64_t rows, N, ld;
-    void* dst;
-};
-hipError_t launch_cast_rows(const CastRowsArgs& a, hipStream_t st);
-// Rows in position order, scaled: dst[j] = route_w[slots[j]] * src[tokens[j]] for positions below bounds[E], from
-// float32 (f32) or the type, rounded to the type; ld elements a row (a multiple of 8), 0 past N.
-struct ScaleRowsArgs {
-    const void* src;    // [tokens][N]
-    int32_t f32;
-    ElemType type;
-    int64_t n, N, ld;
-    const float* route_w;
-    const int32_t *slots, *tokens, *bounds;
-    int32_t E;
-    void* dst;
-};
-hipError_t launch_scale_rows(const ScaleRowsArgs& a, hipStream_t st);
 // out[i] = the sum of dots[i][0 .. parts - 1] in a fixed order, 0 for ids outside [0, E)
 struct JoinDotsArgs {
     const float* dots;

@@ -29,6 +29,7 @@
 //     The count pass already ranks every entry inside its (wave, bucket) group and
 //     stores that rank (16 bits) and each wave's counts, so the place pass needs no
 //     ballots: position = bucket start + chunk offset + wave offset + rank.
+#include "grad_rows.h"
 #include "moe_internal.h"
 #include "quant_mxfp4.h"
 #include "quant_rows.h"
@@ -303,8 +304,12 @@ __device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int own) {
             else if (b.rows.src_type == kElemBf16) quant_row_twice<kElemBf16>(b.rows, r, lane);
             else quant_row_twice<kElemF16>(b.rows, r, lane);
         }
+    } else if (rows_block < b.rows_blocks + b.grad_blocks) {
+        if (b.grad.type == kElemBf16) prepare_rows<__bf16, THREADS>(b.grad, rows_block - b.rows_blocks, b.grad_blocks);
+        else prepare_rows<_Float16, THREADS>(b.grad, rows_block - b.rows_blocks, b.grad_blocks);
     } else {
-        zero_invalid_slots<THREADS>(b.zero, rows_block - b.rows_blocks, gridDim.x - own - b.quant_blocks - b.rows_blocks);
+        const int before = b.quant_blocks + b.rows_blocks + b.grad_blocks;
+        zero_invalid_slots<THREADS>(b.zero, block - before, gridDim.x - own - before);
     }
 }
 
@@ -676,7 +681,9 @@ unsigned beside_grid(BesideRowIds& b) {
     b.quant_blocks = (int32_t)quant_fp4_grid(b.quant, THREADS);
     const int64_t rows_blocks = (b.rows.rows * 64 + THREADS - 1) / THREADS;
     b.rows_blocks = (int32_t)(rows_blocks < kRowsBlocks ? rows_blocks : kRowsBlocks);
-    return (unsigned)(b.quant_blocks + b.rows_blocks + zero_slots_grid(b.zero, THREADS));
+    const int64_t grad_blocks = (b.grad.rows * (b.grad.ld / 8) + THREADS - 1) / THREADS;
+    b.grad_blocks = (int32_t)(grad_blocks < kRowsBlocks ? grad_blocks : kRowsBlocks);
+    return (unsigned)(b.quant_blocks + b.rows_blocks + b.grad_blocks + zero_slots_grid(b.zero, THREADS));
 }
 
 template <bool MASK, bool BESIDE>
