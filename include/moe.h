@@ -241,7 +241,7 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
  * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
  * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids (which also round and scale
- * d_dst's rows)[, rows of g][, join][, experts' gradient[, join]].
+ * d_dst's rows)[, rows of g, for small segments with the experts' gradient][, join][, experts' gradient][, join].
  */
 moe_status moe_mul_mat_id_backward(const moe_weights *w, const void *src1, moe_dtype src1_type,
                                    int32_t src1_rows_per_token, const int32_t *ids,

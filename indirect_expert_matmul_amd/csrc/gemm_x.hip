@@ -111,8 +111,7 @@ struct Where {
     int e, m0, m_len, nt;
 };
 template <int BM, int TX>
-__device__ __forceinline__ bool find_tile(const ExpertGemm& P, int n_nt, Where& w) {
-    const int b = (int)blockIdx.x;
+__device__ __forceinline__ bool find_tile(const ExpertGemm& P, int b, int n_nt, Where& w) {
     const int total = P.tile_off[P.E] * n_nt;
     const int part = (total + 7) >> 3, q = b >> 3, t = (b & 7) * part + q;
     if (q >= part || t >= total) return false;
@@ -137,7 +136,7 @@ __device__ __forceinline__ bool find_tile(const ExpertGemm& P, int n_nt, Where& 
 // TR 0: the product (reduction along W's columns); 1: the row gradient (along its rows).
 // OUT16: rows of the element type, else float32.
 template <class T, int TR, bool OUT16, class G>
-__global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
+__device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
     using Elem = typename T::Elem;
     constexpr int RB = G::RB, W = G::waves;
     constexpr int KS = RB / (int)sizeof(Elem);    // reduction elements per stage
@@ -145,7 +144,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int cols = TR ? P.K : P.N, depth = TR ? P.N : P.K;
     Where at;
-    if (!find_tile<G::BM, G::TX>(P, (cols + G::BN - 1) / G::BN, at)) return;
+    if (!find_tile<G::BM, G::TX>(P, block, (cols + G::BN - 1) / G::BN, at)) return;
     const int e = at.e, m0 = at.m0, m_len = at.m_len, col0 = at.nt * G::BN;
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
@@ -416,6 +415,11 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
     }
 }
 
+template <class T, int TR, bool OUT16, class G>
+__global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
+    gemm_x<T, TR, OUT16, G>(P, (int)blockIdx.x);
+}
+
 // ---------------------------------------------------------------- expert gradient
 // dW_e tile of BM rows (n) x BN columns (k); the reduction runs along e's positions, KS a stage, both operands
 // read transposed. (Weighted calls bring rows of dY that are scaled and in position order: scaling them here, between
@@ -423,7 +427,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
 constexpr int kMapRows = 512;   // ring of positions whose rows are in LDS, refilled by halves
 
 template <class T, class G>
-__global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
+__device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part) {
     using Elem = typename T::Elem;
     constexpr int W = G::waves, NS = G::NSA;
     static_assert(G::NSA == G::NSB, "one ring");
@@ -438,13 +442,13 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     // every expert's tiles in eight equal parts, one to each XCD: experts are of very different lengths (an eighth of
     // all tiles each left the XCDs with the long ones working when the others were done: 64 experts of 1408 x 2048 with Zipf(1.1) ids 337 us, now 303)
     const int n_nt = (P.N + G::BM - 1) / G::BM, n_kt = (P.K + G::BN - 1) / G::BN;
-    const int per = (n_nt * n_kt + 7) >> 3, q = (int)(blockIdx.x >> 3), e = q / per;
-    const int tt = (int)(blockIdx.x & 7) * per + (q - e * per);
+    const int per = (n_nt * n_kt + 7) >> 3, q = block >> 3, e = q / per;
+    const int tt = (block & 7) * per + (q - e * per);
     if (e >= P.E || tt >= n_nt * n_kt) return;
     const int row0 = tt / n_kt * G::BM, col0 = tt % n_kt * G::BN;
     int j0 = P.bounds[e], len = P.bounds[e + 1] - j0;
     if (P.splits > 1) {   // a part of the segment's stages, summed up by the pass that joins the parts
-        const int per = expert_split_len(len, P.splits), from = (int)blockIdx.y * per;
+        const int per = expert_split_len(len, P.splits), from = part * per;
         if (from >= len) return;
         j0 += from;
         len = min(len - from, per);
@@ -614,7 +618,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
         const int row_left = P.N - row, col_left = P.K - col;
         const int64_t first = ((int64_t)e * P.N + row) * P.K + col;
         if (P.f32 || P.splits > 1) {
-            float* o = (P.splits > 1 ? P.parts + (int64_t)blockIdx.y * P.E * P.N * P.K : (float*)P.dW) + first;
+            float* o = (P.splits > 1 ? P.parts + (int64_t)part * P.E * P.N * P.K : (float*)P.dW) + first;
 #pragma unroll
             for (int i = 0; i < G::SM; i++)
 #pragma unroll
@@ -645,9 +649,25 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
     else put(std::false_type{});
 }
 
+template <class T, class G>
+__global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
+    grad_w<T, G>(P, (int)blockIdx.x, (int)blockIdx.y);
+}
+
 using Wide = Tile<2, 4, 4, 2, 128, 2, 3, 2, 64>;   // up to 320 x 256, one block a CU
 using Narrow = Tile<1, 4, 2, 1, 128, 2, 3, 2>;    // 64 x 128, two blocks a CU
 using GradW = Tile<1, 4, 4, 2, 64, 3, 3, 2>;      // 128 x 256, two blocks a CU
+
+// Both gradients in one launch, blocks of the experts' first: neither fills the chip when they are small (both gradients,
+// us per call in one launch against two: E8 k2 300 x 200, 30 tokens 20.0 / 22.8; E8 k2 512 x 512, 2000 tokens 29.0 / 36.6;
+// E32 k4 2880 x 2880, 100 tokens 226 / 238; E64 k6 1408 x 2048, 500 tokens 189 / 189).
+template <class T, bool OUT16>
+__global__ __launch_bounds__(GradW::threads, GradW::OCC) void k_grads(ExpertGradW w, ExpertGemm g, int w_grid) {
+    static_assert(GradW::threads == Narrow::threads && GradW::OCC == Narrow::OCC, "one launch");
+    const int block = (int)blockIdx.x, w_blocks = w_grid * w.splits;
+    if (block < w_blocks) grad_w<T, GradW>(w, block % w_grid, block / w_grid);
+    else gemm_x<T, 1, OUT16, Narrow>(g, block - w_blocks);
+}
 
 template <class T, int TR, bool OUT16, class G>
 hipError_t launch(const ExpertGemm& a, hipStream_t st) {
@@ -663,14 +683,25 @@ hipError_t launch_tile(const ExpertGemm& a, hipStream_t st) {
     return a.tile_m == Wide::BM ? launch<T, TR, OUT16, Wide>(a, st) : launch<T, TR, OUT16, Narrow>(a, st);
 }
 
+constexpr int kGradWLds = GradW::lds + kMapRows * 8;
+
+template <class T, bool OUT16>
+hipError_t launch_both(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st) {
+    constexpr int lds = kGradWLds > Narrow::lds ? kGradWLds : Narrow::lds;
+    static PerDeviceOnce cap;
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grads<T, OUT16>, lds)) return e;
+    const int64_t w_grid = expert_grad_w_grid(w), grid = w_grid * w.splits + expert_gemm_grid(a, 1);
+    k_grads<T, OUT16><<<(unsigned)grid, GradW::threads, lds, st>>>(w, a, (int)w_grid);
+    return hipGetLastError();
+}
+
 template <class T>
 hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
     using G = GradW;
-    constexpr int lds = G::lds + kMapRows * 8;
     static PerDeviceOnce cap;
-    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G>, lds)) return e;
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G>, kGradWLds)) return e;
     const dim3 grid((unsigned)expert_grad_w_grid(a), (unsigned)a.splits);
-    k_grad_w<T, G><<<grid, G::threads, lds, st>>>(a);
+    k_grad_w<T, G><<<grid, G::threads, kGradWLds, st>>>(a);
     return hipGetLastError();
 }
 
@@ -726,6 +757,12 @@ hipError_t launch_expert_grad_x(const ExpertGemm& a, hipStream_t st) {
     if (a.type == kElemBf16) return a.out16 ? launch_tile<Bf16, 1, true>(a, st) : launch_tile<Bf16, 1, false>(a, st);
     return a.out16 ? launch_tile<F16, 1, true>(a, st) : launch_tile<F16, 1, false>(a, st);
 }
+
+hipError_t launch_expert_grads(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st) {
+    if (a.type == kElemBf16) return a.out16 ? launch_both<Bf16, true>(a, w, st) : launch_both<Bf16, false>(a, w, st);
+    return a.out16 ? launch_both<F16, true>(a, w, st) : launch_both<F16, false>(a, w, st);
+}
+bool expert_grads_share(const ExpertGemm& a) { return a.tile_m == Narrow::BM; }
 
 hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st) {
     return a.type == kElemBf16 ? launch_w<Bf16>(a, st) : launch_w<F16>(a, st);

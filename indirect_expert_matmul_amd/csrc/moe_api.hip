@@ -1714,8 +1714,9 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.splits = p.splits;
     gw.parts = p.parts;
     const bool rows_wanted = (want & (kWantX | kWantR)) && n > 0;
-    if (rows_wanted && (s = check_grid(expert_gemm_grid(g, 1), "row gradients"))) return s;
-    if (d_w && (s = check_grid(expert_grad_w_grid(gw) * p.splits, "experts' gradient"))) return s;
+    const bool both = rows_wanted && d_w && expert_grads_share(g);
+    const int64_t x_grid = rows_wanted ? expert_gemm_grid(g, 1) : 0, w_grid = d_w ? expert_grad_w_grid(gw) * p.splits : 0;
+    if ((s = check_grid(both ? x_grid + w_grid : x_grid > w_grid ? x_grid : w_grid, "gradients"))) return s;
     Timer tm(opt, st);
     BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
     if (d_src1 && n > 0 && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
@@ -1726,7 +1727,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     tm.end();
     if (rows_wanted) {
         tm.begin();
-        if ((s = hip_check(launch_expert_grad_x(g, st), "row gradients"))) return s;
+        if ((s = hip_check(both ? launch_expert_grads(g, gw, st) : launch_expert_grad_x(g, st), "row gradients"))) return s;
         tm.end();
         if (p.dots) {
             const JoinDotsArgs jd{p.dots, ids, n, p.dot_parts, E, d_route_w};
@@ -1753,9 +1754,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
         }
     }
     if (d_w) {
-        tm.begin();
-        if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
-        tm.end();
+        if (!both) {
+            tm.begin();
+            if ((s = hip_check(launch_expert_grad_w(gw, st), "experts' gradient"))) return s;
+            tm.end();
+        }
         if (p.splits > 1) {
             tm.begin();
             if ((s = hip_check(launch_join_w(gw, st), "join the experts' gradient"))) return s;

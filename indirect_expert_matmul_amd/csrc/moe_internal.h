@@ -337,6 +337,9 @@ struct ExpertGradW {
 int expert_grad_w_splits(int64_t slots, int64_t E, int64_t N, int64_t K);
 inline __host__ __device__ int expert_split_len(int len, int splits) { return ((len + splits - 1) / splits + 31) & ~31; }
 int64_t expert_grad_w_grid(const ExpertGradW& a);   // blocks, for each of the parts
+// Both in one launch, where the row gradient has the narrow tile.
+hipError_t launch_expert_grads(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st);
+bool expert_grads_share(const ExpertGemm& a);
 hipError_t launch_expert_grad_w(const ExpertGradW& a, hipStream_t st);
 hipError_t launch_join_w(const ExpertGradW& a, hipStream_t st);
 
