@@ -616,37 +616,49 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
     auto put = [&](auto all_c) __attribute__((always_inline)) {
         constexpr bool all = decltype(all_c)::value;
         const int row_left = P.N - row, col_left = P.K - col;
-        const int64_t first = ((int64_t)e * P.N + row) * P.K + col;
-        if (P.f32 || P.splits > 1) {
-            float* o = (P.splits > 1 ? P.parts + (int64_t)part * P.E * P.N * P.K : (float*)P.dW) + first;
+        float* o = (P.splits > 1 ? P.parts + (int64_t)part * P.E * P.N * P.K : (float*)P.dW) + ((int64_t)e * P.N + row) * P.K + col;
 #pragma unroll
-            for (int i = 0; i < G::SM; i++)
+        for (int i = 0; i < G::SM; i++)
 #pragma unroll
-                for (int v = 0; v < 16; v++) {
-                    const int r = i * 32 + 8 * (v >> 2) + (v & 3);
-                    if (all || r < row_left) {
+            for (int v = 0; v < 16; v++) {
+                const int r = i * 32 + 8 * (v >> 2) + (v & 3);
+                if (all || r < row_left) {
 #pragma unroll
-                        for (int c = 0; c < G::SN; c++)
-                            if (all || 32 * c < col_left) __builtin_nontemporal_store(acc[i][c][v], o + (int64_t)r * P.K + 32 * c);
-                    }
+                    for (int c = 0; c < G::SN; c++)
+                        if (all || 32 * c < col_left) __builtin_nontemporal_store(acc[i][c][v], o + (int64_t)r * P.K + 32 * c);
                 }
-        } else {
-            Elem* o = (Elem*)P.dW + first + (odd ? P.K - 1 : 0);
-#pragma unroll
-            for (int i = 0; i < G::SM; i++)
-#pragma unroll
-                for (int v = 0; v < 16; v += 2) {
-                    const int r = i * 32 + 8 * (v >> 2) + (v & 3);
-#pragma unroll
-                    for (int c = 0; c < G::SN; c++) {
-                        const uint32_t w = packed<Elem>(pair_up(acc[i][c][v], acc[i][c][v + 1], odd));
-                        if (all || (r + odd < row_left && 32 * c < col_left)) __builtin_nontemporal_store(w, (uint32_t*)(o + (int64_t)r * P.K + 32 * c));
-                    }
-                }
-        }
+            }
     };
-    if (row0 + G::BM <= P.N && col0 + G::BN <= P.K) put(std::true_type{});
-    else put(std::false_type{});
+    if (P.f32 || P.splits > 1) {
+        if (row0 + G::BM <= P.N && col0 + G::BN <= P.K) put(std::true_type{});
+        else put(std::false_type{});
+        return;
+    }
+    // 16-bit rows go through the ring's LDS, to be stored as whole lines
+    static_assert(G::BM * BROW <= NS * stage, "the tile's rows");
+    uint8_t* tile = smem;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < G::SM; i++)
+#pragma unroll
+        for (int v = 0; v < 16; v += 2) {
+            const int r = wm * G::SM * 32 + 4 * h + i * 32 + 8 * (v >> 2) + (v & 3) + odd;
+#pragma unroll
+            for (int c = 0; c < G::SN; c++) {
+                const int piece = ((wn * G::SN + c) ^ (r & 7)) * 64;   // of 64 bytes, apart in neighbouring rows
+                *(uint32_t*)(tile + r * BROW + piece + (l32 >> 1) * 4) = packed<Elem>(pair_up(acc[i][c][v], acc[i][c][v + 1], odd));
+            }
+        }
+    __syncthreads();
+    constexpr int RL = BROW / 16;   // lanes of a row
+    const int col_out = col0 + tid % RL * 8;
+    Elem* o = (Elem*)P.dW + ((int64_t)e * P.N + row0) * P.K + col_out;
+#pragma unroll 4
+    for (int r = tid / RL; r < G::BM; r += G::threads / RL) {
+        const int at = ((tid % RL * 16) ^ ((r & 7) * 64));
+        const i32x4 v = *(const i32x4*)(tile + r * BROW + at);
+        if (row0 + r < P.N && col_out < P.K) __builtin_nontemporal_store(v, (i32x4*)(o + (int64_t)r * P.K));
+    }
 }
 
 template <class T, class G>
