@@ -439,13 +439,16 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
     int32_t* s_dy = (int32_t*)(smem + NS * stage);   // rows of dY and X of the positions
     int32_t* s_x = s_dy + kMapRows;
 
-    // every expert's tiles in eight equal parts, one to each XCD: experts are of very different lengths (an eighth of
-    // all tiles each left the XCDs with the long ones working when the others were done: 64 experts of 1408 x 2048 with Zipf(1.1) ids 337 us, now 303)
-    const int n_nt = (P.N + G::BM - 1) / G::BM, n_kt = (P.K + G::BN - 1) / G::BN;
-    const int per = (n_nt * n_kt + 7) >> 3, q = block >> 3, e = q / per;
-    const int tt = (block & 7) * per + (q - e * per);
-    if (e >= P.E || tt >= n_nt * n_kt) return;
-    const int row0 = tt / n_kt * G::BM, col0 = tt % n_kt * G::BN;
+    // every expert's tiles in eight parts, one to each XCD and another for the next expert: experts are of very
+    // different lengths (an eighth of all tiles each left the XCDs with the long ones working when the others were
+    // done: 64 experts of 1408 x 2048 with Zipf(1.1) ids 337 us against 303). A part is a rectangle, which reads fewer
+    // rows than a strip (24576 slots to float32, 64 experts of 1408 x 2048: 241 us by strips, now 228)
+    const int n_nt = (P.N + G::BM - 1) / G::BM, n_kt = (P.K + G::BN - 1) / G::BN, pn = 8 / P.pk;
+    const int per_k = (n_kt + P.pk - 1) / P.pk, per = (n_nt + pn - 1) / pn * per_k;
+    const int q = block >> 3, e = q / per, xcd = (block + e) & 7, xn = xcd / P.pk, xk = xcd % P.pk;
+    const int tn = xn * n_nt / pn + (q - e * per) / per_k, tk = xk * n_kt / P.pk + (q - e * per) % per_k;
+    if (e >= P.E || tn >= (xn + 1) * n_nt / pn || tk >= (xk + 1) * n_kt / P.pk) return;
+    const int row0 = tn * G::BM, col0 = tk * G::BN;
     int j0 = P.bounds[e], len = P.bounds[e + 1] - j0;
     if (P.splits > 1) {   // a part of the segment's stages, summed up by the pass that joins the parts
         const int per = expert_split_len(len, P.splits), from = part * per;
@@ -697,8 +700,21 @@ hipError_t launch_tile(const ExpertGemm& a, hipStream_t st) {
 
 constexpr int kGradWLds = GradW::lds + kMapRows * 8;
 
+// Parts of an expert's columns, of eight parts of its tiles, that read the fewest rows of dY and X.
+int grad_w_pk(int64_t N, int64_t K) {
+    const int64_t n = (N + GradW::BM - 1) / GradW::BM, k = (K + GradW::BN - 1) / GradW::BN;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int pk = 1; pk <= 8; pk *= 2) {
+        const int64_t pn = 8 / pk, read = (n + pn - 1) / pn * GradW::BM + (k + pk - 1) / pk * GradW::BN;
+        if (read < least) least = read, best = pk;
+    }
+    return best;
+}
+
 template <class T, bool OUT16>
-hipError_t launch_both(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st) {
+hipError_t launch_both(const ExpertGemm& a, ExpertGradW w, hipStream_t st) {
+    w.pk = grad_w_pk(w.N, w.K);
     constexpr int lds = kGradWLds > Narrow::lds ? kGradWLds : Narrow::lds;
     static PerDeviceOnce cap;
     if (const hipError_t e = set_lds_cap(cap, (const void*)k_grads<T, OUT16>, lds)) return e;
@@ -708,8 +724,9 @@ hipError_t launch_both(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st
 }
 
 template <class T>
-hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
+hipError_t launch_w(ExpertGradW a, hipStream_t st) {
     using G = GradW;
+    a.pk = grad_w_pk(a.N, a.K);
     static PerDeviceOnce cap;
     if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G>, kGradWLds)) return e;
     const dim3 grid((unsigned)expert_grad_w_grid(a), (unsigned)a.splits);
@@ -754,7 +771,8 @@ int expert_grad_w_splits(int64_t slots, int64_t E, int64_t N, int64_t K) {
 
 int64_t expert_grad_w_grid(const ExpertGradW& a) {
     const int64_t n = (a.N + GradW::BM - 1) / GradW::BM, k = (a.K + GradW::BN - 1) / GradW::BN;
-    return a.E * ((n * k + 7) / 8 * 8);
+    const int pk = grad_w_pk(a.N, a.K), pn = 8 / pk;
+    return 8ll * a.E * ((n + pn - 1) / pn) * ((k + pk - 1) / pk);
 }
 
 hipError_t launch_expert_gemm(const ExpertGemm& a, hipStream_t st) {

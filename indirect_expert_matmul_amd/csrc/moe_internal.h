@@ -326,6 +326,7 @@ struct ExpertGradW {
     const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
     int32_t ldy;               // a multiple of 8
     const void* X;             // rows of K
+    int32_t pk;                        // set by the launcher
     const int32_t *dy_rows, *x_rows;   // of position j: rows of dY and X
     const int32_t* bounds;     // [E + 1]
     void* dW;                  // [E][N][K], float32 (f32) or the element type
