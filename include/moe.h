@@ -324,7 +324,7 @@ moe_status moe_quantize_act(const void *x, moe_dtype x_type, int64_t rows, int64
  * q = 0 for a row of zeros, d = NaN and q = 0 for one with an infinity or a NaN. Value = d * q.
  *   x   device BF16, F16 or F32 [rows][K], any K > 0
  *   q   device int8 [rows][K] (written); d device float32 [rows] (written)
- * rows = 0 is a no-op. No workspace. Deterministic.
+ * The three must not overlap. rows = 0 is a no-op. No workspace. Deterministic.
  */
 moe_status moe_quantize_rows(const void *x, moe_dtype x_type, int64_t rows, int64_t K, int8_t *q,
                              float *d, void *stream);

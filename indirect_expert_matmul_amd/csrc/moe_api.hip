@@ -1671,7 +1671,7 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     if (T > 0 && (!src1 || !ids || !d_dst)) return fail(MOE_EINVAL, "NULL pointer argument");
     if ((s = check_aligned(src1, "src1")) || (s = check_aligned(d_src1, "d_src1")) || (s = check_aligned(d_w, "d_w")))
         return s;
-    if (T > 0 && ((d_src1 && (d_src1 == src1 || d_src1 == d_dst || d_src1 == d_w)) ||
+    if (T > 0 && ((d_src1 && (d_src1 == src1 || d_src1 == d_dst || d_src1 == d_w || d_src1 == w->data)) ||
                   (d_w && (d_w == w->data || d_w == src1 || d_w == d_dst))))   // they are read again after the first writes
         return fail(MOE_EINVAL, "d_src1 and d_w must not be one of the inputs or each other");
     const int32_t E = (int32_t)w->n_mat;
@@ -1779,6 +1779,7 @@ moe_status moe_quantize_rows(const void* x, moe_dtype x_type, int64_t rows, int6
     if (!x || !q || !d) return fail(MOE_EINVAL, "NULL pointer argument");
     if ((uintptr_t)x % (x_type == MOE_F32 ? 4 : 2) || (uintptr_t)d % 4)
         return fail(MOE_EINVAL, "x and d must be aligned to their elements");
+    if (x == q || x == d || (void*)q == d) return fail(MOE_EINVAL, "x, q and d must not overlap");
     const QuantRowsArgs a{x, elem_of(x_type), rows, K, q, d};
     return hip_check(launch_quant_rows(a, (hipStream_t)stream), "quantize rows");
 }

@@ -152,7 +152,7 @@ def test_gradient_validation():
     assert _bw(x=FAKE + 8) == moe.MOE_EINVAL
     assert _bw(dx=2 * FAKE + 8) == moe.MOE_EINVAL
     assert _bw(dw=3 * FAKE + 8) == moe.MOE_EINVAL
-    for same in (dict(dx=FAKE), dict(dx=4 * FAKE), dict(dw=FAKE), dict(dw=2 * FAKE), dict(dw=4 * FAKE)):
+    for same in (dict(dx=FAKE), dict(dx=4 * FAKE), dict(dx=FAKE << 4, w=_w(data=FAKE << 4)), dict(dw=FAKE), dict(dw=2 * FAKE), dict(dw=4 * FAKE)):
         assert _bw(**same) == moe.MOE_EINVAL and "inputs" in moe.last_error()
     assert _bw(wsp=FAKE + 8) == moe.MOE_EINVAL
     assert _bw(dy=None) == moe.MOE_EINVAL
@@ -174,6 +174,8 @@ def test_quantize_rows_validation():
     assert f(FAKE + 1, moe.MOE_F16, 4, 8, FAKE, FAKE, None) == moe.MOE_EINVAL
     assert f(FAKE + 2, moe.MOE_F32, 4, 8, FAKE, FAKE, None) == moe.MOE_EINVAL
     assert f(FAKE, moe.MOE_F32, 4, 8, FAKE, FAKE + 2, None) == moe.MOE_EINVAL
+    for x, q, d in ((FAKE, FAKE, 2 * FAKE), (FAKE, 2 * FAKE, FAKE), (FAKE, 2 * FAKE, 2 * FAKE)):
+        assert f(x, moe.MOE_F32, 4, 8, q, d, None) == moe.MOE_EINVAL and "overlap" in moe.last_error()
     assert f(None, moe.MOE_F32, 0, 8, None, None, None) == moe.MOE_OK
 
 

@@ -163,9 +163,9 @@ def test_int8_segments_and_extremes(N):
 
 @pytest.mark.parametrize("src", [BF, HF, F32])
 @pytest.mark.parametrize("T,k,N,K,per_slot,weighted", [(3000, 2, 40, 64, False, False), (2500, 2, 33, 80, True, True),
-                                                       (1500, 3, 24, 4256, False, True)])
+                                                       (1500, 3, 24, 4256, False, True), (300000, 1, 8, 16, False, False)])
 def test_int8_of_many_slots(T, k, N, K, per_slot, weighted, src):
-    """Codes made beside the row ids of several chunks, or (the last) by the quantizer's own launch."""
+    """Codes made beside the row ids of several chunks (300000: several rows a wave), or by the quantizer's own launch."""
     g = torch.Generator().manual_seed(T)
     ids, E = _ids(T, 5, k, g, invalid=0.1), 5
     x = torch.randn((T * (k if per_slot else 1), K), generator=g).to(src)
@@ -288,3 +288,23 @@ def test_gradient_of_long_segments(segments, dtype, dw):
                                           route_w=rw.cuda() if weighted else None, want=("w",), d_w_dtype=dw)[1]
         ref.within(got, *ref.grads(w.double(), x.double(), ids, d.double(), rw if weighted else None, False, dtype, dw)[1],
                    "d_w")
+
+
+def test_gradients_of_many_rows():
+    """More of d_dst than the thread blocks beside the row ids take at once: rounded and scaled rows of all of them."""
+    T, E, N, K = 140000, 3, 1024, 16
+    g = torch.Generator(device="cuda").manual_seed(21)
+    ids = torch.randint(0, E, (T, 1), generator=g, device="cuda", dtype=torch.int32)
+    w = torch.randn((E, N, K), generator=g, device="cuda").to(BF)
+    x = torch.randn((T, K), generator=g, device="cuda").to(BF)
+    rw = torch.rand((T, 1), generator=g, device="cuda")
+    dy = torch.randn((T, N), generator=g, device="cuda")
+    d_x, d_w, _ = moe.moe_mul_mat_id_backward(moe.Weights(w), x, ids, dy, route_w=rw, want=("src1", "w"), d_w_dtype=F32)
+    for e in range(E):
+        at = torch.nonzero(ids[:, 0] == e).flatten()
+        rows = (rw[at] * dy[at]).to(BF).double()          # as the library rounds them
+        xe = x[at].double()
+        ref.within(d_w[e], (rows.t() @ xe).cpu(), ((rows.abs().t() @ xe.abs()) * (len(at) + 1) * ref.U32).cpu(), "d_w")
+        rows, we, f = dy[at].to(BF).double(), w[e].double(), rw[at].double()
+        v, m = f * (rows @ we), f * (rows.abs() @ we.abs()) * (N + 1) * ref.U32
+        ref.within(d_x[at], v.cpu(), ref.rounded(v, m, BF).cpu(), "d_src1")
