@@ -206,8 +206,8 @@ moe_status moe_gather_rows(const void *src1, moe_dtype src1_type, int64_t src1_r
  *            BF16, F16 and I8: src1, w's data and the workspace 16-byte aligned
  *            (MOE_EINVAL), rows and cols < 2^30, opt->act_quant 0. Their GEMV path: n_tokens *
  *            n_used <= 64, I8 also cols <= 16384 (else forcing it is MOE_EINVAL); path 0 takes it
- *            there while n_tokens * n_used <= 4 * n_experts, or 12; tau is not read. The two paths
- *            add the same products in different orders.
+ *            there while n_tokens * n_used <= 4 * n_experts, or 12; tau is not read. The order in
+ *            which a row's products are added goes by the path and the call's sizes.
  *   src1     device [n_tokens][B][K], B = src1_rows_per_token in {1, n_used}
  *   ids      device int32 [n_tokens][n_used]
  *   route_w  NULL: dst = float32 [n_tokens][n_used][N], dst[t][s] = W_{ids[t][s]} src1_row;

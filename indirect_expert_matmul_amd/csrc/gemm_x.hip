@@ -10,7 +10,8 @@
 // the row-id pass.
 //
 // Product and row gradient, k_gemm_x: a block has up to 320 rows of a segment and 256 columns (8 waves,
-// one block a CU; 64 x 128 and two blocks where the segments are short). Both operands come to LDS by direct copies,
+// one block a CU; 64 x 128 and two blocks where the segments are short; 64 x 32, four waves that take parts of the depth in
+// turn, where that makes few blocks). Both operands come to LDS by direct copies,
 // 128 bytes of a row a stage (64 bytes a row reach half the rate), the rows of activations through the row map. Weights
 // have a ring of three stages, activations of two: two stages of weights, which come from HBM, are under
 // way while one is multiplied. Chunks of 16 bytes are swizzled so that the reads of LDS have no
@@ -95,14 +96,15 @@ __device__ __forceinline__ i32x4 read_t(const uint8_t* p) {
 
 // Geometry: WM x WN waves, each SM x SN tiles of 32 x 32; RB bytes of every row a stage, rings of NSA slots for the
 // first operand (activations) and NSB >= NSA for the second (weights); OCC waves a SIMD. TX: rows that a segment's
-// tiles may have beyond BM (the last ring slot of the weights makes room for them).
-template <int WM_, int WN_, int SM_, int SN_, int RB_, int NSA_, int NSB_, int OCC_, int TX_ = 0>
+// tiles may have beyond BM (the last ring slot of the weights makes room for them). KW: groups of those waves that
+// take RB bytes of the rows in turn, each with rings of its own, and add up their sums at the end.
+template <int WM_, int WN_, int SM_, int SN_, int RB_, int NSA_, int NSB_, int OCC_, int TX_ = 0, int KW_ = 1>
 struct Tile {
-    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, RB = RB_, NSA = NSA_, NSB = NSB_, OCC = OCC_, TX = TX_;
-    static constexpr int waves = WM * WN, threads = 64 * waves;
+    static constexpr int WM = WM_, WN = WN_, SM = SM_, SN = SN_, RB = RB_, NSA = NSA_, NSB = NSB_, OCC = OCC_, TX = TX_, KW = KW_;
+    static constexpr int waves = WM * WN, threads = 64 * waves * KW;
     static constexpr int BM = 32 * WM * SM, BN = 32 * WN * SN, MX = SM + TX / (32 * WM);
     static constexpr int a_slot = BM * RB, b_slot = BN * RB;
-    static constexpr int lds = NSA * a_slot + NSB * b_slot;
+    static constexpr int rings = NSA * a_slot + NSB * b_slot, lds = KW * rings;
     static_assert(NSA * TX * RB <= (NSB - NSA) * b_slot, "room for the taller tiles");
 };
 template <int N>
@@ -161,7 +163,7 @@ template <class T, int TR, bool OUT16, class G>
 __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
     using Elem = typename T::Elem;
     constexpr int RB = G::RB, W = G::waves;
-    constexpr int KS = RB / (int)sizeof(Elem);    // reduction elements per stage
+    constexpr int KS = RB / (int)sizeof(Elem), KA = KS * G::KW;   // reduction elements of a group of waves and of all, per stage
     constexpr int EC = 16 / (int)sizeof(Elem);    // elements of a chunk
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int cols = TR ? P.K : P.N, depth = TR ? P.N : P.K;
@@ -170,10 +172,10 @@ __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
     const int e = at.e, m0 = at.m0, m_len = at.m_len, col0 = at.nt * G::BN;
 
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wv = wave % W, wk = wave / W;
     const int wm = wv / G::WN, wn = wv % G::WN;   // waves of a SIMD (wv, wv + 4) share the columns: uneven rows meet there
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
-    const int nst = (depth + KS - 1) / KS;
+    const int nst = (depth + KA - 1) / KA;
     const int subs = (m_len + 31) >> 5;           // 32-row sub-tiles: of wave row wm, wm, wm + WM, ...
     const void* zero = g_zero;
 
@@ -184,22 +186,24 @@ __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
     const int n_copies = subs * (32 / CR);
     static_assert(CB * CR * W == G::BN, "whole copies per wave");
     const uint8_t* ap[CA];
-    const int a_k = ((lane % CL) ^ swz<RB>(lane / CL + (CR == 8 ? 8 * (wv & 1) : 0))) * EC;   // of this lane's chunk
-    static_assert(CR == 16 || W % 2 == 0, "a wave's copies differ in multiples of 16 rows");
+    // of this lane's chunk, of copies i with i % 2 = 0 and 1: the swizzle goes by the row mod 16
+    const auto chunk_k = [&](int i) { return wk * KS + ((lane % CL) ^ swz<RB>(lane / CL + (CR == 8 ? 8 * ((i * W + wv) & 1) : 0))) * EC; };
+    const int a_k[2] = {chunk_k(0), chunk_k(1)};
     auto find_rows = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < CA; i++) {
             const int R = (i * W + wv) * CR + lane / CL;
             const int j = m0 + min(R, m_len - 1);
             const int64_t row = P.a_rows ? P.a_rows[j] : j;
-            ap[i] = (const uint8_t*)P.A + (row * P.lda + a_k) * (int64_t)sizeof(Elem);
+            ap[i] = (const uint8_t*)P.A + (row * P.lda + a_k[i & 1]) * (int64_t)sizeof(Elem);
         }
     };
     constexpr int BROW = TR ? G::BN * 2 : RB;        // bytes of a row of the weight tile in LDS
     constexpr int BLR = BROW / 16;                   // lanes of a row
     const uint8_t* bp[CB];
     int b_k[CB];   // reduction element of this lane's chunk
-    const int64_t bstep = TR ? (int64_t)KS * P.K * (int)sizeof(Elem) : RB;
+    static_assert(!TR || G::KW == 1, "the groups' parts are of the rows' bytes");
+    const int64_t bstep = TR ? (int64_t)KS * P.K * (int)sizeof(Elem) : RB * G::KW;
 #pragma unroll
     for (int i = 0; i < CB; i++) {
         const int R = (wv * CB + i) * (64 / BLR) + lane / BLR;
@@ -208,20 +212,20 @@ __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
             b_k[i] = R;
             bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + R) * P.K + c) * (int64_t)sizeof(Elem);
         } else {
-            b_k[i] = ((lane % CL) ^ swz<RB>(R)) * EC;
+            b_k[i] = wk * KS + ((lane % CL) ^ swz<RB>(R)) * EC;
             bp[i] = (const uint8_t*)P.W + (((int64_t)e * P.N + min(col0 + R, cols - 1)) * P.K + b_k[i]) * (int64_t)sizeof(Elem);
         }
     }
     // copy i of a wave's: of a stage's activations, of its weights; to: the ring slot
     auto copy_a = [&](int i, int s, uint32_t to) __attribute__((always_inline)) {
         if (i * W + wv < n_copies) {
-            const bool in = s * KS + a_k < depth;   // what passes the end is zero on both sides
+            const bool in = s * KA + a_k[i & 1] < depth;   // what passes the end is zero on both sides
             dma16v(in ? (const void*)ap[i] : zero, lds0 + to + (i * W + wv) * 1024);
-            ap[i] += RB;
+            ap[i] += RB * G::KW;
         }
     };
     auto copy_b = [&](int i, int s, uint32_t to) __attribute__((always_inline)) {
-        const bool in = s * KS + b_k[i] < depth;
+        const bool in = s * KA + b_k[i] < depth;
         dma16v(in ? (const void*)bp[i] : zero, lds0 + to + (wv * CB + i) * 1024);
         bp[i] += bstep;
     };
@@ -262,9 +266,9 @@ __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
         constexpr bool tall = decltype(tall_c)::value;
         constexpr int NSB = tall ? NSA : G::NSB, a_slot = tall ? (G::BM + G::TX) * RB : G::a_slot;
         constexpr int NCA = tall ? CA : (G::BM / CR + W - 1) / W;   // activation copies of a wave at most
-        static_assert(NSA == 2 && NSA * a_slot + NSB * G::b_slot <= G::lds, "");
-        auto slot_a = [&](int i) { return (uint32_t)(i * a_slot); };
-        auto slot_b = [&](int i) { return (uint32_t)(NSA * a_slot + i * G::b_slot); };
+        static_assert(NSA == 2 && NSA * a_slot + NSB * G::b_slot <= G::rings, "");
+        auto slot_a = [&](int i) { return (uint32_t)(wk * G::rings + i * a_slot); };
+        auto slot_b = [&](int i) { return (uint32_t)(wk * G::rings + NSA * a_slot + i * G::b_slot); };
 #pragma unroll
         for (int i = 0; i < MACT; i++)
 #pragma unroll
@@ -351,6 +355,38 @@ __device__ __forceinline__ void gemm_x(const ExpertGemm& P, int block) {
         else if (OUT16) s_scale[r] = P.row_w ? P.row_w[o] : 1.f;
     }
     __syncthreads();
+
+    if constexpr (G::KW > 1) {   // the groups' sums, added in order by the waves for a part of the rows each
+        static_assert(G::KW == 4 && W == 1 && G::SN == 1 && !OUT16, "a wave a group, eight rows of a sub-tile a wave");
+        typedef std::conditional_t<std::is_same<T, I8>::value, int32_t, float> Sum;
+        Sum* part = (Sum*)(smem + (G::BM + G::TX) * 8);
+        static_assert((G::BM + G::TX) * 8 + G::KW * G::SM * 4096 <= G::lds, "the ring has room");
+#pragma unroll
+        for (int i = 0; i < G::SM; i++)
+            if (32 * i < m_len) {
+#pragma unroll
+                for (int v = 0; v < 16; v++) part[((wk * G::SM + i) * 16 + v) * 64 + lane] = acc[i][0][v];
+            }
+        __syncthreads();
+        const int col = col0 + l32;
+        float scale = 1.f;
+        if constexpr (std::is_same<T, I8>::value) scale = P.w_scale[(int64_t)e * P.N + min(col, cols - 1)];
+#pragma unroll
+        for (int i = 0; i < G::SM; i++) {
+            if (32 * i >= m_len) break;
+            const int base = 32 * i + 8 * wk + 4 * h;
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                Sum sum = part[(i * 16 + 4 * wk + u) * 64 + lane];
+#pragma unroll
+                for (int w = 1; w < G::KW; w++) sum += part[((w * G::SM + i) * 16 + 4 * wk + u) * 64 + lane];
+                float v = (float)sum;
+                if constexpr (std::is_same<T, I8>::value) v *= s_scale[base + u] * scale;
+                if (base + u < m_len && col < cols) ((float*)P.out)[(uint64_t)(uint32_t)s_row[base + u] * (uint32_t)cols + col] = v;
+            }
+        }
+        return;
+    }
 
     // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the sub-tile, column l % 32. A tile's edges are told
     // apart once: 128 stores a lane with their own conditions took as long as the products of 20 stages.
@@ -693,6 +729,7 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
 
 using Wide = Tile<2, 4, 4, 2, 128, 2, 3, 2, 64>;   // up to 320 x 256, one block a CU
 using Narrow = Tile<1, 4, 2, 1, 128, 2, 3, 2>;    // 64 x 128, two blocks a CU
+using Deep = Tile<1, 1, 2, 1, 128, 2, 3, 1, 0, 4>;   // 64 x 32, four waves along the rows, one block a CU
 using GradW = Tile<1, 4, 4, 2, 64, 3, 3, 2>;      // 128 x 256, two blocks a CU
 
 // Both gradients in one launch, blocks of the experts' first: neither fills the chip when they are small (both gradients,
@@ -706,6 +743,15 @@ __global__ __launch_bounds__(GradW::threads, GradW::OCC) void k_grads(ExpertGrad
     else gemm_x<T, 1, OUT16, Narrow>(g, block - w_blocks);
 }
 
+// Few blocks of the narrow tile: four times as many, whose waves share the depth (mul_mat_id by the grouped path, narrow /
+// deep in us on one MI355X, by narrow blocks: 32, E8 k2 512 x 512, 20 tokens 10.1 / 8.3; 70, E4 k1 256 x 7168, 2000 tokens
+// 57.6 / 48.5; 72, E5 k2 943 x 4192, 141 tokens 43.3 / 22.4; 80, E72 k8 74 x 2608, 68 tokens 23.7 / 14.8; 152, E16 k2 1024 x
+// 1024, 100 tokens 15.0 / 16.6; 184, E8 k2 1024 x 4096, 500 tokens 41.2 / 48.6; 320, E8 k2 4096 x 4096, 64 tokens 68 / 69; int8
+// 72 34.9 / 24.7, 80 22.4 / 17.5, 184 34.9 / 42.3).
+bool deep_tile(const ExpertGemm& a) {
+    return (int64_t)a.m_tiles_max * ((a.N + Narrow::BN - 1) / Narrow::BN) <= 96;
+}
+
 template <class T, int TR, bool OUT16, class G>
 hipError_t launch(const ExpertGemm& a, hipStream_t st) {
     const int64_t grid = expert_gemm_grid(a, TR ? 1 : 0);
@@ -717,7 +763,10 @@ hipError_t launch(const ExpertGemm& a, hipStream_t st) {
 }
 template <class T, int TR, bool OUT16>
 hipError_t launch_tile(const ExpertGemm& a, hipStream_t st) {
-    return a.tile_m == Wide::BM ? launch<T, TR, OUT16, Wide>(a, st) : launch<T, TR, OUT16, Narrow>(a, st);
+    if (a.tile_m == Wide::BM) return launch<T, TR, OUT16, Wide>(a, st);
+    if constexpr (!TR)
+        if (deep_tile(a)) return launch<T, TR, OUT16, Deep>(a, st);
+    return launch<T, TR, OUT16, Narrow>(a, st);
 }
 
 constexpr int kGradWLds = GradW::lds + kMapRows * 8;
@@ -770,7 +819,8 @@ int expert_gemm_tile_m(int64_t slots, int64_t E, int64_t cols) {
 }
 
 int64_t expert_gemm_grid(const ExpertGemm& a, int grad) {
-    const int64_t cols = grad ? a.K : a.N, bn = a.tile_m == Wide::BM ? Wide::BN : Narrow::BN;
+    const int64_t cols = grad ? a.K : a.N;
+    const int64_t bn = a.tile_m == Wide::BM ? Wide::BN : !grad && deep_tile(a) ? Deep::BN : Narrow::BN;
     return ((int64_t)a.m_tiles_max * ((cols + bn - 1) / bn) + 7) / 8 * 8;
 }
 

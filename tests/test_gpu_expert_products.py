@@ -47,6 +47,10 @@ SHAPES = [
     (300, 2, 1, 300, 264, False, False, 0.1),
     (513, 3, 2, 129, 328, True, True, 0.05),
     (700, 1, 1, 512, 64, False, False, 0.0),
+    (120, 60, 2, 257, 328, True, True, 0.1),
+    (150, 70, 2, 130, 72, False, False, 0.1),
+    (500, 3, 2, 2100, 200, False, True, 0.05),
+    (31, 4, 3, 100, 2120, True, False, 0.1),
 ]
 
 

@@ -383,7 +383,15 @@ def test_experts_past_32_bits(T, path, dtype):
     tail = moe.Weights(w.data[E - 2:], None if w.scales is None else w.scales[E - 2:])
     a = moe.moe_mul_mat_id(tail, x, ids, path=path)
     b = moe.moe_mul_mat_id(w, x, ids + (E - 2), path=path)
-    _same(a, b)
+    if dtype == BF and path == moe.PATH_GEMM:
+        # the numbers of experts may take tiles that add in different orders: each float32 sum of K products is off by
+        # at most K 2^-24 of the sum of their magnitudes, so the two differ by at most twice that
+        for e in range(2):
+            t, s = torch.nonzero(ids == e, as_tuple=True)
+            most = 2 * K * 2.0 ** -24 * (x[t].double().abs() @ tail.data[e].double().abs().t())
+            assert ((a[t, s].double() - b[t, s].double()).abs() <= most).all()
+    else:
+        _same(a, b)
     assert a.abs().max() > 0
     if dtype == BF and path == moe.PATH_GEMM:
         dy = torch.randn((T, 2, N), device="cuda").to(BF)
