@@ -272,7 +272,7 @@ __device__ __forceinline__ int bucket_bits(int NB) { return 32 - __clz(NB - 1); 
 // ---------------------------------------------------------------- one workgroup
 // 16 waves (the most one workgroup holds), so each wave walks at most four batches:
 // with 8 waves the two serial walks (count, place) of 6 batches each took 3.3 and
-// 3.6 us of an 11.8 us pass on 3072 entries; with 16 waves and the ids kept in
+// 3.6 us of an 11.8 us pass on 512 x 6 entries; with 16 waves and the ids kept in
 // registers between the walks, the pass takes about 7 us.
 constexpr int kSingleWaves = 16;
 static_assert(kRowIdsOneBlockMax <= (int64_t)kSingleWaves * 64 * kPre,
