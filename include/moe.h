@@ -232,16 +232,20 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  *   w            BF16 or F16, n_mat = n_experts, rows = N, cols = K
  *   src1         device [n_tokens][B][K] of w's type; ids, route_w as in the forward call
  *   d_dst        device [n_tokens][n_used][N], with route_w [n_tokens][N]; of w's type, or F32,
- *                which is rounded once to w's type
+ *                which is rounded once to w's type (but not for d_w with route_w)
  *   d_src1       NULL (not wanted), or device [n_tokens][B][K] of w's type (written, summed in
  *                float32 and rounded once)
  *   d_w          NULL, or device [n_experts][N][K] (written), d_w_type: w's type or F32. With route_w
- *                the rows w_i * dy_i are rounded to w's type before they are multiplied
+ *                the rows w_i * dy_i are float32 products (of d_dst as it is given) that are multiplied
+ *                as sums of two numbers of w's type, off by at most 2^-15 of them (BF16) or 2^-21
+ *                (F16), for an F32 d_w of three, which hold them. F16: times a power of two that
+ *                takes the call's largest finite one of a slot with an expert to [2^14, 2^15), which
+ *                adds up to 2^-38 of that one for each number. Infinities and NaN stay what they are
  *   d_route_w    NULL, or device float32 [n_tokens][n_used] (written); needs route_w
  * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
  * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
- * opt: path must be 0 or 1, act_quant 0; kernel order for timing: row ids (which also round and scale
- * d_dst's rows)[, rows of g, for small segments with the experts' gradient][, join][, experts' gradient][, join].
+ * opt: path must be 0 or 1, act_quant 0; kernel order for timing: [F16, d_w with route_w: the largest
+ * product, ]row ids (which also round and scale d_dst's rows)[, rows of g, for small segments with the experts' gradient][, join][, experts' gradient][, join].
  */
 moe_status moe_mul_mat_id_backward(const moe_weights *w, const void *src1, moe_dtype src1_type,
                                    int32_t src1_rows_per_token, const int32_t *ids,

@@ -480,19 +480,30 @@ __global__ __launch_bounds__(G::threads, G::OCC) void k_gemm_x(ExpertGemm P) {
 
 // ---------------------------------------------------------------- expert gradient
 // dW_e tile of BM rows (n) x BN columns (k); the reduction runs along e's positions, KS a stage, both operands
-// read transposed. (Weighted calls bring rows of dY that are scaled and in position order: scaling them here, between
-// the LDS and the products, took 575 us for 32 experts of 2880 x 2880 and 16384 slots, against 437 without it.)
+// read transposed. Weighted calls bring rows of dY times their factors (scaling them here, between
+// the LDS and the products, took 575 us for 32 experts of 2880 x 2880 and 16384 slots, against 437 without it) as
+// TERMS rows of the type each, whose sum they are: rounded to one 16-bit row, they would leave d_w with half again
+// the error of its own rounding, or of 16 bits where it is float32. A stage has the terms of its positions behind one another
+// and their rows of X once.
 constexpr int kMapRows = 512;   // ring of positions whose rows are in LDS, refilled by halves
 
-template <class T, class G>
+template <class G, int TERMS>
+struct GradWGeometry {
+    static constexpr int KS = TERMS == 1 ? G::RB / 2 : 16;   // positions of a stage
+    static constexpr int stage = KS * (TERMS * G::BM + G::BN) * 2;
+    static constexpr int NS = TERMS == 2 ? G::NSA + 1 : G::NSA;
+    static constexpr int lds = NS * stage + kMapRows * 8;
+};
+
+template <class T, class G, int TERMS>
 __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part) {
     using Elem = typename T::Elem;
-    constexpr int W = G::waves, NS = G::NSA;
+    using Geo = GradWGeometry<G, TERMS>;
+    constexpr int W = G::waves, NS = Geo::NS, KS = Geo::KS, stage = Geo::stage;
     static_assert(G::NSA == G::NSB, "one ring");
-    constexpr int KS = G::RB / 2, Q = KS / 16, kHalf = kMapRows / 2 / KS;   // positions and MFMA steps of a stage; stages of half a map
+    constexpr int KA = TERMS * KS, Q = KA / 16, kHalf = kMapRows / 2 / KS;   // rows of dY and MFMA steps of a stage; stages of half a map
     static_assert(NS + 2 <= kHalf && kMapRows % (2 * KS) == 0, "the map covers the stages in flight");
     constexpr int AROW = G::BM * 2, BROW = G::BN * 2, ALR = AROW / 16, BLR = BROW / 16;
-    constexpr int stage = KS * (AROW + BROW);
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     int32_t* s_dy = (int32_t*)(smem + NS * stage);   // rows of dY and X of the positions
     int32_t* s_x = s_dy + kMapRows;
@@ -532,8 +543,8 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
             dma4v(in ? (const void*)(P.x_rows + j0 + p) : zero, at + kMapRows * 4 + 256 * i);
         }
     };
-    constexpr int CA = KS * ALR / 64 / W, CB = KS * BLR / 64 / W;
-    static_assert(CA * 64 * W == KS * ALR && CB * 64 * W == KS * BLR, "whole copies per wave");
+    constexpr int CA = KA * ALR / 64 / W, CB = KS * BLR / 64 / W;
+    static_assert(CA * 64 * W == KA * ALR && CB * 64 * W == KS * BLR, "whole copies per wave");
     // Where a stage's copies read: the rows come from the map in LDS two stages ahead of the copies and become
     // addresses a stage ahead, between the products (a copy that waits for its address keeps the products waiting).
     int row_a[CA], row_b[CB];
@@ -543,7 +554,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
 #pragma unroll
     for (int i = 0; i < CA; i++) {
         const int R = (wv * CA + i) * (64 / ALR) + lane / ALR;
-        base_a[i] = (const uint8_t*)P.dY + min(row0 + ((lane % ALR) ^ swz_t(R)) * 8, P.ldy - 8) * 2ll;
+        base_a[i] = (const uint8_t*)P.dY + (R / KS * P.term_stride + min(row0 + ((lane % ALR) ^ swz_t(R)) * 8, P.ldy - 8)) * 2ll;
     }
 #pragma unroll
     for (int i = 0; i < CB; i++) {
@@ -555,7 +566,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
 #pragma unroll
         for (int i = 0; i < CA; i++) {
             const int R = (wv * CA + i) * (64 / ALR) + lane / ALR;
-            row_a[i] = s_dy[at + R];
+            row_a[i] = s_dy[at + R % KS];
         }
 #pragma unroll
         for (int i = 0; i < CB; i++) row_b[i] = s_x[at + (wv * CB + i) * (64 / BLR) + lane / BLR];
@@ -568,7 +579,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
         if ((s + 1) * KS > len) {   // the segment's end: zeros past it
 #pragma unroll
             for (int i = 0; i < CA; i++)
-                if (s * KS + (wv * CA + i) * (64 / ALR) + lane / ALR >= len) from_a[i] = (const uint8_t*)zero;
+                if (s * KS + ((wv * CA + i) * (64 / ALR) + lane / ALR) % KS >= len) from_a[i] = (const uint8_t*)zero;
 #pragma unroll
             for (int i = 0; i < CB; i++)
                 if (s * KS + (wv * CB + i) * (64 / BLR) + lane / BLR >= len) from_b[i] = (const uint8_t*)zero;
@@ -579,7 +590,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
 #pragma unroll
         for (int i = 0; i < CA; i++) dma16v(from_a[i], st + (wv * CA + i) * 1024);
 #pragma unroll
-        for (int i = 0; i < CB; i++) dma16v(from_b[i], st + KS * AROW + (wv * CB + i) * 1024);
+        for (int i = 0; i < CB; i++) dma16v(from_b[i], st + KA * AROW + (wv * CB + i) * 1024);
     };
 
     f32x16 acc[G::SM][G::SN];
@@ -601,7 +612,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
     auto read = [&](Frag& f, int slot, int q) __attribute__((always_inline)) {
         const uint8_t* st = smem + slot * stage;
 #pragma unroll
-        for (int c = 0; c < G::SN; c++) f.b[c] = read_t<BROW>(st + KS * AROW + b_lane[c] + q * 16 * BROW);
+        for (int c = 0; c < G::SN; c++) f.b[c] = read_t<BROW>(st + KA * AROW + b_lane[c] + (TERMS == 1 ? q : 0) * 16 * BROW);
 #pragma unroll
         for (int i = 0; i < G::SM; i++) f.a[i] = read_t<AROW>(st + a_lane[i] + q * 16 * AROW);
     };
@@ -635,7 +646,8 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
         Frag f0, f1;
         read(f0, 0, 0);
         int slot = 0;
-        for (int s = 0; s < nst; s++) {
+        // stage s, its first step's operands in f; the next stage's go to f where it has an even number of steps, else to g
+        auto one = [&](int s, Frag& f, Frag& g) __attribute__((always_inline)) {
             auto step = [&](auto q_c, Frag& now, Frag& next) __attribute__((always_inline)) {
                 constexpr int q = decltype(q_c)::value;
                 read(next, slot, q + 1);
@@ -644,20 +656,18 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
                 multiply(now);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            static_assert(Q == 2 || Q == 4, "");
-            step(Int<0>{}, f0, f1);
-            if constexpr (Q == 4) {
-                step(Int<1>{}, f1, f0);
-                step(Int<2>{}, f0, f1);
-            }
+            static_assert(Q == 2 || Q == 3, "");
+            step(Int<0>{}, f, g);
+            if constexpr (Q == 3) step(Int<1>{}, g, f);
+            Frag &last = Q == 3 ? f : g, &first = Q == 3 ? g : f;
             const int was = slot;
             slot = slot == NS - 1 ? 0 : slot + 1;
             if (s + 1 < nst) {
                 landed(s + 1);
-                read(f0, slot, 0);
+                read(first, slot, 0);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            multiply(f1, 0, G::SM / 2);
+            multiply(last, 0, G::SM / 2);
             __builtin_amdgcn_sched_barrier(0);
             if (s + NS < nst) {
                 issue(was);
@@ -665,10 +675,22 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
                 // last stage: the rows two halves on take its place, needed kHalf - NS stages from now.
                 if ((s + 1) % kHalf == 0 && (s + 1 + kHalf) * KS < len) map((s + 1 + kHalf) * KS);
             }
-            multiply(f1, G::SM / 2, G::SM);
+            multiply(last, G::SM / 2, G::SM);
             locate(s + NS + 1);
             __builtin_amdgcn_sched_barrier(0);
+        };
+        for (int s = 0; s < nst; s++) {
+            one(s, f0, f1);
+            if constexpr (Q == 3)
+                if (++s < nst) one(s, f1, f0);
         }
+    }
+    if (TERMS > 1 && P.unscale) {
+        const float u = *P.unscale;
+#pragma unroll
+        for (int i = 0; i < G::SM; i++)
+#pragma unroll
+            for (int c = 0; c < G::SN; c++) acc[i][c] *= u;
     }
 
     // ---- element 4 g + u of lane l: row 8 g + 4 (l / 32) + u of the tile, column l % 32
@@ -696,6 +718,7 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
         return;
     }
     // 16-bit rows go through the ring's LDS, to be stored as whole lines
+    if constexpr (TERMS < 3) {   // of float32 alone
     static_assert(G::BM * BROW <= NS * stage, "the tile's rows");
     uint8_t* tile = smem;
     __syncthreads();
@@ -720,11 +743,12 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
         const i32x4 v = *(const i32x4*)(tile + r * BROW + at);
         if (row0 + r < P.N && col_out < P.K) __builtin_nontemporal_store(v, (i32x4*)(o + (int64_t)r * P.K));
     }
+    }
 }
 
-template <class T, class G>
+template <class T, class G, int TERMS>
 __global__ __launch_bounds__(G::threads, G::OCC) void k_grad_w(ExpertGradW P) {
-    grad_w<T, G>(P, (int)blockIdx.x, (int)blockIdx.y);
+    grad_w<T, G, TERMS>(P, (int)blockIdx.x, (int)blockIdx.y);
 }
 
 using Wide = Tile<2, 4, 4, 2, 128, 2, 3, 2, 64>;   // up to 320 x 256, one block a CU
@@ -735,11 +759,11 @@ using GradW = Tile<1, 4, 4, 2, 64, 3, 3, 2>;      // 128 x 256, two blocks a CU
 // Both gradients in one launch, blocks of the experts' first: neither fills the chip when they are small (both gradients,
 // us per call in one launch against two: E8 k2 300 x 200, 30 tokens 20.0 / 22.8; E8 k2 512 x 512, 2000 tokens 29.0 / 36.6;
 // E32 k4 2880 x 2880, 100 tokens 226 / 238; E64 k6 1408 x 2048, 500 tokens 189 / 189).
-template <class T, bool OUT16>
+template <class T, bool OUT16, int TERMS>
 __global__ __launch_bounds__(GradW::threads, GradW::OCC) void k_grads(ExpertGradW w, ExpertGemm g, int w_grid) {
     static_assert(GradW::threads == Narrow::threads && GradW::OCC == Narrow::OCC, "one launch");
     const int block = (int)blockIdx.x, w_blocks = w_grid * w.splits;
-    if (block < w_blocks) grad_w<T, GradW>(w, block % w_grid, block / w_grid);
+    if (block < w_blocks) grad_w<T, GradW, TERMS>(w, block % w_grid, block / w_grid);
     else gemm_x<T, 1, OUT16, Narrow>(g, block - w_blocks);
 }
 
@@ -769,8 +793,6 @@ hipError_t launch_tile(const ExpertGemm& a, hipStream_t st) {
     return launch<T, TR, OUT16, Narrow>(a, st);
 }
 
-constexpr int kGradWLds = GradW::lds + kMapRows * 8;
-
 // Parts of an expert's columns, of eight parts of its tiles, that read the fewest rows of dY and X.
 int grad_w_pk(int64_t N, int64_t K) {
     const int64_t n = (N + GradW::BM - 1) / GradW::BM, k = (K + GradW::BN - 1) / GradW::BN;
@@ -783,26 +805,35 @@ int grad_w_pk(int64_t N, int64_t K) {
     return best;
 }
 
-template <class T, bool OUT16>
+template <class T, bool OUT16, int TERMS>
 hipError_t launch_both(const ExpertGemm& a, ExpertGradW w, hipStream_t st) {
     w.pk = grad_w_pk(w.N, w.K);
-    constexpr int lds = kGradWLds > Narrow::lds ? kGradWLds : Narrow::lds;
+    constexpr int w_lds = GradWGeometry<GradW, TERMS>::lds, lds = w_lds > Narrow::lds ? w_lds : Narrow::lds;
     static PerDeviceOnce cap;
-    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grads<T, OUT16>, lds)) return e;
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grads<T, OUT16, TERMS>, lds)) return e;
     const int64_t w_grid = expert_grad_w_grid(w), grid = w_grid * w.splits + expert_gemm_grid(a, 1);
-    k_grads<T, OUT16><<<(unsigned)grid, GradW::threads, lds, st>>>(w, a, (int)w_grid);
+    k_grads<T, OUT16, TERMS><<<(unsigned)grid, GradW::threads, lds, st>>>(w, a, (int)w_grid);
     return hipGetLastError();
 }
+template <class T, bool OUT16>
+hipError_t launch_both(const ExpertGemm& a, const ExpertGradW& w, hipStream_t st) {
+    return w.terms == 1 ? launch_both<T, OUT16, 1>(a, w, st) : w.terms == 2 ? launch_both<T, OUT16, 2>(a, w, st) : launch_both<T, OUT16, 3>(a, w, st);
+}
 
-template <class T>
+template <class T, int TERMS>
 hipError_t launch_w(ExpertGradW a, hipStream_t st) {
     using G = GradW;
+    constexpr int lds = GradWGeometry<G, TERMS>::lds;
     a.pk = grad_w_pk(a.N, a.K);
     static PerDeviceOnce cap;
-    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G>, kGradWLds)) return e;
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_grad_w<T, G, TERMS>, lds)) return e;
     const dim3 grid((unsigned)expert_grad_w_grid(a), (unsigned)a.splits);
-    k_grad_w<T, G><<<grid, G::threads, kGradWLds, st>>>(a);
+    k_grad_w<T, G, TERMS><<<grid, G::threads, lds, st>>>(a);
     return hipGetLastError();
+}
+template <class T>
+hipError_t launch_w(const ExpertGradW& a, hipStream_t st) {
+    return a.terms == 1 ? launch_w<T, 1>(a, st) : a.terms == 2 ? launch_w<T, 2>(a, st) : launch_w<T, 3>(a, st);
 }
 
 }  // namespace

@@ -1,9 +1,31 @@
 // The rows of d_dst as the gradients' products of mul_mat_id read them: device code of thread blocks
-// beside the row ids. A pass of memory (16384 slots of 2880 bf16 from 4096 rows, with their factors: 24 us).
+// beside the row ids. A pass of memory (16384 slots of 2880 bf16 from 4096 rows, with their factors, two terms: 47 us).
 #pragma once
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
+
+// The elements that a float32 number is the sum of: each takes the leading bits of what is left (8 of bf16, 11 of f16), the
+// last one is rounded. Two are off by at most 2^-15 (bf16) or 2^-21 (f16) of the number, three hold it. An infinity or
+// a NaN is all of them; a term that would be zero is the smallest number of the sign instead (2^-133, 2^-24), so that all
+// have one sign and an infinity of the other operand does not meet a zero or both signs.
+template <class Elem>
+__device__ __forceinline__ Elem cut_off(float v) {
+    if constexpr (std::is_same<Elem, __bf16>::value)
+        return __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(v) >> 16));
+    else
+        return __builtin_bit_cast(_Float16, (uint16_t)__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v, 0.f)));
+}
+template <class Elem>
+__device__ __forceinline__ Elem next_term(float v, float& rest, bool last) {
+    if (!(fabsf(v) < __builtin_inff())) return (Elem)v;
+    Elem t = last ? (Elem)rest : cut_off<Elem>(rest);
+    rest -= (float)t;
+    if (v != 0.f && (float)t == 0.f) t = __builtin_bit_cast(Elem, (uint16_t)(v < 0.f ? 0x8001 : 1));
+    return t;
+}
 
 // Block `block` of `blocks`: eight columns a thread, in the element type, and with the slots' factors.
 template <class Elem, int THREADS>
@@ -12,6 +34,17 @@ __device__ __forceinline__ void prepare_rows(const GradInArgs& a, int64_t block,
     const uint32_t chunks = (uint32_t)(a.ld / 8);
     const int64_t all = a.rows * chunks;
     const bool whole = !a.f32 && a.N % 8 == 0 && ((uintptr_t)a.src & 15) == 0;
+    float scale = 1.f;
+    if (a.tops) {   // every wave joins the parts by itself
+        float top = 0.f;
+        for (int i = threadIdx.x & 63; i < a.n_tops; i += 64) top = fmaxf(top, a.tops[i]);
+#pragma unroll
+        for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        // exponents below -112 would take the factor past float32
+        const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 127, -112) - 14 : 0;
+        scale = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (block == 0 && threadIdx.x == 0) *a.unscale = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
     for (int64_t i = block * THREADS + threadIdx.x; i < all; i += blocks * THREADS) {
         const int64_t row = i >> 32 ? i / chunks : (int64_t)((uint32_t)i / chunks), c = (i - row * chunks) * 8;
         float v[8];
@@ -35,9 +68,15 @@ __device__ __forceinline__ void prepare_rows(const GradInArgs& a, int64_t block,
         if (a.scaled) {
             for (int s = 0; s < a.k; s++) {
                 const float w = a.route_w[row * a.k + s];
+                float p[8], rest[8];
 #pragma unroll
-                for (int u = 0; u < 8; u++) o[u] = c + u < a.N ? (Elem)(w * v[u]) : (Elem)0.f;
-                *(Vec*)((Elem*)a.scaled + (row * a.k + s) * a.ld + c) = o;
+                for (int u = 0; u < 8; u++) rest[u] = p[u] = c + u < a.N ? w * v[u] * scale : 0.f;
+                Elem* to = (Elem*)a.scaled + (row * a.k + s) * a.ld + c;
+                for (int t = 0; t < a.terms; t++, to += a.rows * a.k * a.ld) {
+#pragma unroll
+                    for (int u = 0; u < 8; u++) o[u] = next_term<Elem>(p[u], rest[u], t + 1 == a.terms);
+                    *(Vec*)to = o;
+                }
             }
         }
     }

@@ -1,7 +1,7 @@
 // What the gradients of mul_mat_id do after the grouped products, joining the slots' gradient rows g:
 //   d_src1[r] = sum over r's slots, ascending, of route_w * g   (float32, rounded once)
 //   d_route_w[i] = sum over the columns of g[i] * src1[r]
-#include "moe_internal.h"
+#include "quant_rows.h"
 
 namespace moe {
 namespace {
@@ -112,7 +112,60 @@ __global__ __launch_bounds__(kThreads) void k_join_w(ExpertGradW a) {
     }
 }
 
+// A wave takes the largest finite magnitude of a row of d_dst, then of its products with the row's factors.
+template <int SRC>
+__global__ __launch_bounds__(kThreads) void k_grad_top(GradTopArgs a) {
+    using S = QuantSrc<SRC>;
+    constexpr int EC = S::EC;
+    __shared__ float tops[kWaves];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    float top = 0.f;
+    for (int64_t r = (int64_t)blockIdx.x * kWaves + wv; r < a.rows; r += (int64_t)gridDim.x * kWaves) {
+        const typename S::Elem* row = (const typename S::Elem*)a.src + r * a.N;
+        float most = 0.f;
+        const auto grow = [&](float v) {
+            const float m = fabsf(v);
+            if (m < __builtin_inff()) most = fmaxf(most, m);
+        };
+        for (int64_t c = lane * EC; c < a.N; c += 64 * EC) {
+            if (c + EC <= a.N) {
+                const typename S::Vec v = S::load(row + c);
+#pragma unroll
+                for (int u = 0; u < EC; u++) grow((float)v[u]);
+            } else {
+                for (int64_t u = c; u < a.N; u++) grow((float)row[u]);
+            }
+        }
+#pragma unroll
+        for (int m = 32; m; m >>= 1) most = fmaxf(most, __shfl_xor(most, m));
+        for (int s = lane; s < a.k; s += 64) {
+            const int32_t e = a.ids[r * a.k + s];
+            const float w = fabsf(a.route_w[r * a.k + s]);
+            if (e >= 0 && e < a.E && w < __builtin_inff()) top = fmaxf(top, fminf(w * most, 3.402823466e38f));
+        }
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+    if (lane == 0) tops[wv] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWaves; w++) top = fmaxf(top, tops[w]);
+        a.tops[blockIdx.x] = top;
+    }
+}
+
 }  // namespace
+
+int grad_tops(int64_t rows) {
+    const int64_t blocks = (rows + kWaves - 1) / kWaves;
+    return (int)(blocks < kGradTops ? blocks : kGradTops);
+}
+hipError_t launch_grad_top(const GradTopArgs& a, hipStream_t st) {
+    if (a.rows <= 0) return hipSuccess;
+    if (a.f32) k_grad_top<kElemF32><<<(unsigned)grad_tops(a.rows), kThreads, 0, st>>>(a);
+    else k_grad_top<kElemF16><<<(unsigned)grad_tops(a.rows), kThreads, 0, st>>>(a);
+    return hipGetLastError();
+}
 
 hipError_t launch_join_w(const ExpertGradW& a, hipStream_t st) {
     const int64_t blocks = ((int64_t)a.E * a.N * a.K / 8 + kThreads - 1) / kThreads;

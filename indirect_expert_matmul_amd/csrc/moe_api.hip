@@ -917,13 +917,16 @@ struct GradPlan {
     float* g;       // per-slot rows of g (not direct)
     float* dots;    // direct: parts of d_route_w
     int dot_parts;
-    void* scaled;   // weighted d_w: rows route_w * dY by slot
+    int terms;      // of which rows route_w * dY are the sums
+    void* scaled;   // weighted d_w: those rows by slot, [terms][n][ld]
+    float* tops;    // float16: parts of their largest, then their scale's inverse
     int splits;     // of the positions of each expert, for d_w
     float* parts;
 };
-// dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses)
+// dy_as_is: d_dst can be read in place (its type, and rows of whole 16-byte chunks at aligned addresses). w_f32: d_w is
+// float32, for which the scaled rows keep all bits (three terms); two hold more than twice the bits of a 16-bit d_w.
 GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_t B, bool weighted, int want,
-                    bool dy_as_is) {
+                    bool dy_as_is, bool w_f32) {
     GradPlan p{};
     const int64_t n = T * k;
     p.tile_m = expert_gemm_tile_m(n, w->n_mat, w->cols);
@@ -931,7 +934,11 @@ GradPlan carve_grad(Carve& c, const moe_weights* w, int64_t T, int32_t k, int32_
     p.r = carve_row_ids(c, n, (int32_t)w->n_mat, true, p.tile_m);
     p.ld = (w->rows + 7) / 8 * 8;
     if (!dy_as_is && (!weighted || (want & (kWantX | kWantR)))) p.dy = c.take((size_t)(weighted ? T : n) * p.ld * 2);
-    if (weighted && (want & kWantW)) p.scaled = c.take((size_t)n * p.ld * 2);
+    p.terms = !weighted ? 1 : w_f32 ? 3 : 2;
+    if (weighted && (want & kWantW)) {
+        p.scaled = c.take((size_t)n * p.ld * 2 * p.terms);
+        if (w->type == MOE_F16) p.tops = (float*)c.take((kGradTops + 1) * 4);
+    }
     p.splits = want & kWantW ? expert_grad_w_splits(n, w->n_mat, w->rows, w->cols) : 1;
     if (p.splits > 1) p.parts = (float*)c.take((size_t)p.splits * w->n_mat * w->rows * w->cols * 4);
     if ((want & (kWantX | kWantR)) && !p.direct) p.g = (float*)c.take((size_t)n * w->cols * 4);
@@ -1644,8 +1651,8 @@ size_t moe_mul_mat_id_backward_workspace_size(const moe_weights* w, moe_dtype d_
                                               const moe_options* opt) {
     if (!w || validate_grad(w, w->type, d_dst_type, src1_rows_per_token, n_tokens, n_used, weighted != 0, want, opt))
         return 0;
-    Carve c(nullptr);   // room for a copy of d_dst also where its address alone asks for one
-    carve_grad(c, w, n_tokens, n_used, src1_rows_per_token, weighted != 0, want, false);
+    Carve c(nullptr);   // room for a copy of d_dst also where its address alone asks for one, and for a float32 d_w
+    carve_grad(c, w, n_tokens, n_used, src1_rows_per_token, weighted != 0, want, false, true);
     return c.off;
 }
 
@@ -1677,11 +1684,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     const int32_t E = (int32_t)w->n_mat;
     const bool as_is = d_dst_type == w->type && w->rows % 8 == 0 && (uintptr_t)d_dst % 16 == 0;
     Carve sz(nullptr);
-    carve_grad(sz, w, T, k, B, weighted, want, as_is);
+    carve_grad(sz, w, T, k, B, weighted, want, as_is, d_w_type == MOE_F32);
     if (sz.off > ws_bytes || !ws) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
     if ((s = check_aligned(ws, "the workspace"))) return s;
     Carve c(ws);
-    const GradPlan p = carve_grad(c, w, T, k, B, weighted, want, as_is);
+    const GradPlan p = carve_grad(c, w, T, k, B, weighted, want, as_is, d_w_type == MOE_F32);
     const hipStream_t st = (hipStream_t)stream;
     const void* dy = as_is ? d_dst : p.dy;
     // positions' tokens (ids_src1 of one row a token) and slots (ids_dst)
@@ -1705,6 +1712,11 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     gw.E = E;
     gw.dY = weighted ? p.scaled : dy;
     gw.ldy = (int32_t)p.ld;
+    gw.terms = p.terms;
+    gw.term_stride = n * p.ld;
+    const bool scale = p.tops && n > 0;
+    float* unscale = scale ? p.tops + kGradTops : nullptr;
+    gw.unscale = unscale;
     gw.X = src1;
     gw.dy_rows = p.r.ids_dst;
     gw.x_rows = B == 1 ? p.r.ids_src1 : p.r.ids_dst;
@@ -1721,7 +1733,14 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     BesideRowIds beside{};   // direct rows of invalid slots: 16-bit rows of K columns are rows of K / 2 words
     if (d_src1 && n > 0 && p.direct) beside.zero = ZeroSlots{ids, (float*)d_src1, n, E, g.K / 2};
     if ((p.dy || p.scaled) && n > 0) beside.grad = GradInArgs{d_dst, d_dst_type == MOE_F32, g.type, weighted ? T : n,
-                                                              w->rows, p.ld, p.dy, route_w, k, p.scaled};
+                                                              w->rows, p.ld, p.dy, route_w, k, p.scaled, p.terms,
+                                                              scale ? p.tops : nullptr, grad_tops(T), unscale};
+    if (scale) {
+        const GradTopArgs top{d_dst, d_dst_type == MOE_F32, T, w->rows, route_w, ids, k, E, p.tops};
+        tm.begin();
+        if ((s = hip_check(launch_grad_top(top, st), "largest scaled gradient"))) return s;
+        tm.end();
+    }
     tm.begin();
     if ((s = hip_check(launch_row_ids(ra, st, nullptr, &beside), "row ids"))) return s;
     tm.end();

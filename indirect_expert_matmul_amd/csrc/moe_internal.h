@@ -228,8 +228,8 @@ struct QuantRowsArgs {
     float* d;           // [rows]
 };
 // Rows of d_dst, float32 (f32) or of the type, as the gradients' products read them: rows of the type, ld elements (a
-// multiple of 8), 0 past N; and rounded once from the product, each slot's row times its factor:
-// scaled[row * k + s] = route_w[row * k + s] * src[row].
+// multiple of 8), 0 past N; and each slot's row times its factor, route_w[row * k + s] * src[row] in float32, as the sum
+// of `terms` rows of the type, scaled[term][row * k + s].
 struct GradInArgs {
     const void* src;    // [rows][N]; rows 0: nothing
     int32_t f32;
@@ -239,7 +239,26 @@ struct GradInArgs {
     const float* route_w;
     int32_t k;
     void* scaled;       // or nullptr
+    int32_t terms;
+    // float16: the terms stand for the product times a power of two that brings the largest magnitude of tops[n_tops]
+    // (launch_grad_top) to [2^14, 2^15); its inverse is written to *unscale
+    const float* tops;  // or nullptr: no factor
+    int32_t n_tops;
+    float* unscale;
 };
+// Parts of the largest finite |route_w[row * k + s] * src[row][c]| over the slots with an expert, one a block.
+constexpr int kGradTops = 512;
+struct GradTopArgs {
+    const void* src;    // [rows][N], float32 or float16
+    int32_t f32;
+    int64_t rows, N;
+    const float* route_w;
+    const int32_t* ids;
+    int32_t k, E;
+    float* tops;        // [grad_tops(rows)]
+};
+int grad_tops(int64_t rows);   // at most kGradTops
+hipError_t launch_grad_top(const GradTopArgs& a, hipStream_t st);
 // Work that the row-id pass's first launch does in thread blocks of its own behind its own ones.
 struct BesideRowIds {
     QuantFp4Args quant;   // bf16; rows 0: none
@@ -325,6 +344,9 @@ struct ExpertGradW {
     int32_t N, K, E;
     const void* dY;            // rows of ldy elements, columns N .. ldy - 1 anything finite
     int32_t ldy;               // a multiple of 8
+    int32_t terms;             // a row of dY is the sum of 1 to 3, term_stride elements apart
+    int64_t term_stride;
+    const float* unscale;      // nullptr, or a factor for the sums
     const void* X;             // rows of K
     int32_t pk;                        // set by the launcher
     const int32_t *dy_rows, *x_rows;   // of position j: rows of dY and X
