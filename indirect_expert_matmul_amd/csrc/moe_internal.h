@@ -259,13 +259,13 @@ struct GradTopArgs {
 };
 int grad_tops(int64_t rows);   // at most kGradTops
 hipError_t launch_grad_top(const GradTopArgs& a, hipStream_t st);
-// Work that the row-id pass's first launch does in thread blocks of its own behind its own ones.
+// Work that the row-id pass's first launch does in thread blocks of its own behind its own ones: one of the first
+// three, and the last.
 struct BesideRowIds {
     QuantFp4Args quant;   // bf16; rows 0: none
     QuantRowsArgs rows;   // rows 0: none; K a multiple of 16
     GradInArgs grad;      // rows 0: none
     ZeroSlots zero;
-    int32_t quant_blocks, rows_blocks, grad_blocks;   // set by the launcher
 };
 hipError_t launch_quant_mxfp4(const QuantFp4Args& a, hipStream_t st);
 // Grouped GEMM of MXFP4 experts (GemmProblem.qs1/d1: codes and E8M0 bytes) with MXFP4

@@ -289,37 +289,70 @@ size_t single_lds_bytes(int NB, bool mask) {
 // lanes of a bucket are found with one ballot per bit of the bucket id.
 constexpr int kSingleMaskBuckets = 512;
 
-// Thread block `block` behind the `own` row-id ones.
+// What the first launch also does, behind the `own` row-id blocks. Each kind of work has instances of its own: sharing
+// one took scalar registers from the others (row ids with 2826 rows of 5472 columns to MXFP4 beside them 10.2 us, 11.2
+// with the other kinds in the same kernel).
+struct Alone {};    // nothing, no blocks
+struct ZeroOnly {};
+template <class WORK>
+struct Beside {
+    WORK work;
+    ZeroSlots zero;
+    int32_t blocks;   // of work
+};
+template <>
+struct Beside<Alone> {};
+
+// Blocks of THREADS threads.
+constexpr int64_t kWorkBlocks = 1 << 14;   // they take several rows past it
+int64_t work_blocks(int64_t n) { return n < kWorkBlocks ? n : kWorkBlocks; }
 template <int THREADS>
-__device__ __forceinline__ void beside_row_ids(const BesideRowIds& b, int own) {
-    const int block = (int)blockIdx.x - own, rows_block = block - b.quant_blocks;
-    if (rows_block < 0) {
-        quantize_mxfp4_blocks<true, THREADS>(b.quant, block);
-    } else if (rows_block < b.rows_blocks) {
-        constexpr int kWavesBeside = THREADS / 64;
-        const int lane = threadIdx.x & 63;
-        for (int64_t r = (int64_t)rows_block * kWavesBeside + (threadIdx.x >> 6); r < b.rows.rows;
-             r += (int64_t)b.rows_blocks * kWavesBeside) {
-            if (b.rows.src_type == kElemF32) quant_row_twice<kElemF32>(b.rows, r, lane);
-            else if (b.rows.src_type == kElemBf16) quant_row_twice<kElemBf16>(b.rows, r, lane);
-            else quant_row_twice<kElemF16>(b.rows, r, lane);
-        }
-    } else if (rows_block < b.rows_blocks + b.grad_blocks) {
-        if (b.grad.type == kElemBf16) prepare_rows<__bf16, THREADS>(b.grad, rows_block - b.rows_blocks, b.grad_blocks);
-        else prepare_rows<_Float16, THREADS>(b.grad, rows_block - b.rows_blocks, b.grad_blocks);
+int64_t work_grid(const ZeroOnly&) { return 0; }
+template <int THREADS>
+int64_t work_grid(const QuantFp4Args& a) { return quant_fp4_grid(a, THREADS); }
+template <int THREADS>
+int64_t work_grid(const QuantRowsArgs& a) { return work_blocks((a.rows * 64 + THREADS - 1) / THREADS); }
+template <int THREADS>
+int64_t work_grid(const GradInArgs& a) { return work_blocks((a.rows * (a.ld / 8) + THREADS - 1) / THREADS); }
+
+template <int THREADS>
+__device__ __forceinline__ void do_work(const ZeroOnly&, int, int) {}
+template <int THREADS>
+__device__ __forceinline__ void do_work(const QuantFp4Args& a, int block, int) { quantize_mxfp4_blocks<true, THREADS>(a, block); }
+template <int THREADS>
+__device__ __forceinline__ void do_work(const QuantRowsArgs& a, int block, int blocks) {
+    constexpr int kWavesBeside = THREADS / 64;
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)block * kWavesBeside + (threadIdx.x >> 6); r < a.rows; r += (int64_t)blocks * kWavesBeside) {
+        if (a.src_type == kElemF32) quant_row_twice<kElemF32>(a, r, lane);
+        else if (a.src_type == kElemBf16) quant_row_twice<kElemBf16>(a, r, lane);
+        else quant_row_twice<kElemF16>(a, r, lane);
+    }
+}
+template <int THREADS>
+__device__ __forceinline__ void do_work(const GradInArgs& a, int block, int blocks) {
+    if (a.type == kElemBf16) prepare_rows<__bf16, THREADS>(a, block, blocks);
+    else prepare_rows<_Float16, THREADS>(a, block, blocks);
+}
+
+// Whether this block is one of those.
+template <int THREADS, class WORK>
+__device__ __forceinline__ bool beside_row_ids(const Beside<WORK>& b, int own) {
+    if constexpr (std::is_same<WORK, Alone>::value) {
+        return false;
     } else {
-        const int before = b.quant_blocks + b.rows_blocks + b.grad_blocks;
-        zero_invalid_slots<THREADS>(b.zero, block - before, gridDim.x - own - before);
+        const int block = (int)blockIdx.x - own;
+        if (block < 0) return false;
+        if (block < b.blocks) do_work<THREADS>(b.work, block, b.blocks);
+        else zero_invalid_slots<THREADS>(b.zero, block - b.blocks, gridDim.x - own - b.blocks);
+        return true;
     }
 }
 
-template <bool MASK, bool BESIDE>
-__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, BesideRowIds beside) {
+template <bool MASK, class WORK>
+__global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs a, Beside<WORK> beside) {
     constexpr int NW = kSingleWaves, NT = NW * 64;
-    if (BESIDE && blockIdx.x > 0) {
-        beside_row_ids<NT>(beside, 1);
-        return;
-    }
+    if (beside_row_ids<NT>(beside, 1)) return;
     extern __shared__ __attribute__((aligned(16))) uint64_t lds_single[];
     __shared__ int32_t wsum[NW];
     const int NB = a.E + 1, nbits = bucket_bits(NB);
@@ -403,12 +436,9 @@ __global__ __launch_bounds__(kSingleWaves * 64) void k_row_ids_single(RowIdsArgs
 // wcnt (chunk-major) for the place pass, the chunk's totals to chunk_cnt (bucket-major)
 // for the scan over chunks. Registers are held to 64 per lane so that four blocks (eight
 // waves per SIMD) fit a CU: 1024 chunks then run in one round instead of one and a third.
-template <bool BESIDE>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, BesideRowIds beside) {
-    if (BESIDE && (int)blockIdx.x >= (int)a.n_chunks) {
-        beside_row_ids<kThreads>(beside, (int)a.n_chunks);
-        return;
-    }
+template <class WORK>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void k_row_ids_count(RowIdsArgs a, Beside<WORK> beside) {
+    if (beside_row_ids<kThreads>(beside, (int)a.n_chunks)) return;
     // LDS, sized for this launch: per wave, a group mask per bucket [kWaves][NB] and the
     // running count per bucket [kWaves][NB]
     extern __shared__ __attribute__((aligned(16))) uint64_t count_lds[];
@@ -674,51 +704,43 @@ void row_ids_carve_scratch(RowIdsArgs& a, void* scratch) {
 
 namespace {
 
-// Thread blocks of THREADS threads for the work beside the row ids.
-constexpr int64_t kRowsBlocks = 1 << 14;   // they take several rows past it
-template <int THREADS>
-unsigned beside_grid(BesideRowIds& b) {
-    b.quant_blocks = (int32_t)quant_fp4_grid(b.quant, THREADS);
-    const int64_t rows_blocks = (b.rows.rows * 64 + THREADS - 1) / THREADS;
-    b.rows_blocks = (int32_t)(rows_blocks < kRowsBlocks ? rows_blocks : kRowsBlocks);
-    const int64_t grad_blocks = (b.grad.rows * (b.grad.ld / 8) + THREADS - 1) / THREADS;
-    b.grad_blocks = (int32_t)(grad_blocks < kRowsBlocks ? grad_blocks : kRowsBlocks);
-    return (unsigned)(b.quant_blocks + b.rows_blocks + b.grad_blocks + zero_slots_grid(b.zero, THREADS));
+template <int THREADS, class WORK>
+unsigned beside_grid(Beside<WORK>& b) {
+    if constexpr (std::is_same<WORK, Alone>::value) {
+        return 0;
+    } else {
+        b.blocks = (int32_t)work_grid<THREADS>(b.work);
+        return (unsigned)(b.blocks + zero_slots_grid(b.zero, THREADS));
+    }
 }
 
-template <bool MASK, bool BESIDE>
-hipError_t launch_single(const RowIdsArgs& a, BesideRowIds b, hipStream_t st) {
+template <bool MASK, class WORK>
+hipError_t launch_single(const RowIdsArgs& a, Beside<WORK> b, hipStream_t st) {
     static PerDeviceOnce lds_cap;   // dynamic LDS cap, once per device
-    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_single<MASK, BESIDE>,
+    if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_single<MASK, WORK>,
                                          (int)single_lds_bytes(MASK ? kSingleMaskBuckets : kMaxBuckets, MASK)))
         return e;
-    const unsigned grid = 1 + (BESIDE ? beside_grid<kSingleWaves * 64>(b) : 0);
-    k_row_ids_single<MASK, BESIDE><<<grid, kSingleWaves * 64, single_lds_bytes(a.E + 1, MASK), st>>>(a, b);
+    const unsigned grid = 1 + beside_grid<kSingleWaves * 64>(b);
+    k_row_ids_single<MASK, WORK><<<grid, kSingleWaves * 64, single_lds_bytes(a.E + 1, MASK), st>>>(a, b);
     return hipGetLastError();
 }
 
-template <bool BESIDE>
-hipError_t launch_count(const RowIdsArgs& a, BesideRowIds b, size_t lds, hipStream_t st) {
+template <class WORK>
+hipError_t launch_count(const RowIdsArgs& a, Beside<WORK> b, size_t lds, hipStream_t st) {
     static PerDeviceOnce cap;   // the count kernel's dynamic LDS cap, once per device
-    if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count<BESIDE>,
+    if (const hipError_t e = set_lds_cap(cap, (const void*)k_row_ids_count<WORK>,
                                          kWaves * kMaxBuckets * (int)(sizeof(uint64_t) + sizeof(int32_t))))
         return e;
-    const unsigned grid = (unsigned)a.n_chunks + (BESIDE ? beside_grid<kThreads>(b) : 0);
-    k_row_ids_count<BESIDE><<<grid, kThreads, lds, st>>>(a, b);
+    const unsigned grid = (unsigned)a.n_chunks + beside_grid<kThreads>(b);
+    k_row_ids_count<WORK><<<grid, kThreads, lds, st>>>(a, b);
     return hipGetLastError();
 }
 
-}  // namespace
-
-// beside: what the first launch also does, or nullptr.
-hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches, const BesideRowIds* beside) {
-    RowIdsArgs a = a0;
-    const BesideRowIds b = beside ? *beside : BesideRowIds{};
+template <class WORK>
+hipError_t launch_with(RowIdsArgs a, hipStream_t st, int* n_launches, const Beside<WORK>& b) {
     if (a.n <= kRowIdsOneBlockMax) {
         if (n_launches) *n_launches = 1;
-        if (a.E + 1 <= kSingleMaskBuckets)
-            return beside ? launch_single<true, true>(a, b, st) : launch_single<true, false>(a, b, st);
-        return beside ? launch_single<false, true>(a, b, st) : launch_single<false, false>(a, b, st);
+        return a.E + 1 <= kSingleMaskBuckets ? launch_single<true>(a, b, st) : launch_single<false>(a, b, st);
     }
     a.chunk = chunk_len(a.n);
     a.n_chunks = (a.n + a.chunk - 1) / a.chunk;
@@ -739,20 +761,30 @@ hipError_t launch_row_ids(const RowIdsArgs& a0, hipStream_t st, int* n_launches,
     if (a.n_chunks <= kLocalScanChunks) {
         static PerDeviceOnce lds_cap;
         if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<true>, kCap)) return e;
-        if (const hipError_t e = beside ? launch_count<true>(a, b, count_lds, st) : launch_count<false>(a, b, count_lds, st))
-            return e;
+        if (const hipError_t e = launch_count(a, b, count_lds, st)) return e;
         k_row_ids_place<true><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);
         if (n_launches) *n_launches = 2;
         return hipGetLastError();
     }
     static PerDeviceOnce lds_cap;
     if (const hipError_t e = set_lds_cap(lds_cap, (const void*)k_row_ids_place<false>, kCap)) return e;
-    if (const hipError_t e = beside ? launch_count<true>(a, b, count_lds, st) : launch_count<false>(a, b, count_lds, st))
-        return e;
+    if (const hipError_t e = launch_count(a, b, count_lds, st)) return e;
     k_row_ids_scan_chunks<<<(unsigned)(a.E + 1), kThreads, 0, st>>>(a);
     k_row_ids_place<false><<<(unsigned)a.n_chunks, kThreads, stage, st>>>(a);
     if (n_launches) *n_launches = 3;
     return hipGetLastError();
+}
+
+}  // namespace
+
+// beside: what the first launch also does, or nullptr.
+hipError_t launch_row_ids(const RowIdsArgs& a, hipStream_t st, int* n_launches, const BesideRowIds* beside) {
+    const BesideRowIds b = beside ? *beside : BesideRowIds{};
+    if (b.quant.rows > 0) return launch_with(a, st, n_launches, Beside<QuantFp4Args>{b.quant, b.zero, 0});
+    if (b.rows.rows > 0) return launch_with(a, st, n_launches, Beside<QuantRowsArgs>{b.rows, b.zero, 0});
+    if (b.grad.rows > 0) return launch_with(a, st, n_launches, Beside<GradInArgs>{b.grad, b.zero, 0});
+    if (b.zero.n > 0) return launch_with(a, st, n_launches, Beside<ZeroOnly>{ZeroOnly{}, b.zero, 0});
+    return launch_with(a, st, n_launches, Beside<Alone>{});
 }
 
 }  // namespace moe
