@@ -71,7 +71,7 @@
  * n_experts <= 1024, Q8_0, MXFP4 and IQ4_NL cols % 32 == 0, IQ4_XS cols % 256 == 0, BF16 and
  * F16 cols % 8 == 0, I8 cols % 16 == 0 and <= 131072. On the grouped GEMM path the
  * activation tensor whose rows are gathered through the row map (moe_ffn_fused: x;
- * moe_mul_mat_id with quantized experts: src1) must be under 4 GiB, and each GEMM launch must hold fewer
+ * moe_mul_mat_id with quantized experts: src1) must be under 4 GiB, and each GEMM or GEMV launch must hold fewer
  * than 2^32 work-items; float32 moe_mul_mat_id needs n_tokens * n_used * N < 2^32.
  */
 #ifndef MOE_H

@@ -292,21 +292,32 @@ hipError_t launch(const DecXArgs& a, dim3 grid, int waves, size_t lds, hipStream
     k_decode_x<TYPE, FUSE, MAKE><<<grid, 64 * waves, lds, st>>>(a);
     return hipGetLastError();
 }
+// Waves of a block, and blocks along the rows.
+struct Shape {
+    int waves;
+    int64_t blocks;
+    int64_t work_items() const { return 64 * waves * blocks; }
+};
+Shape shape(int64_t N, int d_max, bool fuse) {
+    Shape s{fuse ? 1 : kRowWaves, 0};
+    const int rows = kR * (fuse ? 1 : kRowWaves);
+    s.blocks = (N + rows - 1) / rows;
+    if (fuse)   // a wave an expert, as far as a dispatch of so many rows holds them
+        while (s.waves < d_max && s.waves < kSumWaves && 2 * s.work_items() < 1ll << 32) s.waves *= 2;
+    return s;
+}
+int distinct_max(const DecXArgs& a) { return a.T * a.k < a.E ? a.T * a.k : a.E; }
+
 template <int TYPE, bool MAKE>
 hipError_t launch(DecXArgs a, hipStream_t st) {
-    const int n = a.T * a.k, d_max = n < a.E ? n : a.E;
+    const int n = a.T * a.k, d_max = distinct_max(a);
     const bool fuse = a.out_tok != nullptr;
-    int waves = kRowWaves;
+    const Shape g = shape(a.N, d_max, fuse);
+    const int waves = g.waves;
     a.xs = a.T * a.act_B;
-    if (fuse) {
-        waves = 1;
-        while (waves < d_max && waves < kSumWaves) waves *= 2;
-    } else if (a.xs > kP) {
-        a.xs = kP;
-    }
+    if (!fuse && a.xs > kP) a.xs = kP;
     const size_t lds = (MAKE ? (size_t)a.xs * a.K + kDecXSlots * 4 * (1 + kSumWaves) : 0) + (fuse ? (size_t)n * kR * 4 : 0);
-    const int rows = kR * (fuse ? 1 : kRowWaves);
-    const dim3 grid((unsigned)((a.N + rows - 1) / rows), (unsigned)(fuse ? 1 : d_max));
+    const dim3 grid((unsigned)g.blocks, (unsigned)(fuse ? 1 : d_max));
     return fuse ? launch<TYPE, true, MAKE>(a, grid, waves, lds, st) : launch<TYPE, false, MAKE>(a, grid, waves, lds, st);
 }
 
@@ -316,6 +327,8 @@ bool decode_x_makes(int64_t T) { return T == 1; }
 bool decode_x_fuses(ElemType type, int64_t T, int64_t B, int64_t K) {
     return type != kElemI8 || !decode_x_makes(T) || T * B * K <= 64 * 1024;
 }
+
+int64_t decode_x_work_items(const DecXArgs& a) { return shape(a.N, distinct_max(a), a.out_tok != nullptr).work_items(); }
 
 hipError_t launch_decode_x(const DecXArgs& a, hipStream_t st) {
     if (a.type == kElemBf16) return launch<kElemBf16, false>(a, st);

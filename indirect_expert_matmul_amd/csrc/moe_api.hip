@@ -871,6 +871,7 @@ moe_status mul_mat_id_elem(const moe_weights* w, const void* src1, moe_dtype src
         a.out = slot_out;
         a.route_w = route_w;
         a.out_tok = p.fuse ? dst : nullptr;
+        if (decode_x_work_items(a) >= k4GiB) return fail(MOE_ELIMIT, "mul_mat_id: the GEMV's grid exceeds 2^32 work-items");
         if (p.q) {
             const QuantRowsArgs q{src1, elem_of(src1_type), T * B, w->cols, p.q, p.d};
             tm.begin();

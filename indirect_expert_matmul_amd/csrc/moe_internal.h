@@ -384,6 +384,7 @@ struct DecXArgs {
     float* out_tok;           // [T][N], the weighted sum
     int32_t xs;               // set by the launcher
 };
+int64_t decode_x_work_items(const DecXArgs& a);   // of N, E, T, k, out_tok: a dispatch holds fewer than 2^32
 hipError_t launch_decode_x(const DecXArgs& a, hipStream_t st);
 // Whether a weighted call takes the sum itself.
 bool decode_x_fuses(ElemType type, int64_t T, int64_t B, int64_t K);
