@@ -28,3 +28,20 @@ def test_gemv_of_rows_past_full_blocks(dtype):
     assert torch.equal(moe.moe_mul_mat_id(W, x, ids, route_w=rw)[0], want)
     del W, w, want
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("rows,K", [((1 << 27) + 77, 40), ((1 << 26) + 41, 96), ((1 << 25) + 19, 200), ((1 << 24) + 9, 500)])
+def test_quantize_more_narrow_rows_than_a_grid(rows, K):
+    """Blocks that take several rows, at each number of lanes a row: zeros but for some rows."""
+    at = torch.tensor([0, 1, 255, 256, (1 << 22) - 1, 1 << 22, rows - 260, rows - 2, rows - 1])
+    some = torch.randn((len(at), K), generator=torch.Generator().manual_seed(K)).to(BF)
+    x = torch.zeros((rows, K), dtype=BF, device="cuda")
+    x[at.cuda()] = some.cuda()
+    q, d = moe.moe_quantize_rows(x)
+    one, scale = moe.moe_quantize_rows(some.cuda())
+    assert torch.equal(q[at.cuda()], one) and torch.equal(d[at.cuda()], scale)
+    assert int((d != 0).sum()) == len(at)
+    del x
+    assert int(q.view(-1)[:rows * K // 8 * 8].view(torch.int64).count_nonzero()) <= 2 * len(at) * (K // 8 + 1)
+    del q, d
+    torch.cuda.empty_cache()
