@@ -242,8 +242,8 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  *                takes the call's largest finite one of a slot with an expert to [2^14, 2^15), which
  *                adds up to 2^-38 of that one for each number. Infinities and NaN stay what they are
  *   d_route_w    NULL, or device float32 [n_tokens][n_used] (written); needs route_w
- * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output.
- * w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
+ * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output
+ * (MOE_EINVAL). w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.
  * opt: path must be 0 or 1, act_quant 0; kernel order for timing: [F16, d_w with route_w: the largest
  * product, ]row ids (which also round and scale d_dst's rows)[, rows of g, for small segments with the experts' gradient][, join][, experts' gradient][, join].
  */
@@ -328,7 +328,7 @@ moe_status moe_quantize_act(const void *x, moe_dtype x_type, int64_t rows, int64
  * q = 0 for a row of zeros, d = NaN and q = 0 for one with an infinity or a NaN. Value = d * q.
  *   x   device BF16, F16 or F32 [rows][K], any K > 0
  *   q   device int8 [rows][K] (written); d device float32 [rows] (written)
- * The three must not overlap. rows = 0 is a no-op. No workspace. Deterministic.
+ * The three must not overlap (MOE_EINVAL). rows = 0 is a no-op. No workspace. Deterministic.
  */
 moe_status moe_quantize_rows(const void *x, moe_dtype x_type, int64_t rows, int64_t K, int8_t *q,
                              float *d, void *stream);

@@ -98,6 +98,15 @@ moe_status check_aligned(const void* p, const char* name) {
     if ((uintptr_t)p % 16) return fail(MOE_EINVAL, "%s must be 16-byte aligned", name);
     return MOE_OK;
 }
+// Device memory of a call; nullptr or no bytes: none.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes);
+}
 moe_status check_elem_weights(const moe_weights* w, const char* name) {
     moe_status s;
     const int64_t unit = w->type == MOE_I8 ? 16 : 8;
@@ -1688,6 +1697,16 @@ moe_status moe_mul_mat_id_backward(const moe_weights* w, const void* src1, moe_d
     carve_grad(sz, w, T, k, B, weighted, want, as_is, d_w_type == MOE_F32);
     if (sz.off > ws_bytes || !ws) return fail(MOE_EWORKSPACE, "workspace needs %zu bytes", sz.off);
     if ((s = check_aligned(ws, "the workspace"))) return s;
+    const int64_t stack = (int64_t)((uint64_t)w->n_mat * w->rows * w->cols), slots4 = n * 4, src_bytes = T * B * w->cols * 2;
+    const Span in[] = {{src1, src_bytes}, {w->data, 2 * stack}, {ids, slots4}, {route_w, slots4},
+                       {d_dst, (weighted ? T : n) * w->rows * (d_dst_type == MOE_F32 ? 4 : 2)}};
+    const Span out[] = {{d_src1, src_bytes}, {d_w, stack * (d_w_type == MOE_F32 ? 4 : 2)}, {d_route_w, slots4}};
+    for (const Span& o : out) {
+        for (const Span& i : in)
+            if (overlap(o, i)) return fail(MOE_EINVAL, "outputs must not overlap inputs");
+        for (const Span& other : out)
+            if (&o != &other && overlap(o, other)) return fail(MOE_EINVAL, "outputs must not overlap each other");
+    }
     Carve c(ws);
     const GradPlan p = carve_grad(c, w, T, k, B, weighted, want, as_is, d_w_type == MOE_F32);
     const hipStream_t st = (hipStream_t)stream;
@@ -1799,7 +1818,11 @@ moe_status moe_quantize_rows(const void* x, moe_dtype x_type, int64_t rows, int6
     if (!x || !q || !d) return fail(MOE_EINVAL, "NULL pointer argument");
     if ((uintptr_t)x % (x_type == MOE_F32 ? 4 : 2) || (uintptr_t)d % 4)
         return fail(MOE_EINVAL, "x and d must be aligned to their elements");
-    if (x == q || x == d || (void*)q == d) return fail(MOE_EINVAL, "x, q and d must not overlap");
+    int64_t bytes;
+    if (__builtin_mul_overflow(rows, K, &bytes) || __builtin_mul_overflow(bytes, x_type == MOE_F32 ? 4 : 2, &bytes))
+        return fail(MOE_ELIMIT, "rows * K must be under 2^63 bytes");
+    const Span xs{x, bytes}, qs{q, rows * K}, ds{d, rows * 4};
+    if (overlap(xs, qs) || overlap(xs, ds) || overlap(qs, ds)) return fail(MOE_EINVAL, "x, q and d must not overlap");
     const QuantRowsArgs a{x, elem_of(x_type), rows, K, q, d};
     return hip_check(launch_quant_rows(a, (hipStream_t)stream), "quantize rows");
 }
