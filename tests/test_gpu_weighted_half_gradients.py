@@ -63,3 +63,66 @@ def test_zeros_and_no_experts():
     ids[ids == 2] = -1   # an expert without slots
     got = _d_w(w, x, ids, dy, rw, per_slot, F32)
     assert (got[2] == 0).all() and got.abs().max() > 0
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("T,E,k,N,K,per_slot", [(9, 5, 3, 40, 64, True), (700, 3, 2, 260, 528, False), (2600, 2, 2, 75, 72, True)])
+def test_used_workspace_of_the_size_asked_for(T, E, k, N, K, per_slot, dtype):
+    """Workspaces of exactly the reported size full of NaN, with either type of d_w; the same bits each time."""
+    w, x, ids, dy, rw, per_slot = _call(T, E, k, N, K, dtype, per_slot, 0.1, 13)
+    W, B = moe.Weights(w.cuda()), k if per_slot else 1
+    x, ids, dy, rw = x.cuda(), ids.cuda(), dy.cuda(), rw.cuda()
+    for want in (("w",), ("src1", "w", "route_w")):
+        for dw in (dtype, F32):
+            for dd in (dy, dy.float()):
+                need = moe.moe_mul_mat_id_backward_workspace_size(W, moe._elem_type(dd), B, T, k, True, want)
+                first = None
+                for _ in range(3):
+                    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+                    got = moe.moe_mul_mat_id_backward(W, x, ids, dd, route_w=rw, src1_rows_per_token=B, want=want, d_w_dtype=dw,
+                                                      workspace=ws[:need])
+                    assert (ws[need:] == 255).all()
+                    first = got if first is None else first
+                    for a, b in zip(got, first):
+                        assert a is b or torch.equal(a, b)
+                    assert all(torch.isfinite(t).all() for t in got if t is not None)
+
+
+def test_two_captured_gradients_in_turn():
+    """Gradients of both types captured, replayed on new inputs of another size of numbers each time (the scale is the
+    replay's own), with eager calls between."""
+    calls, graphs, outs = [], [], []
+    for i, (dtype, dw) in enumerate(((HF, HF), (BF, BF), (HF, F32))):
+        w, x, ids, dy, rw, _ = _call(300, 5, 2, 75, 72, dtype, False, 0.1, 20 + i)
+        a = dict(W=moe.Weights(w.cuda()), x=x.cuda(), ids=ids.cuda(), dy=dy.cuda(), rw=rw.cuda(), dw=dw)
+
+        def run(a=a):
+            return moe.moe_mul_mat_id_backward(a["W"], a["x"], a["ids"], a["dy"], route_w=a["rw"], d_w_dtype=a["dw"])
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run())
+        calls.append((a, run))
+        graphs.append(g)
+    for r in range(5):
+        for a, _ in calls:
+            a["dy"].normal_().mul_(2.0 ** (3 * r - 8))
+            a["rw"].uniform_().mul_(2.0 ** (-4 * r))
+            a["x"].normal_()
+        for j in ((0, 1, 2), (2, 0, 1))[r % 2]:
+            graphs[j].replay()
+            calls[(j + 1) % 3][1]()
+        torch.cuda.synchronize()
+        for (a, run), o in zip(calls, outs):
+            for u, v in zip(run(), o):
+                assert torch.equal(u, v) and torch.isfinite(u).all() and u.abs().max() > 0
+
+
+def test_top_of_many_tokens():
+    """More tokens than the blocks that look for the largest product take one of; the largest is in the last row."""
+    w, x, ids, dy, rw, per_slot = _call(9001, 3, 1, 16, 8, HF, False, 0.0, 31)
+    dy[-1, -1] = 6e4
+    rw = rw * 1e-3
+    rw[-1] = 2.0
+    ref.within(_d_w(w, x, ids, dy, rw, per_slot, F32), *_bounds(w, x, ids, dy, rw, per_slot, F32), "d_w")
