@@ -15,7 +15,7 @@
 //     rows of every selected expert, its waves an expert each in turn, and the slots' values in LDS.
 // Bound by memory: the selected experts' rows, once. Measured (one MI355X, per call): one token with 4 experts of 2880 x
 // 2880 bf16 12.3 us (5.4 TB/s; of int8 10.2, an empty call's time); 8 tokens with 6 of 64 experts of 2048 x 1408 bf16,
-// weighted, 34 us (5.9 TB/s); 8 tokens with 8 of 128 experts of 2048 x 7168 bf16 213 us (7.0 TB/s), int8 125.
+// weighted, 36 to 37 us (5.5 TB/s); 8 tokens with 8 of 128 experts of 2048 x 7168 bf16 213 us (7.0 TB/s), int8 125.
 #include <type_traits>
 
 #include "quant_rows.h"

@@ -19,9 +19,9 @@
 // operands of the next step are read before the products of this one, and the copies are issued
 // between products: a wave issues in order. A segment's tiles are of equal height, in steps of 32 rows: 2 rows of
 // waves take them in turn, and those of a SIMD share the columns, so that an odd step costs half.
-// Measured (one MI355X): 32768 slots, 128 experts of 2048 x 7168: bf16 1120 us, 860 TFLOP/s, with 4.5 GB of memory
-// traffic (3.8 at least); the clock is down to 1.5 to 1.9 GHz at the power limit, and the products alone took 660,
-// the copies alone 850. int8 615 us, 1560 TOP/s. One expert of 8192 x 8192 with 4096 slots: row gradient 1054 TFLOP/s. 3054
+// Measured (one MI355X): 32768 slots, 128 experts of 2048 x 7168: bf16 1120 to 1160 us, 830 to 860 TFLOP/s, with 4.5 GB of
+// memory traffic (4.1 at least); the products alone took 660, the copies alone 850, so that a part of them does not
+// overlap; the clock is down to 1.5 to 1.9 GHz and the matrix units are busy half of its cycles. int8 615 us, 1560 TOP/s. One expert of 8192 x 8192 with 4096 slots: row gradient 1054 TFLOP/s. 3054
 // slots, 64 experts of 1408 x 2048 (the narrow tile): 80 to 90 us for 388 MB, 4.6 TB/s.
 // Tried without gain: deeper rings of 64-byte stages, 256 x 128 tiles, wave priorities, three narrow blocks a CU, the row
 // gradient's 16-bit rows through LDS, streaming stores of the rows.
@@ -30,7 +30,8 @@
 // starts or stores; both operands are read transposed, through a map of the positions' rows in LDS.
 // Measured: 32 experts of 2880 x 2880, 16384 slots to bf16 375 us, 725 TFLOP/s (256 x 256 tiles of one block a CU were no
 // faster; the stores alone take 104, all but the stores 319); 64 experts of 1408 x 2048, 24576
-// slots to float32 228 us, of which writing 738 MB alone takes 132.
+// slots to float32 228 us, of which writing 738 MB alone takes 132. Weighted, with rows of two terms: the former 604 us,
+// matrix units busy half of the cycles (reading X's operand once for both terms made no difference).
 #include <type_traits>
 
 #include "lds_dma.h"

@@ -13,7 +13,7 @@ static __device__ __forceinline__ float quant_scale(uint32_t top) {
     return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(top) / 127.0f;
 }
 // rint(x / d) within +-127, d > 0 and r = 1 / d. The quotient by the reciprocal is at most 3 * 2^-24 of it off, that
-// is 2.3e-5: where that could move it past a half, which is one element in ten thousand, it is divided (fast false:
+// is 2.3e-5: where that could move it past a half, which is two elements in ten thousand, it is divided (fast false:
 // always).
 static __device__ __forceinline__ int quant_code(float x, float d, float r, bool fast) {
     const float t = x * r;
