@@ -1818,10 +1818,10 @@ moe_status moe_quantize_rows(const void* x, moe_dtype x_type, int64_t rows, int6
     if (!x || !q || !d) return fail(MOE_EINVAL, "NULL pointer argument");
     if ((uintptr_t)x % (x_type == MOE_F32 ? 4 : 2) || (uintptr_t)d % 4)
         return fail(MOE_EINVAL, "x and d must be aligned to their elements");
-    int64_t bytes;
-    if (__builtin_mul_overflow(rows, K, &bytes) || __builtin_mul_overflow(bytes, x_type == MOE_F32 ? 4 : 2, &bytes))
-        return fail(MOE_ELIMIT, "rows * K must be under 2^63 bytes");
-    const Span xs{x, bytes}, qs{q, rows * K}, ds{d, rows * 4};
+    int64_t n, bytes;
+    if (__builtin_mul_overflow(rows, K, &n) || __builtin_mul_overflow(n, 4, &bytes))
+        return fail(MOE_ELIMIT, "rows * K must be under 2^61");
+    const Span xs{x, x_type == MOE_F32 ? bytes : bytes / 2}, qs{q, n}, ds{d, rows * 4};
     if (overlap(xs, qs) || overlap(xs, ds) || overlap(qs, ds)) return fail(MOE_EINVAL, "x, q and d must not overlap");
     const QuantRowsArgs a{x, elem_of(x_type), rows, K, q, d};
     return hip_check(launch_quant_rows(a, (hipStream_t)stream), "quantize rows");
