@@ -240,7 +240,7 @@ moe_status moe_mul_mat_id(const moe_weights *w, const void *src1, moe_dtype src1
  *                as sums of two numbers of w's type, off by at most 2^-15 of them (BF16) or 2^-21
  *                (F16), for an F32 d_w of three, which hold them. F16: times a power of two that
  *                takes the call's largest finite one of a slot with an expert to [2^14, 2^15), which
- *                adds up to 2^-38 of that one for each number. Infinities and NaN stay what they are
+ *                adds up to 2^-38 of that one. Infinities and NaN stay what they are
  *   d_route_w    NULL, or device float32 [n_tokens][n_used] (written); needs route_w
  * At least one of d_src1, d_w and d_route_w. No output may overlap an input or another output
  * (MOE_EINVAL). w's data, src1, d_src1, d_w and the workspace 16-byte aligned (MOE_EINVAL); rows and cols < 2^30.

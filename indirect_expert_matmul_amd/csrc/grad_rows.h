@@ -9,22 +9,27 @@
 namespace moe {
 
 // The elements that a float32 number is the sum of: each takes the leading bits of what is left (8 of bf16, 11 of f16), the
-// last one is rounded. Two are off by at most 2^-15 (bf16) or 2^-21 (f16) of the number, three hold it. An infinity or
-// a NaN is all of them; a term that would be zero is the smallest number of the sign instead (2^-133, 2^-24), so that all
-// have one sign and an infinity of the other operand does not meet a zero or both signs.
+// last one is rounded. Two are off by at most 2^-15 (bf16) or 2^-21 (f16) of the number, three hold it; f16 adds up to its
+// smallest number, 2^-24. An infinity or a NaN is all of them. All have the number's sign and none is zero, so that an
+// infinity of the other operand meets neither a zero nor both signs: a bf16 term of zero is 2^-133 instead; that is too
+// little to count, which 2^-24 is not beside small numbers, so f16's leading bits are those of the next number towards
+// zero and leave something (but for numbers of one or two times 2^-24).
 template <class Elem>
 __device__ __forceinline__ Elem cut_off(float v) {
-    if constexpr (std::is_same<Elem, __bf16>::value)
+    if constexpr (std::is_same<Elem, __bf16>::value) {
         return __builtin_bit_cast(__bf16, (uint16_t)(__float_as_uint(v) >> 16));
-    else
-        return __builtin_bit_cast(_Float16, (uint16_t)__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(v, 0.f)));
+    } else {
+        const float less = v == 0.f ? v : __uint_as_float(__float_as_uint(v) - 1u);
+        return __builtin_bit_cast(_Float16, (uint16_t)__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(less, 0.f)));
+    }
 }
 template <class Elem>
 __device__ __forceinline__ Elem next_term(float v, float& rest, bool last) {   // selects: a branch an element costs more
     Elem t = last ? (Elem)rest : cut_off<Elem>(rest);
     rest -= (float)t;
     const uint32_t bits = __float_as_uint(v), small = v != 0.f ? bits >> 31 << 15 | 1u : 0u;
-    const uint32_t some = (float)t == 0.f ? small : __builtin_bit_cast(uint16_t, t);
+    const bool none = (float)t == 0.f && (std::is_same<Elem, __bf16>::value || last);
+    const uint32_t some = none ? small : __builtin_bit_cast(uint16_t, t);
     return __builtin_bit_cast(Elem, (uint16_t)((bits & 0x7f800000u) == 0x7f800000u ? __builtin_bit_cast(uint16_t, (Elem)v) : some));
 }
 

@@ -4,7 +4,7 @@ factors are not rounded to the experts' type on the way.
 Bounds. The rows v = w_i * dy_i (float32, off by U32 of v) go to the products in parts whose sum is off by at most
 PART[dtype] of v (two parts, the first cut off and the second rounded: 2^-7 * 2^-8 for bfloat16's 8 bits, 2^-10 * 2^-11
 for float16's 11; three parts, for a float32 result, hold all 24 bits). float16 rows are scaled by a power of two that
-puts the call's largest |v| of a slot with an expert within [2^14, 2^15]: each part is off by at most one smallest
+puts the call's largest |v| of a slot with an expert within [2^14, 2^15]: the last part is off by at most one smallest
 subnormal, 2^-24, which is at most 2^-38 of that largest one. The sums add (n + 1) * U32."""
 import pytest
 import torch
@@ -52,7 +52,7 @@ def _bounds(w, x, ids, dy, rw, per_slot, dw):
         d[i] = v[at].t() @ xe
         tol[i] = v[at].abs().t() @ xe.abs() * ((parts * len(at) + 2) * ref.U32 + (PART[w.dtype] if dw != F32 else 0.0))
         if w.dtype == HF:
-            tol[i] += parts * 2.0 ** -38 * top * xe.abs().sum(0)[None, :]
+            tol[i] += 2.0 ** -38 * top * xe.abs().sum(0)[None, :]
     return d, ref.rounded(d, tol, dw)
 
 

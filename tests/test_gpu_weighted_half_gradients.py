@@ -126,3 +126,29 @@ def test_top_of_many_tokens():
     rw = rw * 1e-3
     rw[-1] = 2.0
     ref.within(_d_w(w, x, ids, dy, rw, per_slot, F32), *_bounds(w, x, ids, dy, rw, per_slot, F32), "d_w")
+
+
+@pytest.mark.parametrize("dw", [HF, F32])
+def test_small_products_beside_a_large_one(dw):
+    """Columns of d_dst whose numbers, of a few bits, are 2^-26 to 2^-36 of another column's: relative to their own size
+    off by the roundings of float32 sums and of the result (a whole number of units of 2^-24 is a sum of two such)."""
+    T, E, k, N, K = 60, 2, 1, 24, 16
+    g = torch.Generator().manual_seed(40)
+    ids = torch.randint(0, E, (T, k), generator=g).to(torch.int32)
+    w = torch.zeros((E, N, K), dtype=HF)
+    x = torch.randint(1, 4, (T, K), generator=g).to(HF)
+    dy = torch.randint(1, 8, (T, N), generator=g).double() * torch.exp2(-torch.arange(N).double() - 12)
+    dy[:, 0] = 6.0 * 2 ** 12
+    dy, rw = dy.to(HF), torch.exp2(-torch.randint(0, 2, (T, k), generator=g).float())
+    got = _d_w(w, x, ids, dy, rw, False, dw).double().cpu()
+    v = dy.double() * rw.double()
+    top = v.max()
+    for e in range(E):
+        at = torch.nonzero(ids[:, 0] == e).flatten()
+        want = v[at].t() @ x[at].double()
+        tol = want * 3 * len(at) * ref.U32 + (ref.half_step(HF) * want + ref.tiny(HF) if dw == HF else 0)
+        big = (v[at] >= 2 * top * 2.0 ** -38).all(0)   # at least three units
+        assert big.sum() >= 10
+        past = want - tol >= torch.finfo(dw).max   # 24576 of every slot: a float16 result's sum is infinite
+        assert torch.equal(torch.isinf(got[e]), past) and past.any() == (dw == HF)
+        assert (past | ((got[e] - want).abs() <= tol))[big].all()
