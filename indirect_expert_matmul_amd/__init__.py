@@ -615,7 +615,7 @@ def moe_mul_mat_id_backward(w: Weights, src1: torch.Tensor, ids: torch.Tensor, d
                             workspace: Optional[torch.Tensor] = None, stream=None, events=None):
     """(d_src1, d_w, d_route_w) of moe_mul_mat_id with bfloat16 or float16 experts, from the gradient
     ``d_dst`` of its result: [T][k][N], with ``route_w`` [T][N]; the experts' dtype, or float32, which is
-    rounded to it. ``want`` names the gradients to compute, by default "src1", "w" and, with route_w,
+    rounded to it (but not for d_w with ``route_w``, whose products with it are kept in float32). ``want`` names the gradients to compute, by default "src1", "w" and, with route_w,
     "route_w"; the others come back as None. d_src1 has src1's shape and dtype, d_w the experts' shape
     and dtype or float32 (``d_w_dtype``), d_route_w is float32 [T][k]."""
     _check_ids(ids, route_w)

@@ -719,31 +719,31 @@ __device__ __forceinline__ void grad_w(const ExpertGradW& P, int block, int part
         return;
     }
     // 16-bit rows go through the ring's LDS, to be stored as whole lines
-    if constexpr (TERMS < 3) {   // of float32 alone
-    static_assert(G::BM * BROW <= NS * stage, "the tile's rows");
-    uint8_t* tile = smem;
-    __syncthreads();
+    if constexpr (TERMS < 3) {   // three terms: of a float32 d_w alone
+        static_assert(G::BM * BROW <= NS * stage, "the tile's rows");
+        uint8_t* tile = smem;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < G::SM; i++)
+        for (int i = 0; i < G::SM; i++)
 #pragma unroll
-        for (int v = 0; v < 16; v += 2) {
-            const int r = wm * G::SM * 32 + 4 * h + i * 32 + 8 * (v >> 2) + (v & 3) + odd;
+            for (int v = 0; v < 16; v += 2) {
+                const int r = wm * G::SM * 32 + 4 * h + i * 32 + 8 * (v >> 2) + (v & 3) + odd;
 #pragma unroll
-            for (int c = 0; c < G::SN; c++) {
-                const int piece = ((wn * G::SN + c) ^ (r & 7)) * 64;   // of 64 bytes, apart in neighbouring rows
-                *(uint32_t*)(tile + r * BROW + piece + (l32 >> 1) * 4) = packed<Elem>(pair_up(acc[i][c][v], acc[i][c][v + 1], odd));
+                for (int c = 0; c < G::SN; c++) {
+                    const int piece = ((wn * G::SN + c) ^ (r & 7)) * 64;   // of 64 bytes, apart in neighbouring rows
+                    *(uint32_t*)(tile + r * BROW + piece + (l32 >> 1) * 4) = packed<Elem>(pair_up(acc[i][c][v], acc[i][c][v + 1], odd));
+                }
             }
-        }
-    __syncthreads();
-    constexpr int RL = BROW / 16;   // lanes of a row
-    const int col_out = col0 + tid % RL * 8;
-    Elem* o = (Elem*)P.dW + ((int64_t)e * P.N + row0) * P.K + col_out;
+        __syncthreads();
+        constexpr int RL = BROW / 16;   // lanes of a row
+        const int col_out = col0 + tid % RL * 8;
+        Elem* o = (Elem*)P.dW + ((int64_t)e * P.N + row0) * P.K + col_out;
 #pragma unroll 4
-    for (int r = tid / RL; r < G::BM; r += G::threads / RL) {
-        const int at = ((tid % RL * 16) ^ ((r & 7) * 64));
-        const i32x4 v = *(const i32x4*)(tile + r * BROW + at);
-        if (row0 + r < P.N && col_out < P.K) __builtin_nontemporal_store(v, (i32x4*)(o + (int64_t)r * P.K));
-    }
+        for (int r = tid / RL; r < G::BM; r += G::threads / RL) {
+            const int at = ((tid % RL * 16) ^ ((r & 7) * 64));
+            const i32x4 v = *(const i32x4*)(tile + r * BROW + at);
+            if (row0 + r < P.N && col_out < P.K) __builtin_nontemporal_store(v, (i32x4*)(o + (int64_t)r * P.K));
+        }
     }
 }
 
